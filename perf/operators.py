@@ -1,0 +1,413 @@
+"""The expert-side operators of a mixture-of-experts step, as measured cases.
+
+dispatch and combine move a token's row to the ranks that own its experts and
+back.  The three operators here are what a decode step computes around them:
+
+* route          -- a router's logits to each token's expert ids and weights
+* expert_linear  -- y[r] = W[id_r] x[r], dense 16-bit or 4-bit weights
+* moe_layer      -- out[t] = sum_j w[t,j] FFN_{id[t,j]}(x[t]), a gated feed-forward
+
+Weights.  Dense: [E, N, K] rows of K elements.  4-bit: W[e,n,k] = (q - 8) *
+scale[e,n,k // g] with q in 0..15, stored in tiles of 16 rows by 128 columns:
+data uint8 [E, ceil(N/16), ceil(K/128), 1024] and scales (of the activations'
+type) [E, ceil(N/16), ceil(K/128) * 128 / g, 16].  In a tile, element (row,
+kk) is in the 32-bit word (q * 16 + row) * 4 + j, where j = kk // 32 and
+q = kk % 32 // 8; element e = kk % 8 of the word is nibble e // 2 + 4 * (e % 2).
+
+`run` computes the plain form in float32 (float64 where selection turns on the
+last bits) unless `own` is set, where it calls the package.
+"""
+
+import math
+
+import torch
+
+own = False
+
+DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+
+
+# --------------------------------------------------------------------------
+# cases
+# --------------------------------------------------------------------------
+
+def _route(name, n, E, k, dtype, score, bias=False, groups=1, top_groups=1, group_top=2, renorm=True, scale=1.0):
+    return dict(name=name, op="route", n=n, E=E, k=k, dtype=dtype, score=score, bias=bias, groups=groups,
+                top_groups=top_groups, group_top=group_top, renorm=renorm, scale=scale)
+
+
+def _linear(name, n, E, N, K, dtype, g, ids, out):
+    return dict(name=name, op="linear", n=n, E=E, N=N, K=K, dtype=dtype, g=g, ids=ids, out=out)
+
+
+def _layer(name, n, E, k, H, I, dtype, g, routed, total=0, offset=0, score="softmax", bias=False, groups=1,
+           top_groups=1, scale=1.0):
+    return dict(name=name, op="layer", n=n, E=E, k=k, H=H, I=I, dtype=dtype, g=g, routed=routed, total=total or E,
+                offset=offset, score=score, bias=bias, groups=groups, top_groups=top_groups, group_top=2,
+                renorm=True, scale=scale)
+
+
+def listed():
+    return [
+        # one token's selection with a balancing bias and group limits: decode, all latency
+        _route("route one token", 1, 256, 8, "f32", "sigmoid", True, 8, 4, 2, True, 2.5),
+        # the 8 ranks x 128 tokens of a DeepSeek-V3-shaped step
+        _route("route a step", 1024, 256, 8, "bf16", "softmax"),
+        # 32 ranks x 256 tokens, 128 experts: the largest step the benchmark has
+        _route("route a large step", 8192, 128, 8, "f32", "softmax", renorm=False),
+        # a 4-bit projection of one token: a shared expert's matrix
+        _linear("linear 4-bit one token", 1, 1, 4096, 7168, "bf16", 128, False, "bf16"),
+        # one expert's matrix for each of 48 rows, 4 bits with small groups, some rows not of this rank
+        _linear("linear 4-bit experts", 48, 32, 4096, 7168, "f16", 32, True, "f16"),
+        # odd sizes: rows that no 16-byte load is aligned with, float32 results
+        _linear("linear odd", 37, 8, 1001, 2050, "bf16", 0, True, "f32"),
+        # a whole layer for one token, 256 experts of 4 bits, routed in the call
+        _layer("layer 4-bit one token", 1, 256, 8, 7168, 2048, "bf16", 128, True, score="sigmoid", bias=True, groups=8,
+               top_groups=4, scale=2.5),
+        # a whole layer for one token, dense weights, routed before
+        _layer("layer one token", 1, 64, 8, 4096, 1024, "bf16", 0, False),
+        # a tiny model's layer: all latency
+        _layer("layer tiny", 5, 8, 2, 128, 64, "f16", 0, True),
+        # a batch of 32 decoding sequences
+        _layer("layer a batch", 32, 64, 8, 4096, 1024, "bf16", 0, True),
+        # odd sizes, small groups
+        _layer("layer odd", 19, 16, 4, 1000, 328, "f16", 32, False),
+        # one rank's 32 experts on the 1024 rows it received of an 8 x 128 token step
+        _layer("layer received rows", 1024, 32, 8, 7168, 2048, "bf16", 128, False, total=256, offset=96),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["route", "linear", "layer", "layer"])
+    if op == "route":
+        E = rng.choice([8, 16, 60, 64, 128, 160, 256, 384])
+        k = rng.randint(1, 8)
+        score = rng.choice(["softmax", "sigmoid"])
+        grouped = rng.random() < 0.4
+        G = rng.choice([g for g in (2, 4, 8) if E % g == 0]) if grouped else 1
+        top = rng.randint(-(-G // 2), G) if grouped else 1
+        return dict(op="route", n=_log(rng, 1, 8192), E=E, k=k, dtype=rng.choice(["f32", "bf16", "f16"]), score=score,
+                    bias=rng.random() < 0.5, groups=G, top_groups=top, group_top=rng.choice([1, 2]),
+                    renorm=rng.random() < 0.7, scale=rng.choice([1.0, 2.5]))
+    g = rng.choice([0, 0, 32, 64, 128])
+    if op == "linear":
+        ids = rng.random() < 0.7
+        E = _log(rng, 2, 64) if ids else 1
+        N, K = _log(rng, 64, 8192), _log(rng, 64, 8192)
+        while E * N * K > 1.0e9:
+            E = max(1, E // 2)
+        dtype = rng.choice(["bf16", "f16"])
+        return dict(op="linear", n=_log(rng, 1, 200), E=E, N=N, K=K, dtype=dtype, g=g, ids=ids,
+                    out=rng.choice([dtype, dtype, "f32"]))
+    E = _log(rng, 4, 64)
+    k = rng.randint(1, min(8, E))
+    H, I = 8 * _log(rng, 16, 900), 8 * _log(rng, 8, 300)
+    while E * H * I * 3 > 1.2e9:
+        H, I = 8 * (H // 16), 8 * max(1, I // 12)
+    n = _log(rng, 1, 256) if rng.random() < 0.8 else _log(rng, 256, 1024)
+    routed = rng.random() < 0.5
+    ranks = 1 if routed else rng.choice([1, 1, 2, 4])
+    return dict(op="layer", n=n, E=E, k=k, H=H, I=I, dtype=rng.choice(["bf16", "f16"]), g=g, routed=routed,
+                total=E * ranks, offset=E * rng.randrange(ranks), score=rng.choice(["softmax", "sigmoid"]),
+                bias=rng.random() < 0.3, groups=1, top_groups=1, group_top=2, renorm=True, scale=1.0)
+
+
+# --------------------------------------------------------------------------
+# inputs
+# --------------------------------------------------------------------------
+
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed * 2654435761 % (1 << 62) + 17)
+    return g
+
+
+def _randn(gen, shape, dtype, std=1.0):
+    return torch.randn(shape, generator=gen, device="cuda", dtype=dtype).mul_(std)
+
+
+def _weights(gen, E, N, K, dtype, g):
+    """(dense [E,N,K], None) or (4-bit data, scales); either way about 1/sqrt(K) in size."""
+    std = 1.0 / math.sqrt(K)
+    if not g:
+        return _randn(gen, (E, N, K), dtype, std), None
+    nt, kb = -(-N // 16), -(-K // 128)
+    data = torch.randint(0, 256, (E, nt, kb, 1024), generator=gen, device="cuda", dtype=torch.uint8)
+    spread = torch.rand((E, nt, kb * 128 // g, 16), generator=gen, device="cuda") + 0.5
+    return data, (spread * (std / 4.6)).to(dtype)
+
+
+def _logits(gen, n, E, dtype):
+    """A router's logits: some experts are more popular than others."""
+    return (_randn(gen, (n, E), torch.float32) + 0.5 * _randn(gen, (E,), torch.float32)).to(dtype)
+
+
+def _bias(gen, E):
+    return _randn(gen, (E,), torch.float32, 0.05)
+
+
+def prepare(case, seed):
+    c, gen = case, _gen(seed)
+    dt = DTYPES[c["dtype"]]
+    s = {"case": c}
+    if c["op"] == "route":
+        s["logits"] = _logits(gen, c["n"], c["E"], dt)
+        s["bias"] = _bias(gen, c["E"]) if c["bias"] else None
+        return s
+    if c["op"] == "linear":
+        s["x"] = _randn(gen, (c["n"], c["K"]), dt)
+        s["w"], s["scales"] = _weights(gen, c["E"], c["N"], c["K"], dt, c["g"])
+        s["ids"] = None
+        if c["ids"]:  # one row in E + 1 belongs to no expert here
+            s["ids"] = torch.randint(-1, c["E"], (c["n"],), generator=gen, device="cuda", dtype=torch.int32)
+        return s
+    s["x"] = _randn(gen, (c["n"], c["H"]), dt)
+    s["gate_up"], s["gate_up_scales"] = _weights(gen, c["E"], 2 * c["I"], c["H"], dt, c["g"])
+    s["down"], s["down_scales"] = _weights(gen, c["E"], c["H"], c["I"], dt, c["g"])
+    s["bias"] = _bias(gen, c["E"]) if c["bias"] else None
+    logits = _logits(gen, c["n"], c["total"], torch.float32)
+    if c["routed"]:
+        s["logits"] = logits
+    else:
+        v, ids = logits.sort(dim=1, descending=True)
+        s["ids"] = ids[:, :c["k"]].to(torch.int32).contiguous()
+        s["weights"] = torch.softmax(v[:, :c["k"]], 1).contiguous()
+        if c["total"] > c["E"]:  # received rows: a row without an expert of this rank is marked invalid
+            mine = ((s["ids"] >= c["offset"]) & (s["ids"] < c["offset"] + c["E"])).any(1, keepdim=True)
+            s["ids"] = torch.where(mine, s["ids"], torch.full_like(s["ids"], -1))
+            s["weights"] = torch.where(mine, s["weights"], torch.zeros_like(s["weights"]))
+    return s
+
+
+# --------------------------------------------------------------------------
+# one pass
+# --------------------------------------------------------------------------
+
+def _plain_route(c, logits, bias):
+    x = logits.double().clamp(max=torch.finfo(torch.float32).max)
+    score = torch.softmax(x, 1) if c["score"] == "softmax" else torch.sigmoid(x)
+    if bias is not None:
+        choice = score + bias.double()
+    elif c["groups"] > 1:
+        choice = score
+    else:
+        choice = x
+    if c["groups"] > 1:
+        n, E, G = x.shape[0], x.shape[1], c["groups"]
+        best = choice.view(n, G, E // G).sort(dim=2, descending=True)[0][:, :, :c["group_top"]].sum(2)
+        order = best.sort(dim=1, descending=True, stable=True)[1][:, :c["top_groups"]]
+        open_groups = torch.zeros_like(best, dtype=torch.bool).scatter_(1, order, True)
+        choice = choice.masked_fill(~open_groups.repeat_interleave(E // G, 1), -math.inf)
+    ids = choice.sort(dim=1, descending=True, stable=True)[1][:, :c["k"]]
+    w = score.gather(1, ids)
+    if c["renorm"]:
+        w = w / w.sum(1, keepdim=True)
+    return ids.to(torch.int32), (w * c["scale"]).float()
+
+
+def _dequantize(data, scales, N, K):
+    """float32 [E, N, K] of 4-bit weights."""
+    E, nt, kb, _ = data.shape
+    d = data.view(E, nt, kb, 4, 16, 4, 4)                           # q, row, j, byte
+    nib = torch.stack((d & 15, d >> 4), -1)                         # nibble = 2 * byte + half
+    nib = nib.view(E, nt, kb, 4, 16, 4, 2, 4)                       # nibble = 4 * odd + pair
+    nib = nib.permute(0, 1, 4, 2, 5, 3, 7, 6)                       # row, block, j, q, pair, odd
+    groups = scales.shape[2]
+    w = nib.reshape(E, nt * 16, groups, kb * 128 // groups).float().sub_(8)
+    w.mul_(scales.float().permute(0, 1, 3, 2).reshape(E, nt * 16, groups, 1))
+    return w.view(E, nt * 16, kb * 128)[:, :N, :K]
+
+
+def _plain_weights(data, scales, N, K, index=None):
+    if index is not None:
+        data = data[index]
+        scales = scales[index] if scales is not None else None
+    return data.float() if scales is None else _dequantize(data, scales, N, K)
+
+
+def _plain_linear(c, s):
+    x, out = s["x"].float(), DTYPES[c["out"]]
+    if s["ids"] is None:
+        return (x @ _plain_weights(s["w"], s["scales"], c["N"], c["K"])[0].t()).to(out)
+    ids = s["ids"].long()
+    inside = (ids >= 0) & (ids < c["E"])
+    e = ids.clamp(0, c["E"] - 1)
+    if c["n"] <= c["E"]:
+        y = torch.bmm(_plain_weights(s["w"], s["scales"], c["N"], c["K"], e), x.unsqueeze(2)).squeeze(2)
+    else:
+        w = _plain_weights(s["w"], s["scales"], c["N"], c["K"]).reshape(c["E"] * c["N"], c["K"])
+        y = (x @ w.t()).view(c["n"], c["E"], c["N"])[torch.arange(c["n"], device=x.device), e]
+    return (y * inside.unsqueeze(1)).to(out)
+
+
+def _plain_layer(c, s):
+    n, E, k, H, I = c["n"], c["E"], c["k"], c["H"], c["I"]
+    ids, w = _plain_route(c, s["logits"], s["bias"]) if c["routed"] else (s["ids"], s["weights"])
+    e = ids.long() - c["offset"]
+    w = torch.where((e >= 0) & (e < E), w, torch.zeros_like(w))
+    e = e.clamp(0, E - 1)
+    x = s["x"].float()
+    if n * k <= E:  # the experts of each (token, slot)
+        pick = e.reshape(-1)
+        xs = x.repeat_interleave(k, 0).unsqueeze(2)
+        gu = torch.bmm(_plain_weights(s["gate_up"], s["gate_up_scales"], 2 * I, H, pick), xs)
+        gate, up = gu[:, :I], gu[:, I:]
+        act = gate * torch.sigmoid(gate) * up
+        y = torch.bmm(_plain_weights(s["down"], s["down_scales"], H, I, pick), act).view(n, k, H)
+        return (y * w.unsqueeze(2)).sum(1).to(s["x"].dtype)
+    # every expert on every token, weighted by zero where it was not chosen
+    share = torch.zeros((n, E), device=x.device).scatter_add_(1, e, w)
+    gu = (x @ _plain_weights(s["gate_up"], s["gate_up_scales"], 2 * I, H).reshape(E * 2 * I, H).t()).view(n, E, 2 * I)
+    gate, up = gu[:, :, :I], gu[:, :, I:]
+    act = gate * torch.sigmoid(gate) * up * share.unsqueeze(2)
+    down = _plain_weights(s["down"], s["down_scales"], H, I).permute(0, 2, 1).reshape(E * I, H)
+    return (act.view(n, E * I) @ down).to(s["x"].dtype)
+
+
+def _router(package, c, bias):
+    return package.Router(top_k=c["k"], score=c["score"], bias=bias, num_groups=c["groups"],
+                          top_groups=c["top_groups"], group_top=c["group_top"], renormalize=c["renorm"],
+                          scale=c["scale"])
+
+
+def _own(c, s):
+    import combine_token_dest_amd as package
+
+    def weight(data, scales, N, K):
+        return data if scales is None else package.W4Weights(data, scales, N, K)
+
+    if c["op"] == "route":
+        ids, w = package.route(s["logits"], _router(package, c, s["bias"]))
+        return {"topk_ids": ids, "topk_weights": w}
+    if c["op"] == "linear":
+        return package.expert_linear(s["x"], weight(s["w"], s["scales"], c["N"], c["K"]), s["ids"],
+                                     out_dtype=DTYPES[c["out"]])
+    gate_up = weight(s["gate_up"], s["gate_up_scales"], 2 * c["I"], c["H"])
+    down = weight(s["down"], s["down_scales"], c["H"], c["I"])
+    if c["routed"]:
+        return package.moe_layer(s["x"], gate_up, down, router_logits=s["logits"], router=_router(package, c, s["bias"]))
+    return package.moe_layer(s["x"], gate_up, down, s["ids"], s["weights"], expert_offset=c["offset"])
+
+
+def run(state):
+    c = state["case"]
+    if own:
+        return _own(c, state)
+    if c["op"] == "route":
+        ids, w = _plain_route(c, state["logits"], state["bias"])
+        return {"topk_ids": ids, "topk_weights": w}
+    return _plain_linear(c, state) if c["op"] == "linear" else _plain_layer(c, state)
+
+
+# --------------------------------------------------------------------------
+# what a pass cannot do without
+# --------------------------------------------------------------------------
+
+def _matrix_bytes(N, K, g):
+    return 2.0 * N * K if not g else N * K / 2.0 + 2.0 * N * K / g
+
+
+def work(case):
+    c = case
+    n, E = c["n"], c["E"]
+    if c["op"] == "route":
+        b = n * E * DTYPES[c["dtype"]].itemsize + 8.0 * n * c["k"] + (4.0 * E if c["bias"] else 0)
+        return {"bytes": b, "flops": 4.0 * n * E}
+    if c["op"] == "linear":
+        rows = n * (E / (E + 1.0)) if c["ids"] else n
+        used = E * (1 - (1 - 1.0 / (E + 1)) ** n) if c["ids"] else 1
+        b = used * _matrix_bytes(c["N"], c["K"], c["g"]) + n * (2.0 * c["K"] + DTYPES[c["out"]].itemsize * c["N"])
+        return {"bytes": b, "flops": 2.0 * rows * c["N"] * c["K"]}
+    used = E * (1 - (1 - c["k"] / float(c["total"])) ** n)
+    pairs = n * c["k"] * E / float(c["total"])
+    b = used * (_matrix_bytes(2 * c["I"], c["H"], c["g"]) + _matrix_bytes(c["H"], c["I"], c["g"]))
+    b += 4.0 * n * c["H"] + (4.0 * n * c["total"] if c["routed"] else 8.0 * n * c["k"])
+    return {"bytes": b, "flops": 6.0 * pairs * c["H"] * c["I"]}
+
+
+# --------------------------------------------------------------------------
+# the definition in 64 bits
+# --------------------------------------------------------------------------
+
+def _exact_select(c, logits, bias):
+    """Ids as lists and weights as float64 [n, k], token by token on the host."""
+    x = logits.double().cpu().numpy()
+    b = bias.double().cpu().numpy() if bias is not None else None
+    n, E = x.shape
+    ids, ws = [], []
+    for t in range(n):
+        row = x[t]
+        if c["score"] == "softmax":
+            top = row.max()
+            p = [math.exp(v - top) for v in row]
+            z = math.fsum(p)
+            p = [v / z for v in p]
+        else:
+            p = [1.0 / (1.0 + math.exp(-v)) if v >= 0 else math.exp(v) / (1.0 + math.exp(v)) for v in row]
+        key = [p[e] + b[e] for e in range(E)] if b is not None else p if c["groups"] > 1 else list(row)
+        allowed = range(E)
+        if c["groups"] > 1:
+            size = E // c["groups"]
+            value = [sum(sorted(key[g * size:(g + 1) * size], reverse=True)[:c["group_top"]])
+                     for g in range(c["groups"])]
+            kept = sorted(range(c["groups"]), key=lambda g: (-value[g], g))[:c["top_groups"]]
+            allowed = [e for g in kept for e in range(g * size, (g + 1) * size)]
+        chosen = sorted(allowed, key=lambda e: (-key[e], e))[:c["k"]]
+        w = [p[e] for e in chosen]
+        z = math.fsum(w) if c["renorm"] else 1.0
+        ids.append(chosen)
+        ws.append([v / z * c["scale"] for v in w])
+    return ids, torch.tensor(ws, dtype=torch.float64)
+
+
+def _exact_matrix(data, scales, e, N, K):
+    """Expert e's [N, K] in float64."""
+    if scales is None:
+        return data[e].double()
+    n = torch.arange(N, device=data.device).unsqueeze(1)
+    k = torch.arange(K, device=data.device).unsqueeze(0)
+    word = (k % 32 // 8 * 16 + n % 16) * 4 + k % 128 // 32
+    nibble = k % 8 // 2 + 4 * (k % 2)
+    tile = (n // 16) * data.shape[2] + k // 128
+    byte = data[e].reshape(-1)[tile * 1024 + word * 4 + nibble // 2].int()
+    q = (byte >> (nibble % 2 * 4)) & 15
+    g = data.shape[2] * 128 // scales.shape[2]
+    return (q - 8).double() * scales[e].double()[n // 16, k // g, n % 16]
+
+
+def exact(case, seed):
+    c = case
+    if c["op"] == "route" and c["n"] * c["E"] > 4e6:
+        return None
+    s = prepare(case, seed)
+    if c["op"] == "route":
+        return {"topk_ids": None, "topk_weights": _exact_select(c, s["logits"], s["bias"])[1]}
+    x = s["x"].double()
+    if c["op"] == "linear":
+        y = torch.zeros((c["n"], c["N"]), dtype=torch.float64, device="cuda")
+        owner = [0] * c["n"] if s["ids"] is None else s["ids"].tolist()
+        for e in sorted(set(owner) & set(range(c["E"]))):
+            rows = torch.tensor([r for r, v in enumerate(owner) if v == e], device="cuda")
+            y[rows] = x[rows] @ _exact_matrix(s["w"], s["scales"], e, c["N"], c["K"]).t()
+        return y
+    if c["routed"]:
+        ids, w = _exact_select(c, s["logits"], s["bias"])
+    else:
+        ids, w = s["ids"].tolist(), s["weights"].double().cpu()
+    out = torch.zeros((c["n"], c["H"]), dtype=torch.float64, device="cuda")
+    for e in range(c["E"]):
+        at = [(t, j) for t in range(c["n"]) for j in range(c["k"]) if ids[t][j] == e + c["offset"]]
+        if not at:
+            continue
+        rows = torch.tensor([t for t, _ in at], device="cuda")
+        share = torch.tensor([float(w[t, j]) for t, j in at], dtype=torch.float64, device="cuda")
+        gu = x[rows] @ _exact_matrix(s["gate_up"], s["gate_up_scales"], e, 2 * c["I"], c["H"]).t()
+        gate, up = gu[:, :c["I"]], gu[:, c["I"]:]
+        act = gate / (1 + torch.exp(-gate)) * up
+        y = act @ _exact_matrix(s["down"], s["down_scales"], e, c["H"], c["I"]).t()
+        out.index_add_(0, rows, y * share.unsqueeze(1))
+    return out
