@@ -12,7 +12,8 @@ scale[e,n,k // g] with q in 0..15, stored in tiles of 16 rows by 128 columns:
 data uint8 [E, ceil(N/16), ceil(K/128), 1024] and scales (of the activations'
 type) [E, ceil(N/16), ceil(K/128) * 128 / g, 16].  In a tile, element (row,
 kk) is in the 32-bit word (q * 16 + row) * 4 + j, where j = kk // 32 and
-q = kk % 32 // 8; element e = kk % 8 of the word is nibble e // 2 + 4 * (e % 2).
+q = kk % 32 // 8; of the word's eight elements (kk % 8), 0 to 3 are the low
+halves of its bytes and 4 to 7 the high halves.
 
 `run` computes the plain form in float32 (float64 where selection turns on the
 last bits) unless `own` is set, where it calls the package.
@@ -90,6 +91,7 @@ def draw(rng):
         grouped = rng.random() < 0.4
         G = rng.choice([g for g in (2, 4, 8) if E % g == 0]) if grouped else 1
         top = rng.randint(-(-G // 2), G) if grouped else 1
+        k = min(k, top * (E // G)) if grouped else k
         return dict(op="route", n=_log(rng, 1, 8192), E=E, k=k, dtype=rng.choice(["f32", "bf16", "f16"]), score=score,
                     bias=rng.random() < 0.5, groups=G, top_groups=top, group_top=rng.choice([1, 2]),
                     renorm=rng.random() < 0.7, scale=rng.choice([1.0, 2.5]))
@@ -213,9 +215,8 @@ def _dequantize(data, scales, N, K):
     """float32 [E, N, K] of 4-bit weights."""
     E, nt, kb, _ = data.shape
     d = data.view(E, nt, kb, 4, 16, 4, 4)                           # q, row, j, byte
-    nib = torch.stack((d & 15, d >> 4), -1)                         # nibble = 2 * byte + half
-    nib = nib.view(E, nt, kb, 4, 16, 4, 2, 4)                       # nibble = 4 * odd + pair
-    nib = nib.permute(0, 1, 4, 2, 5, 3, 7, 6)                       # row, block, j, q, pair, odd
+    nib = torch.stack((d & 15, d >> 4), -2)                         # q, row, j, half, byte
+    nib = nib.permute(0, 1, 4, 2, 5, 3, 6, 7)                       # row, block, j, q, half, byte
     groups = scales.shape[2]
     w = nib.reshape(E, nt * 16, groups, kb * 128 // groups).float().sub_(8)
     w.mul_(scales.float().permute(0, 1, 3, 2).reshape(E, nt * 16, groups, 1))
@@ -371,10 +372,9 @@ def _exact_matrix(data, scales, e, N, K):
     n = torch.arange(N, device=data.device).unsqueeze(1)
     k = torch.arange(K, device=data.device).unsqueeze(0)
     word = (k % 32 // 8 * 16 + n % 16) * 4 + k % 128 // 32
-    nibble = k % 8 // 2 + 4 * (k % 2)
     tile = (n // 16) * data.shape[2] + k // 128
-    byte = data[e].reshape(-1)[tile * 1024 + word * 4 + nibble // 2].int()
-    q = (byte >> (nibble % 2 * 4)) & 15
+    byte = data[e].reshape(-1)[tile * 1024 + word * 4 + k % 4].int()
+    q = (byte >> (k % 8 // 4 * 4)) & 15
     g = data.shape[2] * 128 // scales.shape[2]
     return (q - 8).double() * scales[e].double()[n // 16, k // g, n % 16]
 
