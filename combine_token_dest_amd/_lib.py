@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import (POINTER, Structure, c_char_p, c_int, c_int32, c_int64, c_size_t, c_uint64,
+from ctypes import (POINTER, Structure, c_char_p, c_float, c_int, c_int32, c_int64, c_size_t, c_uint64,
                     c_void_p, byref)
 from typing import List, Optional, Sequence
 
@@ -39,10 +39,17 @@ EXPORTS = [
     "moe_ep_is_platform_supported", "moe_ep_workspace_bytes", "moe_ep_create", "moe_ep_dispatch",
     "moe_ep_get_combine_input_buffer", "moe_ep_combine", "moe_ep_destroy",
     "moe_ep_create_vmm", "moe_ep_workspace", "moe_ep_checkpoint_prepare", "moe_ep_checkpoint_restore",
-    "moe_ep_dispatch_noalloc", "moe_ep_active_rank_mask", "moe_ep_status_string", "moe_ep_last_error",
+    "moe_ep_dispatch_noalloc", "moe_ep_active_rank_mask", "moe_ep_route", "moe_ep_expert_linear",
+    "moe_ep_layer_workspace_bytes", "moe_ep_layer", "moe_ep_status_string", "moe_ep_last_error",
 ]
 
 MOE_EP_NOALLOC_MAX_ROWS = 65536
+
+MOE_EP_MAX_EXPERTS = 1024
+MOE_EP_MAX_TOPK = 64
+
+MOE_EP_SCORE_SOFTMAX = 0
+MOE_EP_SCORE_SIGMOID = 1
 
 R = MOE_EP_MAX_RANKS
 
@@ -81,6 +88,38 @@ class moe_ep_combine_args(Structure):
     _fields_ = [
         ("expert_output", c_void_p * R), ("output", c_void_p * R), ("dtype", c_int32),
         ("active_rank_mask", c_uint64),
+    ]
+
+
+class moe_ep_router(Structure):
+    _fields_ = [
+        ("num_experts", c_int32), ("top_k", c_int32), ("score", c_int32), ("num_groups", c_int32),
+        ("top_groups", c_int32), ("group_top", c_int32), ("renormalize", c_int32),
+        ("invalid_expert_id", c_int32), ("scale", c_float), ("bias", c_void_p),
+    ]
+
+
+class moe_ep_weight(Structure):
+    _fields_ = [("data", c_void_p), ("scales", c_void_p), ("group_size", c_int32)]
+
+
+class moe_ep_linear_args(Structure):
+    _fields_ = [
+        ("x", c_void_p), ("x_stride", c_int64), ("expert_ids", c_void_p), ("out", c_void_p),
+        ("out_stride", c_int64), ("weight", moe_ep_weight), ("dtype", c_int32), ("out_dtype", c_int32),
+        ("num_rows", c_int32), ("num_experts", c_int32), ("expert_offset", c_int32),
+        ("in_features", c_int32), ("out_features", c_int32),
+    ]
+
+
+class moe_ep_layer_args(Structure):
+    _fields_ = [
+        ("hidden", c_void_p), ("hidden_stride", c_int64), ("topk_ids", c_void_p), ("topk_weights", c_void_p),
+        ("router", POINTER(moe_ep_router)), ("router_logits", c_void_p), ("logits_stride", c_int64),
+        ("out", c_void_p), ("out_stride", c_int64), ("gate_up", moe_ep_weight), ("down", moe_ep_weight),
+        ("workspace", c_void_p), ("workspace_bytes", c_size_t), ("dtype", c_int32), ("out_dtype", c_int32),
+        ("logits_dtype", c_int32), ("num_tokens", c_int32), ("top_k", c_int32), ("num_experts", c_int32),
+        ("expert_offset", c_int32), ("hidden_size", c_int32), ("intermediate_size", c_int32),
     ]
 
 
@@ -133,6 +172,15 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.moe_ep_dispatch_noalloc.restype = c_int
     lib.moe_ep_active_rank_mask.argtypes = [POINTER(c_int32), c_int32, POINTER(c_uint64)]
     lib.moe_ep_active_rank_mask.restype = c_int
+    lib.moe_ep_route.argtypes = [POINTER(moe_ep_router), c_void_p, c_int32, c_int64, c_int32, c_void_p,
+                                 c_void_p, c_void_p]
+    lib.moe_ep_route.restype = c_int
+    lib.moe_ep_expert_linear.argtypes = [POINTER(moe_ep_linear_args), c_void_p]
+    lib.moe_ep_expert_linear.restype = c_int
+    lib.moe_ep_layer_workspace_bytes.argtypes = [POINTER(moe_ep_layer_args), POINTER(c_size_t)]
+    lib.moe_ep_layer_workspace_bytes.restype = c_int
+    lib.moe_ep_layer.argtypes = [POINTER(moe_ep_layer_args), c_void_p]
+    lib.moe_ep_layer.restype = c_int
     lib.moe_ep_status_string.argtypes = [c_int]
     lib.moe_ep_status_string.restype = c_char_p
     lib.moe_ep_last_error.argtypes = []
@@ -229,3 +277,23 @@ def moe_ep_active_rank_mask(ranks: Sequence[int]) -> int:
     out = c_uint64(0)
     _check(load().moe_ep_active_rank_mask(arr, len(ranks), byref(out)), "moe_ep_active_rank_mask")
     return out.value
+
+
+def moe_ep_route(router: moe_ep_router, logits: int, logits_dtype: int, logits_stride: int, num_tokens: int,
+                 topk_ids: int, topk_weights: int, stream: int) -> None:
+    _check(load().moe_ep_route(byref(router), logits, logits_dtype, logits_stride, num_tokens, topk_ids,
+                               topk_weights, stream), "moe_ep_route")
+
+
+def moe_ep_expert_linear(args: moe_ep_linear_args, stream: int) -> None:
+    _check(load().moe_ep_expert_linear(byref(args), stream), "moe_ep_expert_linear")
+
+
+def moe_ep_layer_workspace_bytes(args: moe_ep_layer_args) -> int:
+    out = c_size_t(0)
+    _check(load().moe_ep_layer_workspace_bytes(byref(args), byref(out)), "moe_ep_layer_workspace_bytes")
+    return out.value
+
+
+def moe_ep_layer(args: moe_ep_layer_args, stream: int) -> None:
+    _check(load().moe_ep_layer(byref(args), stream), "moe_ep_layer")

@@ -12,6 +12,7 @@ import shutil
 import subprocess
 import sys
 import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -46,16 +47,24 @@ def build(verbose: bool = False) -> str:
         k_obj = os.path.join(tmp, "moe_ep_kernels.o")
         a_obj = os.path.join(tmp, "moe_ep_api.o")
         p_obj = os.path.join(tmp, "moe_ep_plan.o")
+        xk_obj = os.path.join(tmp, "moe_experts_kernels.o")
+        xa_obj = os.path.join(tmp, "moe_experts_api.o")
         lib_tmp = os.path.join(tmp, LIB_NAME)
-        steps = [
+        compile_steps = [
+            [HIPCC, f"--offload-arch={ARCH}", *COMMON, *DEVICE_FLAGS, "-x", "hip", "-c",
+             os.path.join(CSRC, "moe_experts_kernels.hip"), "-o", xk_obj],
             [HIPCC, f"--offload-arch={ARCH}", *COMMON, *DEVICE_FLAGS, "-x", "hip", "-c",
              os.path.join(CSRC, "moe_ep_kernels.hip"), "-o", k_obj],
             [HIPCC, *COMMON, "-c", os.path.join(CSRC, "moe_ep_api.cpp"), "-o", a_obj],
             [HIPCC, *COMMON, "-c", os.path.join(CSRC, "moe_ep_plan.cpp"), "-o", p_obj],
-            [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", k_obj, a_obj, p_obj, "-o", lib_tmp],
+            [HIPCC, *COMMON, "-c", os.path.join(CSRC, "moe_experts_api.cpp"), "-o", xa_obj],
         ]
-        for cmd in steps:
-            out = _run(cmd)
+        link = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", k_obj, a_obj, p_obj, xk_obj, xa_obj,
+                "-o", lib_tmp]
+        with ThreadPoolExecutor(max_workers=len(compile_steps)) as pool:
+            outs = list(pool.map(_run, compile_steps))
+        outs.append(_run(link))
+        for out in outs:
             if verbose and out.strip():
                 print(out)
         shutil.move(lib_tmp, LIB_PATH + ".tmp")

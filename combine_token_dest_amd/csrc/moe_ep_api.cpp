@@ -39,6 +39,24 @@ int ok() {
   return MOE_EP_OK;
 }
 
+}  // namespace
+
+// The message of a call that failed in another file of the library.
+namespace moe_ep_detail {
+int report(int status, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+int report(int status, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  g_last_error = buf;
+  return status;
+}
+}  // namespace moe_ep_detail
+
+namespace {
+
 constexpr int64_t kAlign = 256;
 
 int64_t align_up(int64_t x, int64_t a) {

@@ -1,0 +1,111 @@
+// Internal interface between the host code of the expert-side operators
+// (moe_experts_api.cpp) and their gfx950 kernels (moe_experts_kernels.hip):
+// the router's selection, the experts' linear product and the whole layer.
+// Not installed, not part of the ABI.
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+#include <stdint.h>
+
+#include "moe_ep.h"
+
+namespace moe_ep_detail {
+
+// Records a failed call's message for moe_ep_last_error() and returns status
+// (moe_ep_api.cpp).
+int report(int status, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+
+// Tokens of one pass over the experts' weights: a workgroup keeps an
+// expert's list of tokens in LDS (8 KiB).  Longer calls run several passes.
+constexpr int kPassTokens = 2048;
+// Tokens whose output tile one workgroup of the down product sums in LDS:
+// 64 bytes a token and wave, 64 KiB at eight waves.
+constexpr int kChunkTokens = 128;
+constexpr int kMaxChunks = kPassTokens / kChunkTokens;
+// Waves of a workgroup of the expert kernels; they share the sum over k.
+constexpr int kExpertWaves = 8;
+
+struct RouteKArgs {
+  const void* logits;
+  int64_t logits_stride;      // elements
+  const float* bias;          // [num_experts] or NULL
+  int32_t* ids;               // [n, top_k]
+  float* weights;             // [n, top_k]
+  int32_t n;
+  int32_t num_experts;
+  int32_t top_k;
+  int32_t logits_dtype;
+  int32_t score;
+  int32_t num_groups;
+  int32_t top_groups;
+  int32_t group_top;
+  int32_t renormalize;
+  int32_t invalid_id;
+  float scale;
+};
+
+// One expert matrix [N, K] per expert.
+struct WeightK {
+  const uint8_t* data;
+  const uint16_t* scales;     // 4-bit weights only
+  int64_t expert_bytes;       // of data, per expert
+  int64_t expert_scales;      // scale elements per expert
+  int32_t rows;               // N
+  int32_t cols;               // K
+  int32_t kblocks;            // 4-bit: tiles of 128 columns per row
+  int32_t groups;             // 4-bit: scale groups per row (kblocks * 128 / group size)
+};
+
+// What the layer's first kernel leaves in the workspace for its second.
+// Slot a is one expert that may have tokens (a pair's or an expert's index).
+struct PlanK {
+  int32_t* expert;            // [slots]
+  int32_t* off;               // [slots, kMaxChunks + 1]: where chunk c's tokens start in the slot's list
+  int32_t* pair;              // [slots, n]: token << 6 | top-k slot, tokens ascending
+  float* weight;              // [slots, n]: the pair's weight
+  uint16_t* act;              // [2, n * top_k, act_stride]: activations, high and low part
+  int64_t act_plane;          // elements from a high part to its low part
+  int32_t act_stride;
+  int32_t slots;
+};
+
+// The product whose rows are gathered by expert: expert_linear, and the
+// layer's gate and up product.
+struct RowsKArgs {
+  const uint16_t* x;
+  int64_t x_stride;
+  const int32_t* ids;         // [n, top_k], or NULL: every row is expert 0's
+  const float* topk_weights;  // [n, top_k] or NULL (layer only)
+  WeightK w;
+  PlanK plan;                 // layer only
+  void* out;                  // linear only
+  int64_t out_stride;
+  int32_t out_f32;
+  int32_t n;
+  int32_t top_k;
+  int32_t offset;             // first expert id
+  int32_t num_experts;
+  int32_t by_pair;            // slots are (token, k) pairs, else experts
+  int32_t inter;              // layer: intermediate size; linear: out features
+};
+
+// The layer's down product, summed over the experts of each token.
+struct DownKArgs {
+  WeightK w;
+  PlanK plan;
+  void* out;
+  int64_t out_stride;
+  int32_t out_f32;
+  int32_t n;
+  int32_t top_k;
+  int32_t tiles;              // of 16 output columns
+  int32_t chunks;
+};
+
+hipError_t launch_route(const RouteKArgs& a, hipStream_t stream);
+// dtype: MOE_EP_BF16 or MOE_EP_F16; group: 0 for dense weights, else 32, 64 or 128.
+hipError_t launch_expert_linear(const RowsKArgs& a, int dtype, int group, hipStream_t stream);
+hipError_t launch_gate_up(const RowsKArgs& a, int dtype, int group, hipStream_t stream);
+hipError_t launch_down(const DownKArgs& a, int dtype, int group, hipStream_t stream);
+
+}  // namespace moe_ep_detail

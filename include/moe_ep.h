@@ -302,6 +302,165 @@ MOE_EP_API int moe_ep_dispatch_noalloc(moe_ep_handle handle, const moe_ep_dispat
  * range. */
 MOE_EP_API int moe_ep_active_rank_mask(const int32_t* ranks, int32_t n, uint64_t* out_mask);
 
+/* ------------------------------------------------------------------------
+ * Expert-side operators: what a decode step computes around dispatch and
+ * combine.  A router's logits become the topk_ids and topk_weights that
+ * dispatch takes (moe_ep_route); the experts' matrices are applied to the
+ * rows of their tokens (moe_ep_expert_linear, one matrix; moe_ep_layer, the
+ * whole gated feed-forward summed over a token's experts).  They need no
+ * handle.  Activations and dense weights are MOE_EP_BF16 or MOE_EP_F16,
+ * sums float32, and a result is rounded once.  Results do not depend on
+ * timing: the same inputs give the same bits.
+ *
+ * The stream must belong to the current HIP device (ERR_INVALID_ARG
+ * otherwise), and so must every device pointer.  Pointers to 16-bit
+ * elements, to int32 and to float must be aligned to their element
+ * (ERR_ALIGN otherwise); 4-bit weights and their scales to 16 bytes.  Row
+ * strides are in elements.
+ * ------------------------------------------------------------------------ */
+
+/* Most experts of a router, a linear product or a layer. */
+#define MOE_EP_MAX_EXPERTS 1024
+/* Most experts per token of a router or a layer. */
+#define MOE_EP_MAX_TOPK 64
+
+typedef enum moe_ep_score {
+  MOE_EP_SCORE_SOFTMAX = 0,       /* softmax over the experts */
+  MOE_EP_SCORE_SIGMOID = 1        /* each expert's own sigmoid */
+} moe_ep_score;
+
+/* How a token's logits l[0 .. num_experts) choose its top_k experts.
+ *
+ *   score   s = softmax(l) or sigmoid(l)
+ *   choice  c = s + bias with a bias, else s (without bias and groups c = l,
+ *           which has the same order and no ties from rounding)
+ *   groups  with num_groups > 1 the experts form num_groups equal blocks; a
+ *           group counts the sum of its group_top best open choices, and
+ *           only the top_groups best groups stay open
+ *   ids     the top_k best open choices, best first
+ *   weights s[ids], divided by their sum when renormalize is set, times scale
+ *
+ * Equal choices and equal groups go to the lower index.  Choices are
+ * compared in float64.  An expert whose logit or bias is -inf or NaN is
+ * closed: it has no share in the softmax and is never chosen.  A logit of
+ * +inf counts as the largest float32.  Slots that no open expert is left
+ * for get invalid_expert_id and weight 0; so does every weight of a token
+ * whose chosen scores sum to 0 under renormalize. */
+typedef struct moe_ep_router {
+  int32_t num_experts;            /* 1..MOE_EP_MAX_EXPERTS */
+  int32_t top_k;                  /* 1..min(num_experts, MOE_EP_MAX_TOPK) */
+  int32_t score;                  /* moe_ep_score */
+  int32_t num_groups;             /* divides num_experts; 1 = no groups */
+  int32_t top_groups;             /* 1..num_groups, holding at least top_k experts */
+  int32_t group_top;              /* 1 or 2 */
+  int32_t renormalize;
+  int32_t invalid_expert_id;
+  float scale;
+  const float* bias;              /* device [num_experts], or NULL */
+} moe_ep_router;
+
+/* Chooses the experts of num_tokens tokens: logits device [num_tokens,
+ * num_experts] of logits_dtype (any moe_ep_dtype), rows logits_stride apart;
+ * topk_ids device int32 and topk_weights device float, both [num_tokens,
+ * top_k], as moe_ep_dispatch takes them.  One kernel launch. */
+MOE_EP_API int moe_ep_route(const moe_ep_router* router, const void* logits, int32_t logits_dtype,
+                            int64_t logits_stride, int32_t num_tokens, int32_t* topk_ids,
+                            float* topk_weights, void* stream);
+
+/* The matrices [N, K] of a set of experts.
+ *
+ * group_size 0: dense, data is [experts, N, K] of the activations' type and
+ * scales is ignored.
+ *
+ * group_size g = 32, 64 or 128: 4-bit integers q in 0..15 with
+ *   W[n][k] = (q - 8) * scale[n][k / g]
+ * in tiles of 16 rows by 128 columns, 1024 bytes each:
+ *   data    uint8 [experts, ceil(N/16), ceil(K/128), 1024]
+ *   scales  of the activations' type [experts, ceil(N/16),
+ *           ceil(K/128) * 128 / g, 16], a tile's 16 rows side by side
+ * In a tile, row r's columns c = 32 j + 8 i + e (j, i < 4, e < 8) are in the
+ * 4 bytes at (16 i + r) * 16 + 4 j: byte e of them holds column e < 4 in its
+ * low half and column e + 4 in its high half.  Rows past N and columns past
+ * K are padding of any value.  A token whose activations hold an infinity
+ * gets NaN from 4-bit weights. */
+typedef struct moe_ep_weight {
+  const void* data;
+  const void* scales;
+  int32_t group_size;
+} moe_ep_weight;
+
+typedef struct moe_ep_linear_args {
+  const void* x;                  /* device [num_rows, in_features] of dtype */
+  int64_t x_stride;               /* >= 0; 0 repeats one row */
+  const int32_t* expert_ids;      /* device [num_rows], or NULL: every row is expert 0's */
+  void* out;                      /* device [num_rows, out_features] of out_dtype; must not overlap x */
+  int64_t out_stride;             /* >= out_features */
+  moe_ep_weight weight;           /* N = out_features, K = in_features */
+  int32_t dtype;                  /* MOE_EP_BF16 or MOE_EP_F16 */
+  int32_t out_dtype;              /* dtype, or MOE_EP_F32 */
+  int32_t num_rows;
+  int32_t num_experts;            /* 1..MOE_EP_MAX_EXPERTS */
+  int32_t expert_offset;          /* expert_ids of the first expert, >= 0 */
+  int32_t in_features;
+  int32_t out_features;
+} moe_ep_linear_args;
+
+/* out[r] = W[expert_ids[r] - expert_offset] x[r].  Rows whose id is outside
+ * [expert_offset, expert_offset + num_experts) get zeros.  Made for the few
+ * rows of a decode step: the weights of each used expert are read once per
+ * 2048 rows.  One kernel launch per 2048 rows. */
+MOE_EP_API int moe_ep_expert_linear(const moe_ep_linear_args* args, void* stream);
+
+typedef struct moe_ep_layer_args {
+  const void* hidden;             /* device [num_tokens, hidden_size] of dtype */
+  int64_t hidden_stride;          /* >= 0; 0 repeats one row */
+  const int32_t* topk_ids;        /* device [num_tokens, top_k]; NULL with router */
+  const float* topk_weights;      /* device [num_tokens, top_k], or NULL: all 1 */
+  const moe_ep_router* router;    /* host; chooses ids and weights from router_logits, or NULL */
+  const void* router_logits;      /* device [num_tokens, router->num_experts], with router */
+  int64_t logits_stride;
+  void* out;                      /* device [num_tokens, hidden_size] of out_dtype */
+  int64_t out_stride;             /* >= hidden_size */
+  moe_ep_weight gate_up;          /* N = 2 * intermediate_size (gate rows, then up rows), K = hidden_size */
+  moe_ep_weight down;             /* N = hidden_size, K = intermediate_size */
+  void* workspace;                /* device, moe_ep_layer_workspace_bytes() bytes, 256-byte aligned */
+  size_t workspace_bytes;
+  int32_t dtype;                  /* MOE_EP_BF16 or MOE_EP_F16 */
+  int32_t out_dtype;              /* dtype, or MOE_EP_F32 */
+  int32_t logits_dtype;           /* any moe_ep_dtype */
+  int32_t num_tokens;
+  int32_t top_k;                  /* 1..MOE_EP_MAX_TOPK; the router's with router */
+  int32_t num_experts;            /* experts whose weights are here, 1..MOE_EP_MAX_EXPERTS */
+  int32_t expert_offset;          /* id of the first of them, >= 0 */
+  int32_t hidden_size;
+  int32_t intermediate_size;
+} moe_ep_layer_args;
+
+/* Bytes of device workspace moe_ep_layer needs for these sizes (num_tokens,
+ * top_k, num_experts, intermediate_size and whether a router is set are
+ * read; pointers are not followed). */
+MOE_EP_API int moe_ep_layer_workspace_bytes(const moe_ep_layer_args* args, size_t* out_bytes);
+
+/* The experts of a mixture-of-experts layer, whole:
+ *   out[t] = sum_j topk_weights[t][j] * down_e( silu(gate_e hidden[t]) * (up_e hidden[t]) ),
+ *   e = topk_ids[t][j] - expert_offset,
+ * over the slots j whose e is in [0, num_experts); a token with none gets
+ * zeros.  An expert named twice by a token counts with both weights.  With
+ * all experts here this is a whole layer; with one rank's experts on the
+ * rows dispatch left that rank it is the expert computation between
+ * dispatch and combine, and out may be the rank's combine input buffer.
+ *
+ * Made for few tokens: each used expert's weights are read once per 2048
+ * tokens (the down weights once per 128).  Two kernel launches per 2048
+ * tokens, and a third for the router's choice.  out may be hidden itself
+ * (same address, stride and type) but not overlap it otherwise.  The
+ * workspace holds nothing between calls; calls that may overlap in time
+ * (other streams, graphs replayed side by side) need one each.
+ *
+ * Between the products an activation keeps 16 significant bits (bfloat16)
+ * or 22 (float16, where it saturates at 131008). */
+MOE_EP_API int moe_ep_layer(const moe_ep_layer_args* args, void* stream);
+
 /* Static text for a status code. */
 MOE_EP_API const char* moe_ep_status_string(int status);
 
