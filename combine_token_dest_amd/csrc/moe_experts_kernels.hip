@@ -379,13 +379,16 @@ template <bool W4> struct Step;
 template <> struct Step<false> { static constexpr int kCols = 64, kMac = 2; };
 template <> struct Step<true> { static constexpr int kCols = 128, kMac = 4; };
 
-// Where a lane finds its part of 16 weight rows that start at row `first`.
+// Where a wave finds 16 weight rows that start at row `first`: bases that are
+// the same for all lanes (kept in scalar registers) and each lane's 32-bit
+// offset from them.
 template <bool W4>
 struct RowPtr {
-  const uint8_t* a;           // the lane's A row, at its k offset
-  const uint16_t* sc;         // 4-bit: scale of the lane's first accumulator row, group 0
-  int row0;                   // 4-bit: that row
-  int last;                   // 4-bit: the last row
+  const uint8_t* a;           // A rows
+  uint32_t a_off;             // bytes: the lane's row and k offset
+  const uint16_t* sc;         // 4-bit: scales of the tile, group 0
+  uint32_t sc_off, sc_off2;   // bytes: the four rows with the lane's first accumulator row, and the next four
+  int sc_shift;               // bits from the first of those four rows to the lane's, the same for all lanes
 };
 
 template <bool W4>
@@ -393,136 +396,164 @@ __device__ __forceinline__ RowPtr<W4> row_ptr(const WeightK& w, int expert, int 
   const int lane = threadIdx.x & 63;
   const int q = lane >> 4;
   RowPtr<W4> r;
-  const int row = min(first + (lane & 15), w.rows - 1);
+  const int row = min(first + (lane & 15), w.rows - 1);   // rows past the last repeat it
   const uint8_t* base = w.data + (int64_t)expert * w.expert_bytes;
   if constexpr (W4) {
-    r.a = base + ((int64_t)(row >> 4) * w.kblocks * 64 + q * 16 + (row & 15)) * 16;
-    r.last = w.rows - 1;
-    r.row0 = min(first + 4 * q, w.rows - 1);
-    r.sc = w.scales + (int64_t)expert * w.expert_scales;
+    const int tile = first >> 4;
+    r.a = base + (int64_t)tile * w.kblocks * 1024;
+    r.a_off = (uint32_t)((row >> 4) - tile) * w.kblocks * 1024 + (q * 16 + (row & 15)) * 16;
+    r.sc = w.scales + (int64_t)expert * w.expert_scales + (int64_t)tile * w.groups * 16;
+    const int quad = (first + 4 * q) & ~3, last = (w.rows - 1) & ~3;
+    const int r1 = min(quad, last), r2 = min(quad + 4, last);
+    r.sc_off = ((uint32_t)((r1 >> 4) - tile) * w.groups * 16 + (r1 & 15)) * 2;
+    r.sc_off2 = ((uint32_t)((r2 >> 4) - tile) * w.groups * 16 + (r2 & 15)) * 2;
+    r.sc_shift = (first & 3) * 16;
   } else {
-    r.a = base + ((int64_t)row * w.cols + q * 8) * 2;
+    r.a = base + (int64_t)first * w.cols * 2;
+    r.a_off = ((uint32_t)(row - first) * w.cols + q * 8) * 2;
+    r.sc = nullptr;
+    r.sc_off = r.sc_off2 = 0;
+    r.sc_shift = 0;
   }
   return r;
 }
 
-template <class T, bool W4, int GJ, int TL, int P, bool B>
+// The scales of the lane's four accumulator rows for one group: one 8-byte
+// load, or (SHIFT) two and a shift where the up rows do not start on a
+// multiple of four.  SHIFT waits for its loads on the spot.
+template <bool SHIFT>
+__device__ __forceinline__ u32x2 load_scales(const uint16_t* base, uint32_t off, uint32_t off2, int shift, int group) {
+  const uint8_t* p = reinterpret_cast<const uint8_t*>(base + (int64_t)group * 16);
+  const u32x2 v = *reinterpret_cast<const u32x2*>(p + off);
+  if constexpr (!SHIFT) {
+    return v;
+  } else {
+    const uint64_t next = *reinterpret_cast<const uint64_t*>(p + off2);
+    return __builtin_bit_cast(u32x2, __builtin_bit_cast(uint64_t, v) >> shift |
+                                         (shift ? next << (64 - shift) : 0));
+  }
+}
+
+template <class T>
+__device__ __forceinline__ f32x4 scale_floats(const u32x2& v) {
+  return f32x4{T::to_float((uint16_t)v[0]), T::to_float((uint16_t)(v[0] >> 16)), T::to_float((uint16_t)v[1]),
+               T::to_float((uint16_t)(v[1] >> 16))};
+}
+
+// Eight 4-bit weights as 0..15 of the 16-bit type: the low halves of the
+// word's bytes are elements 0-3, the high halves 4-7.
+template <class T>
+__device__ __forceinline__ u32x4 decode(uint32_t w) {
+  const uint32_t lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;
+  return u32x4{T::template nibbles<false>(lo), T::template nibbles<true>(lo), T::template nibbles<false>(hi),
+               T::template nibbles<true>(hi)};
+}
+
+// What one step loads of the weights, two steps ahead of its use.
+template <bool W4, int GJ, int TL>
 struct Stage {
-  static constexpr int kA = W4 ? 1 : 2;
   static constexpr int kG = W4 ? 4 / GJ : 1;
-  u32x4 a[TL][kA];
-  f32x4 sc[W4 ? TL : 1][kG];
-  u32x4 b[B ? P : 1][B ? Step<W4>::kMac : 1];
+  u32x4 a[TL][W4 ? 1 : 2];
+  u32x2 sc[W4 ? TL : 1][kG];
 };
 
 // acc[tl][ct] += A(16 rows of tile tl, step columns) * B(columns of ct), over
 // the steps s0, s0 + ds, ... below s1.  P planes of B (high, low part) are
-// `plane` elements apart.  kend / bend: columns of A's and B's rows.
-template <class T, bool W4, int GJ, int TL, int CT, int P>
+// `plane` elements apart.  bend: columns of B's rows.
+template <class T, bool W4, bool SHIFT, int GJ, int TL, int CT, int P>
 __device__ __forceinline__ void mac(f32x4 (&acc)[TL][CT], const WeightK& w, const RowPtr<W4> (&ap)[TL],
                                     const uint16_t* const (&bp)[CT], int64_t plane, int bend, int s0, int s1,
                                     int ds) {
   constexpr int kCols = Step<W4>::kCols, kMac = Step<W4>::kMac;
   constexpr bool kStageB = CT == 1;
-  constexpr int kDepth = 2;
-  typedef Stage<T, W4, GJ, TL, P, kStageB> St;
-  const int q8 = ((threadIdx.x & 63) >> 4) * 8;
+  constexpr int kDepth = W4 && GJ == 1 ? 2 : TL == 1 ? 4 : 2;
+  typedef Stage<W4, GJ, TL> St;
+  // B comes from L2: one step ahead for one column tile, at its use for more
+  // (there are no registers for it).
+  u32x4 bs[kStageB ? P : 1][kStageB ? kMac : 1];
+  const u32x4 minus8 = {T::kMinus8, T::kMinus8, T::kMinus8, T::kMinus8};
+  // Bases stay in scalar registers and offsets in one vector register each:
+  // left alone, the compiler keeps a 64-bit vector address per load across
+  // the caller's loop.
+  const uint8_t* abase[TL];
+  const uint16_t* scbase[TL];
+  uint32_t aoff[TL], scoff[TL];
+#pragma unroll
+  for (int t = 0; t < TL; ++t) {
+    abase[t] = ap[t].a;
+    scbase[t] = ap[t].sc;
+    aoff[t] = ap[t].a_off;
+    scoff[t] = ap[t].sc_off;
+    asm volatile("" : "+s"(abase[t]), "+v"(aoff[t]));
+    if constexpr (W4) asm volatile("" : "+s"(scbase[t]), "+v"(scoff[t]));
+  }
   const int kend = w.cols;
   // Steps with no column past an end of either row; at most one step follows.
   const int full = (W4 ? bend : (kend < bend ? kend : bend)) / kCols;
 
-  auto load_b = [&](auto tail, int ct, int pl, int j, int s) -> u32x4 {
-    const uint16_t* p = bp[ct] + pl * plane + (int64_t)s * kCols + 32 * j;
-    if constexpr (!decltype(tail)::value) return load8(p);
-    else return load8_guarded(p, s * kCols + 32 * j + q8, bend);
+  auto load_b = [&](int ct, int pl, int j, int s) -> u32x4 {
+    return load8(bp[ct] + pl * plane + (int64_t)s * kCols + 32 * j);
   };
-  auto load = [&](auto tail, St& st, int s) {
-    constexpr bool kTail = decltype(tail)::value;
+  auto load = [&](St& st, int s) {
 #pragma unroll
     for (int t = 0; t < TL; ++t) {
       if constexpr (W4) {
-        st.a[t][0] = *reinterpret_cast<const u32x4*>(ap[t].a + (int64_t)s * 1024);
-        const int row0 = ap[t].row0;
+        st.a[t][0] = *reinterpret_cast<const u32x4*>(abase[t] + (int64_t)s * 1024 + aoff[t]);
 #pragma unroll
-        for (int g = 0; g < St::kG; ++g) {
-          const int64_t grp = (int64_t)s * St::kG + g;
-          if ((row0 & 3) == 0) {
-            const u32x2 v = *reinterpret_cast<const u32x2*>(
-                ap[t].sc + ((int64_t)(row0 >> 4) * w.groups + grp) * 16 + (row0 & 15));
-            st.sc[t][g] = f32x4{T::to_float((uint16_t)v[0]), T::to_float((uint16_t)(v[0] >> 16)),
-                                T::to_float((uint16_t)v[1]), T::to_float((uint16_t)(v[1] >> 16))};
-          } else {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const int row = min(row0 + r, ap[t].last);
-              st.sc[t][g][r] = T::to_float(ap[t].sc[((int64_t)(row >> 4) * w.groups + grp) * 16 + (row & 15)]);
-            }
-          }
-          if constexpr (kTail) {        // groups past the last column: whatever the padding holds
-            if (grp * 32 * GJ >= kend) st.sc[t][g] = f32x4{0, 0, 0, 0};
-          }
-        }
+        for (int g = 0; g < St::kG; ++g) st.sc[t][g] = load_scales<SHIFT>(scbase[t], scoff[t], ap[t].sc_off2, ap[t].sc_shift, s * St::kG + g);
       } else {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint16_t* p = reinterpret_cast<const uint16_t*>(ap[t].a) + (int64_t)s * kCols + 32 * h;
-          if constexpr (!kTail) st.a[t][h] = load8(p);
-          else st.a[t][h] = load8_guarded(p, s * kCols + 32 * h + q8, kend);
-        }
+        for (int h = 0; h < 2; ++h)
+          st.a[t][h] = load8(reinterpret_cast<const uint16_t*>(abase[t] + ((int64_t)s * kCols + 32 * h) * 2 + aoff[t]));
       }
     }
+  };
+  auto stage_b = [&](int s) {
     if constexpr (kStageB) {
 #pragma unroll
       for (int pl = 0; pl < P; ++pl) {
 #pragma unroll
-        for (int j = 0; j < kMac; ++j) st.b[pl][j] = load_b(tail, 0, pl, j, s);
+        for (int j = 0; j < kMac; ++j) bs[pl][j] = load_b(0, pl, j, s);
       }
     }
   };
-  auto compute = [&](auto tail, const St& st, int s) {
+  auto compute = [&](const St& st, int s) {
     if constexpr (W4) {
-      u32x4 f[TL][4];
 #pragma unroll
-      for (int t = 0; t < TL; ++t) {
+      for (int g = 0; g < St::kG; ++g) {
+        f32x4 sc[TL];
+        u32x4 f[TL][GJ];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t lo = st.a[t][0][j] & 0x0F0F0F0Fu, hi = (st.a[t][0][j] >> 4) & 0x0F0F0F0Fu;
-          f[t][j] = u32x4{T::template nibbles<false>(lo), T::template nibbles<true>(lo),
-                          T::template nibbles<false>(hi), T::template nibbles<true>(hi)};
-        }
-      }
-      const u32x4 minus8 = {T::kMinus8, T::kMinus8, T::kMinus8, T::kMinus8};
+        for (int t = 0; t < TL; ++t) {
+          sc[t] = scale_floats<T>(st.sc[t][g]);
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct) {
-        u32x4 b[P][4];
-#pragma unroll
-        for (int pl = 0; pl < P; ++pl) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if constexpr (kStageB) b[pl][j] = st.b[pl][j];
-            else b[pl][j] = load_b(tail, ct, pl, j, s);
-          }
+          for (int i = 0; i < GJ; ++i) f[t][i] = decode<T>(st.a[t][0][g * GJ + i]);
         }
 #pragma unroll
-        for (int g = 0; g < St::kG; ++g) {
-          f32x4 corr = {0, 0, 0, 0};
+        for (int ct = 0; ct < CT; ++ct) {
+          f32x4 corr = {0, 0, 0, 0}, part[TL];
 #pragma unroll
-          for (int j = g * GJ; j < (g + 1) * GJ; ++j) {
+          for (int t = 0; t < TL; ++t) part[t] = f32x4{0, 0, 0, 0};
 #pragma unroll
-            for (int pl = 0; pl < P; ++pl) corr = T::mfma(minus8, b[pl][j], corr);
+          for (int i = 0; i < GJ; ++i) {
+#pragma unroll
+            for (int pl = 0; pl < P; ++pl) {
+              u32x4 b;
+              if constexpr (kStageB) b = bs[pl][g * GJ + i];
+              else b = load_b(ct, pl, g * GJ + i, s);
+              corr = T::mfma(minus8, b, corr);
+#pragma unroll
+              for (int t = 0; t < TL; ++t) part[t] = T::mfma(f[t][i], b, part[t]);
+            }
           }
 #pragma unroll
           for (int t = 0; t < TL; ++t) {
-            f32x4 part = corr;
 #pragma unroll
-            for (int j = g * GJ; j < (g + 1) * GJ; ++j) {
-#pragma unroll
-              for (int pl = 0; pl < P; ++pl) part = T::mfma(f[t][j], b[pl][j], part);
-            }
-#pragma unroll
-            for (int r = 0; r < 4; ++r) acc[t][ct][r] = __builtin_fmaf(st.sc[t][g][r], part[r], acc[t][ct][r]);
+            for (int r = 0; r < 4; ++r)
+              acc[t][ct][r] = __builtin_fmaf(sc[t][r], part[t][r] + corr[r], acc[t][ct][r]);
           }
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
     } else {
 #pragma unroll
@@ -532,8 +563,8 @@ __device__ __forceinline__ void mac(f32x4 (&acc)[TL][CT], const WeightK& w, cons
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             u32x4 b;
-            if constexpr (kStageB) b = st.b[pl][h];
-            else b = load_b(tail, ct, pl, h, s);
+            if constexpr (kStageB) b = bs[pl][h];
+            else b = load_b(ct, pl, h, s);
 #pragma unroll
             for (int t = 0; t < TL; ++t) acc[t][ct] = T::mfma(st.a[t][h], b, acc[t][ct]);
           }
@@ -542,28 +573,78 @@ __device__ __forceinline__ void mac(f32x4 (&acc)[TL][CT], const WeightK& w, cons
     }
   };
 
-  St st[kDepth];
-  const std::integral_constant<bool, false> body{};
-  const std::integral_constant<bool, true> tail{};
+  // The loads of a step go out kDepth steps ahead.  No branch stands between
+  // a load and its use in the main loop: where paths join, the wait for a
+  // load becomes a wait for all of them.
   const int last = min(s1, full);
-#pragma unroll
-  for (int d = 0; d < kDepth; ++d) {
-    if (s0 + d * ds < last) load(body, st[d], s0 + d * ds);
-  }
-  int s = s0;
-  for (; s < last; s += kDepth * ds) {
+  const int count = s0 < last ? (last - s0 + ds - 1) / ds : 0;
+  if (count > 0) {
+    St st[kDepth];
 #pragma unroll
     for (int d = 0; d < kDepth; ++d) {
-      const int cur = s + d * ds;
-      if (cur < last) {
-        compute(body, st[d], cur);
-        if (cur + kDepth * ds < last) load(body, st[d], cur + kDepth * ds);
+      if (d < count) load(st[d], s0 + d * ds);
+    }
+    stage_b(s0);
+    int i = 0, s = s0;
+    for (; i + 2 * kDepth <= count; i += kDepth) {
+#pragma unroll
+      for (int d = 0; d < kDepth; ++d) {
+        compute(st[d], s);
+        stage_b(s + ds);
+        load(st[d], s + kDepth * ds);
+        s += ds;
+      }
+    }
+#pragma unroll
+    for (int d = 0; d < 2 * kDepth - 1; ++d) {
+      if (i + d < count) {
+        compute(st[d % kDepth], s);
+        if (i + d + 1 < count) stage_b(s + ds);
+        if (d < kDepth - 1 && i + d + kDepth < count) load(st[d], s + kDepth * ds);
+        s += ds;
       }
     }
   }
+  // The last columns, 32 at a time and element by element where a row ends.
   if (full < s1 && full >= s0 && (full - s0) % ds == 0) {
-    load(tail, st[0], full);
-    compute(tail, st[0], full);
+    const int q8 = ((threadIdx.x & 63) >> 4) * 8;
+#pragma unroll 1
+    for (int j = 0; j < kMac; ++j) {
+      const int k = full * kCols + 32 * j;
+      if (k >= bend) break;
+      u32x4 a[TL];
+      f32x4 sc[TL];
+#pragma unroll
+      for (int t = 0; t < TL; ++t) {
+        if constexpr (W4) {
+          a[t] = decode<T>(*reinterpret_cast<const uint32_t*>(ap[t].a + (int64_t)full * 1024 + ap[t].a_off + 4 * j));
+          sc[t] = scale_floats<T>(load_scales<SHIFT>(scbase[t], scoff[t], ap[t].sc_off2, ap[t].sc_shift, k / (32 * GJ)));
+        } else {
+          a[t] = load8_guarded(reinterpret_cast<const uint16_t*>(ap[t].a + (int64_t)k * 2 + ap[t].a_off), k + q8, kend);
+        }
+      }
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        f32x4 corr = {0, 0, 0, 0}, part[TL];
+#pragma unroll
+        for (int t = 0; t < TL; ++t) part[t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int pl = 0; pl < P; ++pl) {
+          const u32x4 b = load8_guarded(bp[ct] + pl * plane + k, k + q8, bend);
+          if constexpr (W4) corr = T::mfma(minus8, b, corr);
+#pragma unroll
+          for (int t = 0; t < TL; ++t) part[t] = T::mfma(a[t], b, part[t]);
+        }
+#pragma unroll
+        for (int t = 0; t < TL; ++t) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            if constexpr (W4) acc[t][ct][r] = __builtin_fmaf(sc[t][r], part[t][r] + corr[r], acc[t][ct][r]);
+            else acc[t][ct][r] += part[t][r];
+          }
+        }
+      }
+    }
   }
 }
 
@@ -599,7 +680,7 @@ __device__ __forceinline__ void store_out(void* out, int64_t i, float v, int f32
 // time.  GATED: silu(gate) * up goes to the workspace in two 16-bit parts
 // (the down product then sees it to 16 bits and more, not rounded to the 8 of
 // a bfloat16), and the tile-0 workgroups leave the plan down_kernel follows.
-template <class T, int G, bool GATED, int CTM>
+template <class T, int G, bool GATED, bool SHIFT>
 __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const RowsKArgs a) {
   constexpr bool W4 = G != 0;
   constexpr int GJ = W4 ? G / 32 : 1;
@@ -678,6 +759,7 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const RowsKArgs a) {
 
   const int steps = (a.w.cols + Step<W4>::kCols - 1) / Step<W4>::kCols;
   RowPtr<W4> ap[TL];
+  expert = __builtin_amdgcn_readfirstlane(expert);
   ap[0] = row_ptr<W4>(a.w, expert, tile * 16);
   if constexpr (GATED) ap[1] = row_ptr<W4>(a.w, expert, a.inter + tile * 16);
 
@@ -695,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const RowsKArgs a) {
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) acc[t][ct] = f32x4{0, 0, 0, 0};
     }
-    mac<T, W4, GJ, TL, CT, 1>(acc, a.w, ap, bp, 0, a.w.cols, wave, steps, kExpertWaves);
+    mac<T, W4, SHIFT, GJ, TL, CT, 1>(acc, a.w, ap, bp, 0, a.w.cols, wave, steps, kExpertWaves);
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
       __syncthreads();
@@ -728,16 +810,7 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const RowsKArgs a) {
       }
     }
   };
-  for (int c0 = 0; c0 < m; c0 += 16 * CTM) {
-    const int left = min(m - c0, 16 * CTM);
-    if constexpr (CTM == 1) {
-      run(std::integral_constant<int, 1>{}, c0);
-    } else {
-      if (left <= 16) run(std::integral_constant<int, 1>{}, c0);
-      else if (left <= 32) run(std::integral_constant<int, 2>{}, c0);
-      else run(std::integral_constant<int, 4>{}, c0);
-    }
-  }
+  for (int c0 = 0; c0 < m; c0 += 16) run(std::integral_constant<int, 1>{}, c0);
 }
 
 // A workgroup takes one tile of 16 output columns and one chunk of up to 128
@@ -746,7 +819,7 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const RowsKArgs a) {
 // weight * product into its own copy of the chunk's output tile in LDS (each
 // token at most once per expert, so lanes never meet), and the copies are
 // added in wave order at the end.
-template <class T, int G, int CTM>
+template <class T, int G>
 __global__ void __launch_bounds__(kThreads, 4) down_kernel(const DownKArgs a) {
   constexpr bool W4 = G != 0;
   constexpr int GJ = W4 ? G / 32 : 1;
@@ -789,9 +862,10 @@ __global__ void __launch_bounds__(kThreads, 4) down_kernel(const DownKArgs a) {
     const int k0 = (int)(s % steps);
     const int k1 = (int)min((int64_t)steps, k0 + (end - s));
     s += k1 - k0;
-    const int expert = p.expert[slot];
+    const int expert = __builtin_amdgcn_readfirstlane(p.expert[slot]);
     const int* off = p.off + slot * (kMaxChunks + 1) + chunk;
-    const int o0 = off[0], m = off[1] - o0;
+    const int o0 = __builtin_amdgcn_readfirstlane(off[0]);
+    const int m = __builtin_amdgcn_readfirstlane(off[1]) - o0;
     const int64_t at = (int64_t)slot * a.n + o0;
     RowPtr<W4> ap[1] = {row_ptr<W4>(a.w, expert, tile * 16)};
     auto run = [&](auto ct_c, int c0) {
@@ -811,7 +885,7 @@ __global__ void __launch_bounds__(kThreads, 4) down_kernel(const DownKArgs a) {
       f32x4 acc[1][CT];
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) acc[0][ct] = f32x4{0, 0, 0, 0};
-      mac<T, W4, GJ, 1, CT, 2>(acc, a.w, ap, bp, p.act_plane, p.act_stride, k0, k1, 1);
+      mac<T, W4, false, GJ, 1, CT, 2>(acc, a.w, ap, bp, p.act_plane, p.act_stride, k0, k1, 1);
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) {
         if (tok[ct] >= 0) {
@@ -823,16 +897,7 @@ __global__ void __launch_bounds__(kThreads, 4) down_kernel(const DownKArgs a) {
         }
       }
     };
-    for (int c0 = 0; c0 < m; c0 += 16 * CTM) {
-      const int left = min(m - c0, 16 * CTM);
-      if constexpr (CTM == 1) {
-        run(std::integral_constant<int, 1>{}, c0);
-      } else {
-        if (left <= 16) run(std::integral_constant<int, 1>{}, c0);
-        else if (left <= 32) run(std::integral_constant<int, 2>{}, c0);
-        else run(std::integral_constant<int, 4>{}, c0);
-      }
-    }
+    for (int c0 = 0; c0 < m; c0 += 16) run(std::integral_constant<int, 1>{}, c0);
   }
   __syncthreads();
   for (int i = tid; i < nc * 16; i += kThreads) {
@@ -849,8 +914,13 @@ template <class T, int G, bool GATED>
 void start_rows(const RowsKArgs& a, hipStream_t stream) {
   const int slots = a.ids == nullptr ? 1 : a.by_pair ? a.n * a.top_k : a.num_experts;
   const dim3 grid((a.inter + 15) / 16, slots);
-  if (a.n <= 16) rows_kernel<T, G, GATED, 1><<<grid, kThreads, 0, stream>>>(a);
-  else rows_kernel<T, G, GATED, 4><<<grid, kThreads, 0, stream>>>(a);
+  if constexpr (GATED && G != 0) {
+    if (a.inter % 4 != 0) {               // the up rows' scales straddle their groups of four
+      rows_kernel<T, G, GATED, true><<<grid, kThreads, 0, stream>>>(a);
+      return;
+    }
+  }
+  rows_kernel<T, G, GATED, false><<<grid, kThreads, 0, stream>>>(a);
 }
 
 template <class T, bool GATED>
@@ -869,8 +939,7 @@ void start_down(const DownKArgs& a, hipStream_t stream) {
   const int grid = (a.tiles + 7) / 8 * 8 * a.chunks;
   const int nc = std::min(a.n, kChunkTokens);
   const size_t lds = (size_t)kExpertWaves * nc * 16 * sizeof(float);
-  if (nc <= 16) down_kernel<T, G, 1><<<grid, kThreads, lds, stream>>>(a);
-  else down_kernel<T, G, 4><<<grid, kThreads, lds, stream>>>(a);
+  down_kernel<T, G><<<grid, kThreads, lds, stream>>>(a);
 }
 
 template <class T>
