@@ -48,18 +48,21 @@ def build(verbose: bool = False) -> str:
         a_obj = os.path.join(tmp, "moe_ep_api.o")
         p_obj = os.path.join(tmp, "moe_ep_plan.o")
         xk_obj = os.path.join(tmp, "moe_experts_kernels.o")
+        xr_obj = os.path.join(tmp, "moe_route_kernels.o")
         xa_obj = os.path.join(tmp, "moe_experts_api.o")
         lib_tmp = os.path.join(tmp, LIB_NAME)
         compile_steps = [
             [HIPCC, f"--offload-arch={ARCH}", *COMMON, *DEVICE_FLAGS, "-x", "hip", "-c",
              os.path.join(CSRC, "moe_experts_kernels.hip"), "-o", xk_obj],
             [HIPCC, f"--offload-arch={ARCH}", *COMMON, *DEVICE_FLAGS, "-x", "hip", "-c",
+             os.path.join(CSRC, "moe_route_kernels.hip"), "-o", xr_obj],
+            [HIPCC, f"--offload-arch={ARCH}", *COMMON, *DEVICE_FLAGS, "-x", "hip", "-c",
              os.path.join(CSRC, "moe_ep_kernels.hip"), "-o", k_obj],
             [HIPCC, *COMMON, "-c", os.path.join(CSRC, "moe_ep_api.cpp"), "-o", a_obj],
             [HIPCC, *COMMON, "-c", os.path.join(CSRC, "moe_ep_plan.cpp"), "-o", p_obj],
             [HIPCC, *COMMON, "-c", os.path.join(CSRC, "moe_experts_api.cpp"), "-o", xa_obj],
         ]
-        link = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", k_obj, a_obj, p_obj, xk_obj, xa_obj,
+        link = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", k_obj, a_obj, p_obj, xk_obj, xr_obj, xa_obj,
                 "-o", lib_tmp]
         with ThreadPoolExecutor(max_workers=len(compile_steps)) as pool:
             outs = list(pool.map(_run, compile_steps))

@@ -167,7 +167,7 @@ constexpr int32_t kMaxSide = 1 << 24;
 // Workspace of one pass: [ids][weights] with a router, the plan, the
 // activations.  Every part starts on 256 bytes.
 struct LayerSpace {
-  int64_t ids, weights, expert, off, pair, weight, act, total;
+  int64_t ids, weights, head, pair, act, total;
   int32_t n, slots, act_stride;
   bool by_pair;
 };
@@ -193,10 +193,8 @@ int make_space(const moe_ep_layer_args* a, LayerSpace* s) {
   };
   s->ids = take(a->router ? pairs * 4 : 0);
   s->weights = take(a->router ? pairs * 4 : 0);
-  s->expert = take((int64_t)s->slots * 4);
-  s->off = take((int64_t)s->slots * (kMaxChunks + 1) * 4);
-  s->pair = take((int64_t)s->slots * s->n * 4);
-  s->weight = take((int64_t)s->slots * s->n * 4);
+  s->head = take((int64_t)s->slots * kMaxChunks * 4);
+  s->pair = take((int64_t)s->slots * s->n * 8);
   s->act = take(2 * pairs * s->act_stride * 2);
   s->total = std::max<int64_t>(off, 256);
   return MOE_EP_OK;
@@ -324,10 +322,8 @@ int moe_ep_layer(const moe_ep_layer_args* a, void* stream) {
 
   uint8_t* ws = static_cast<uint8_t*>(a->workspace);
   PlanK p;
-  p.expert = reinterpret_cast<int32_t*>(ws + s.expert);
-  p.off = reinterpret_cast<int32_t*>(ws + s.off);
-  p.pair = reinterpret_cast<int32_t*>(ws + s.pair);
-  p.weight = reinterpret_cast<float*>(ws + s.weight);
+  p.head = reinterpret_cast<int32_t*>(ws + s.head);
+  p.pair = ws + s.pair;
   p.act = reinterpret_cast<uint16_t*>(ws + s.act);
   p.act_stride = s.act_stride;
   r.x_stride = a->hidden_stride;

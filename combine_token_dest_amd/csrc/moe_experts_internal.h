@@ -59,15 +59,28 @@ struct WeightK {
 // What the layer's first kernel leaves in the workspace for its second.
 // Slot a is one expert that may have tokens (a pair's or an expert's index).
 struct PlanK {
-  int32_t* expert;            // [slots]
-  int32_t* off;               // [slots, kMaxChunks + 1]: where chunk c's tokens start in the slot's list
-  int32_t* pair;              // [slots, n]: token << 6 | top-k slot, tokens ascending
-  float* weight;              // [slots, n]: the pair's weight
+  int32_t* head;              // [chunks, slots]: pack_head() of the slot's tokens in the chunk
+  void* pair;                 // [slots, n] of {token << 6 | top-k slot, weight}, tokens ascending
   uint16_t* act;              // [2, n * top_k, act_stride]: activations, high and low part
   int64_t act_plane;          // elements from a high part to its low part
   int32_t act_stride;
   int32_t slots;
 };
+
+// A slot's tokens in one chunk: how many (up to 128), where they start in
+// its list (below 2048), and its expert (below 1024).
+#ifdef __HIP__
+#define MOE_EP_HD __host__ __device__ __forceinline__
+#else
+#define MOE_EP_HD inline
+#endif
+static_assert(kChunkTokens <= 255 && kPassTokens <= 2048 && MOE_EP_MAX_EXPERTS <= 1024, "fields of a packed head");
+MOE_EP_HD int32_t pack_head(int count, int start, int expert) {
+  return (int32_t)((uint32_t)count | (uint32_t)(count ? start : 0) << 8 | (uint32_t)expert << 19);
+}
+MOE_EP_HD int head_count(int32_t h) { return h & 255; }
+MOE_EP_HD int head_start(int32_t h) { return (h >> 8) & 2047; }
+MOE_EP_HD int head_expert(int32_t h) { return (h >> 19) & 1023; }
 
 // The product whose rows are gathered by expert: expert_linear, and the
 // layer's gate and up product.
@@ -87,6 +100,8 @@ struct RowsKArgs {
   int32_t num_experts;
   int32_t by_pair;            // slots are (token, k) pairs, else experts
   int32_t inter;              // layer: intermediate size; linear: out features
+  int32_t split;              // waves that share a tile (set by the launcher)
+  int32_t tiles_per_block;    // (set by the launcher)
 };
 
 // The layer's down product, summed over the experts of each token.

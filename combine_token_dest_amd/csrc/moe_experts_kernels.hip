@@ -1,15 +1,13 @@
-// gfx950 kernels of the expert-side operators: the router's selection
-// (route_kernel), the experts' linear product (rows_kernel) and the two
-// kernels of a whole mixture-of-experts layer for a few tokens (rows_kernel
-// with the gated epilogue, then down_kernel).
+// gfx950 kernels of the experts' products: the linear product (rows_kernel)
+// and the two kernels of a whole mixture-of-experts layer for a few tokens
+// (rows_kernel with the gated epilogue, then down_kernel).
 //
 // At decode sizes an expert sees a handful of tokens, so its matrices are
 // read once for little arithmetic: the products are bound by streaming the
-// weights from HBM.  Both product kernels therefore give one wave 16 weight
-// rows as the A operand of v_mfma_f32_16x16x32 and up to 16 tokens as the
-// columns of B; the eight waves of a workgroup share the sum over k and add
-// their float32 accumulators through LDS in a fixed order, so results do not
-// depend on timing.
+// weights from HBM.  Both kernels give a wave 16 weight rows as the A operand
+// of v_mfma_f32_16x16x32 and up to 16 tokens as the columns of B; waves that
+// share rows split the sum over k and add their float32 accumulators through
+// LDS in a fixed order, so results do not depend on timing.
 //
 // 4-bit weights: W[n,k] = (q - 8) * scale[n, k / g].  A byte 0000qqqq read as
 // e4m3 is the subnormal q * 2^-9, so v_cvt_scalef32_pk_{bf16,f16}_fp8 with
@@ -21,355 +19,37 @@
 #include <stdint.h>
 
 #include <algorithm>
-#include <cfloat>
-#include <climits>
 #include <type_traits>
 
+#include "moe_experts_device.h"
 #include "moe_experts_internal.h"
 
 namespace moe_ep_detail {
 namespace {
 
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-
-struct BF16 {
-  static __device__ __forceinline__ f32x4 mfma(const u32x4& a, const u32x4& b, const f32x4& c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
-                                                   0, 0);
-  }
-  template <bool HI>
-  static __device__ __forceinline__ uint32_t nibbles(uint32_t w) {
-    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 512.0f, HI));
-  }
-  static constexpr uint32_t kMinus8 = 0xC100C100u;   // two of -8.0
-  static __device__ __forceinline__ float to_float(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
-  static __device__ __forceinline__ uint16_t from_float(float f) {
-    return __builtin_bit_cast(uint16_t, static_cast<__bf16>(f));
-  }
-  // v as high + low: 16 significant bits.  Infinities and NaN stay in the high part.
-  static __device__ __forceinline__ void split(float v, uint16_t* hi, uint16_t* lo) {
-    *hi = from_float(v);
-    const float h = to_float(*hi);
-    *lo = __builtin_isfinite(h) ? from_float(v - h) : (uint16_t)0;
-  }
-};
-
-struct F16 {
-  static __device__ __forceinline__ f32x4 mfma(const u32x4& a, const u32x4& b, const f32x4& c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
-                                                  0);
-  }
-  template <bool HI>
-  static __device__ __forceinline__ uint32_t nibbles(uint32_t w) {
-    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 512.0f, HI));
-  }
-  static constexpr uint32_t kMinus8 = 0xC800C800u;
-  static __device__ __forceinline__ float to_float(uint16_t v) {
-    return static_cast<float>(__builtin_bit_cast(_Float16, v));
-  }
-  static __device__ __forceinline__ uint16_t from_float(float f) {
-    return __builtin_bit_cast(uint16_t, static_cast<_Float16>(f));
-  }
-  // 22 significant bits up to 65504; a finite value beyond that keeps the
-  // rest in the low part, and saturates at 131008.
-  static __device__ __forceinline__ void split(float v, uint16_t* hi, uint16_t* lo) {
-    if (!__builtin_isfinite(v)) {
-      *hi = from_float(v);
-      *lo = 0;
-      return;
-    }
-    *hi = from_float(__builtin_fminf(__builtin_fmaxf(v, -65504.0f), 65504.0f));
-    *lo = from_float(__builtin_fminf(__builtin_fmaxf(v - to_float(*hi), -65504.0f), 65504.0f));
-  }
-};
-
-// ---------------------------------------------------------------------------
-// route
-// ---------------------------------------------------------------------------
-
-__device__ __forceinline__ float load_logit(const void* p, int64_t i, int dtype) {
-  if (dtype == MOE_EP_F32) return static_cast<const float*>(p)[i];
-  const uint16_t v = static_cast<const uint16_t*>(p)[i];
-  return dtype == MOE_EP_BF16 ? BF16::to_float(v) : F16::to_float(v);
-}
-
-// -inf closes the expert; NaN does too; +inf reads as the largest float.
-__device__ __forceinline__ float clean_logit(float l) {
-  return l == l ? __builtin_fminf(l, FLT_MAX) : -INFINITY;
-}
-
+// Global memory, said to the compiler: a pointer whose origin it cannot see
+// would be read with flat loads, which also count as LDS accesses and make
+// every wait a wait for all loads.
 template <typename V>
-__device__ __forceinline__ bool better(V v1, int e1, V v0, int e0) {
-  return v1 > v0 || (v1 == v0 && e1 < e0);
+__device__ __forceinline__ V gload(const void* p) {
+  return *reinterpret_cast<const __attribute__((address_space(1))) V*>(reinterpret_cast<uintptr_t>(p));
 }
-
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp(uint32_t x) {
-  return __builtin_amdgcn_update_dpp(x, x, CTRL, 0xf, 0xf, false);
-}
-template <int CTRL>
-__device__ __forceinline__ float dpp(float x) {
-  return __uint_as_float(dpp<CTRL>(__float_as_uint(x)));
-}
-template <int CTRL>
-__device__ __forceinline__ double dpp(double x) {
-  u32x2 u = __builtin_bit_cast(u32x2, x);
-  u[0] = dpp<CTRL>(u[0]);
-  u[1] = dpp<CTRL>(u[1]);
-  return __builtin_bit_cast(double, u);
-}
-
-// x of both halves of a pair of 16-lane rows (W = 16) or of a pair of 32-lane
-// halves (W = 32): the two results are the pair's first and second member.
-template <int W>
-__device__ __forceinline__ void both(uint32_t x, uint32_t* a, uint32_t* b) {
-  if constexpr (W == 16) {
-    auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
-    *a = r[0];
-    *b = r[1];
-  } else {
-    auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
-    *a = r[0];
-    *b = r[1];
-  }
-}
-template <int W>
-__device__ __forceinline__ void both(float x, float* a, float* b) {
-  uint32_t u, v;
-  both<W>(__float_as_uint(x), &u, &v);
-  *a = __uint_as_float(u);
-  *b = __uint_as_float(v);
-}
-template <int W>
-__device__ __forceinline__ void both(double x, double* a, double* b) {
-  const u32x2 u = __builtin_bit_cast(u32x2, x);
-  u32x2 p, q;
-  uint32_t s, t;
-  both<W>(u[0], &s, &t);
-  p[0] = s;
-  q[0] = t;
-  both<W>(u[1], &s, &t);
-  p[1] = s;
-  q[1] = t;
-  *a = __builtin_bit_cast(double, p);
-  *b = __builtin_bit_cast(double, q);
-}
-
-// All-reductions over the LPT (16 or 64) lanes of a token.
-template <int CTRL, typename V>
-__device__ __forceinline__ void best_step(V& v, int& e) {
-  const V ov = dpp<CTRL>(v);
-  const int oe = (int)dpp<CTRL>((uint32_t)e);
-  if (better(ov, oe, v, e)) {
-    v = ov;
-    e = oe;
-  }
-}
-template <int W, typename V>
-__device__ __forceinline__ void best_pair(V& v, int& e) {
-  V a, b;
-  uint32_t ea, eb;
-  both<W>(v, &a, &b);
-  both<W>((uint32_t)e, &ea, &eb);
-  const bool second = better(b, (int)eb, a, (int)ea);
-  v = second ? b : a;
-  e = second ? (int)eb : (int)ea;
-}
-template <int LPT, typename V>
-__device__ __forceinline__ void reduce_best(V& v, int& e) {
-  best_step<0x128>(v, e);   // row_ror:8, 4, 2, 1
-  best_step<0x124>(v, e);
-  best_step<0x122>(v, e);
-  best_step<0x121>(v, e);
-  if constexpr (LPT == 64) {
-    best_pair<16>(v, e);
-    best_pair<32>(v, e);
-  }
-}
-template <int LPT, typename V>
-__device__ __forceinline__ V reduce_sum(V v) {
-  v += dpp<0x128>(v);
-  v += dpp<0x124>(v);
-  v += dpp<0x122>(v);
-  v += dpp<0x121>(v);
-  if constexpr (LPT == 64) {
-    V a, b;
-    both<16>(v, &a, &b);
-    v = a + b;
-    both<32>(v, &a, &b);
-    v = a + b;
-  }
-  return v;
-}
-template <int LPT>
-__device__ __forceinline__ float reduce_max(float v) {
-  int e = 0;
-  reduce_best<LPT>(v, e);
-  return v;
-}
-
-__device__ __forceinline__ double score64(int score, float l, float top) {
-  return score == MOE_EP_SCORE_SIGMOID ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)top);
-}
-
-constexpr int kRouteThreads = 256;
-
-// One token per LPT lanes, expert e = v * LPT + lane in register v.  The
-// selection is top_k rounds of an all-lane maximum of (choice, lowest index).
-// Without a bias or groups the choice is the logit itself (V = float): it
-// orders the experts as the score does, without the ties of a saturated
-// score.  Otherwise it is the score in float64 (V = double), so that a
-// near-tie is decided by the values and not by a float32 rounding.
-// Weights are computed in float64 by one lane per slot and rounded once.
-template <typename V, int LPT, int VPL, bool GROUPS>
-__global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteKArgs a) {
-  constexpr int kTokens = 64 / LPT;
-  const int lane = threadIdx.x & 63;
-  const int wave = threadIdx.x >> 6;
-  const int sub = lane & (LPT - 1);
-  const int64_t token = ((int64_t)blockIdx.x * (kRouteThreads / 64) + wave) * kTokens + lane / LPT;
-  const int64_t t = token < a.n ? token : a.n - 1;
-  const int E = a.num_experts;
-  const int64_t row = t * a.logits_stride;
-
-  float l[VPL];
-#pragma unroll
-  for (int v = 0; v < VPL; ++v) {
-    const int e = v * LPT + sub;
-    l[v] = load_logit(a.logits, row + (e < E ? e : E - 1), a.logits_dtype);
-  }
-#pragma unroll
-  for (int v = 0; v < VPL; ++v) l[v] = v * LPT + sub < E ? clean_logit(l[v]) : -INFINITY;
-
-  V c[VPL];
-  float top = 0.0f;
-  double total = 1.0;
-  if constexpr (std::is_same<V, double>::value) {
-    if (a.score == MOE_EP_SCORE_SOFTMAX) {
-      float m = l[0];
-#pragma unroll
-      for (int v = 1; v < VPL; ++v) m = __builtin_fmaxf(m, l[v]);
-      top = reduce_max<LPT>(m);
-      double s = 0.0;
-#pragma unroll
-      for (int v = 0; v < VPL; ++v) {
-        c[v] = l[v] == -INFINITY ? 0.0 : score64(MOE_EP_SCORE_SOFTMAX, l[v], top);
-        s += c[v];
-      }
-      total = reduce_sum<LPT>(s);
-    }
-#pragma unroll
-    for (int v = 0; v < VPL; ++v) {
-      const int e = v * LPT + sub;
-      double x = a.score == MOE_EP_SCORE_SOFTMAX ? c[v] / total : score64(MOE_EP_SCORE_SIGMOID, l[v], 0.0f);
-      if (a.bias) x += (double)a.bias[e < E ? e : E - 1];
-      c[v] = l[v] > -INFINITY && x > -INFINITY ? x : -INFINITY;   // a NaN bias closes too
-    }
-    if constexpr (GROUPS) {
-      // LPT is 64 here: one token per wave.
-      extern __shared__ double lds[];
-      const int G = a.num_groups;
-      const int size = E / G;
-      double* cs = lds + wave * (E + G);
-      double* gv = cs + E;
-#pragma unroll
-      for (int v = 0; v < VPL; ++v) {
-        const int e = v * LPT + sub;
-        if (e < E) cs[e] = c[v];
-      }
-      __syncthreads();
-      for (int g = sub; g < G; g += LPT) {
-        double b1 = -INFINITY, b2 = -INFINITY;
-        for (int i = 0; i < size; ++i) {
-          const double x = cs[g * size + i];
-          if (x > b1) {
-            b2 = b1;
-            b1 = x;
-          } else if (x > b2) {
-            b2 = x;
-          }
-        }
-        gv[g] = a.group_top > 1 && b2 > -INFINITY ? b1 + b2 : b1;
-      }
-      __syncthreads();
-#pragma unroll
-      for (int v = 0; v < VPL; ++v) {
-        const int e = v * LPT + sub;
-        if (e < E) {
-          const int g = e / size;
-          const double mine = gv[g];
-          int ahead = 0;
-          for (int h = 0; h < G; ++h) ahead += better(gv[h], h, mine, g) ? 1 : 0;
-          if (ahead >= a.top_groups) c[v] = -INFINITY;
-        }
-      }
-    }
-  } else {
-#pragma unroll
-    for (int v = 0; v < VPL; ++v) c[v] = l[v];
-  }
-
-  int mine = INT_MAX;       // the expert of slot `sub`
-  for (int r = 0; r < a.top_k; ++r) {
-    V bv = -INFINITY;
-    int be = INT_MAX;
-#pragma unroll
-    for (int v = 0; v < VPL; ++v) {
-      if (c[v] > bv) {
-        bv = c[v];
-        be = v * LPT + sub;
-      }
-    }
-    reduce_best<LPT>(bv, be);
-    if (std::is_same<V, float>::value && r == 0) top = (float)bv;
-    if (sub == r) mine = be;
-#pragma unroll
-    for (int v = 0; v < VPL; ++v) {
-      if (be == v * LPT + sub) c[v] = -INFINITY;
-    }
-  }
-
-  if constexpr (std::is_same<V, float>::value) {
-    if (a.score == MOE_EP_SCORE_SOFTMAX && !a.renormalize) {
-      float s = 0.0f;
-#pragma unroll
-      for (int v = 0; v < VPL; ++v) s += l[v] == -INFINITY ? 0.0f : expf(l[v] - top);
-      total = (double)reduce_sum<LPT>(s);
-    }
-  }
-  const bool open = mine != INT_MAX && sub < a.top_k;
-  double s = 0.0;
-  if (open) s = score64(a.score, clean_logit(load_logit(a.logits, row + mine, a.logits_dtype)), top);
-  const double z = a.renormalize ? reduce_sum<LPT>(s) : total;
-  if (token < a.n && sub < a.top_k) {
-    a.ids[token * a.top_k + sub] = open ? mine : a.invalid_id;
-    a.weights[token * a.top_k + sub] = z > 0.0 ? (float)(s / z * (double)a.scale) : 0.0f;
-  }
-}
-
-// ---------------------------------------------------------------------------
-// the experts' products
-// ---------------------------------------------------------------------------
 
 // A 16-byte load of 16-bit elements from any element address (gfx950 takes
 // unaligned global loads; aligned ones cost nothing extra).
 struct __attribute__((packed, aligned(2))) Elems8 {
   u32x4 v;
 };
-__device__ __forceinline__ u32x4 load8(const uint16_t* p) {
-  return reinterpret_cast<const Elems8*>(p)->v;
+__device__ __forceinline__ u32x4 load8(const void* p) {
+  return reinterpret_cast<const __attribute__((address_space(1))) Elems8*>(reinterpret_cast<uintptr_t>(p))->v;
 }
 // The same where only elements k < end of a row exist: zeros beyond.
-__device__ __forceinline__ u32x4 load8_guarded(const uint16_t* p, int k, int end) {
+__device__ __forceinline__ u32x4 load8_guarded(const void* p, int k, int end) {
   if (k + 8 <= end) return load8(p);
   u32x4 v = {0, 0, 0, 0};
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    if (k + i < end) v[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
+    if (k + i < end) v[i >> 1] |= (uint32_t)static_cast<const uint16_t*>(p)[i] << (16 * (i & 1));
   }
   return v;
 }
@@ -381,13 +61,13 @@ template <> struct Step<true> { static constexpr int kCols = 128, kMac = 4; };
 
 // Where a wave finds 16 weight rows that start at row `first`: bases that are
 // the same for all lanes (kept in scalar registers) and each lane's 32-bit
-// offset from them.
+// byte offset from them.
 template <bool W4>
 struct RowPtr {
   const uint8_t* a;           // A rows
-  uint32_t a_off;             // bytes: the lane's row and k offset
+  uint32_t a_off;             // the lane's row and k offset
   const uint16_t* sc;         // 4-bit: scales of the tile, group 0
-  uint32_t sc_off, sc_off2;   // bytes: the four rows with the lane's first accumulator row, and the next four
+  uint32_t sc_off, sc_off2;   // the four rows with the lane's first accumulator row, and the next four
   int sc_shift;               // bits from the first of those four rows to the lane's, the same for all lanes
 };
 
@@ -424,11 +104,11 @@ __device__ __forceinline__ RowPtr<W4> row_ptr(const WeightK& w, int expert, int 
 template <bool SHIFT>
 __device__ __forceinline__ u32x2 load_scales(const uint16_t* base, uint32_t off, uint32_t off2, int shift, int group) {
   const uint8_t* p = reinterpret_cast<const uint8_t*>(base + (int64_t)group * 16);
-  const u32x2 v = *reinterpret_cast<const u32x2*>(p + off);
+  const u32x2 v = gload<u32x2>(p + off);
   if constexpr (!SHIFT) {
     return v;
   } else {
-    const uint64_t next = *reinterpret_cast<const uint64_t*>(p + off2);
+    const uint64_t next = gload<uint64_t>(p + off2);
     return __builtin_bit_cast(u32x2, __builtin_bit_cast(uint64_t, v) >> shift |
                                          (shift ? next << (64 - shift) : 0));
   }
@@ -449,368 +129,437 @@ __device__ __forceinline__ u32x4 decode(uint32_t w) {
                T::template nibbles<true>(hi)};
 }
 
-// What one step loads of the weights, two steps ahead of its use.
-template <bool W4, int GJ, int TL>
-struct Stage {
-  static constexpr int kG = W4 ? 4 / GJ : 1;
-  u32x4 a[TL][W4 ? 1 : 2];
-  u32x2 sc[W4 ? TL : 1][kG];
-};
-
-// acc[tl][ct] += A(16 rows of tile tl, step columns) * B(columns of ct), over
+// One wave's product of TL tiles of 16 weight rows with 16 columns of B over
 // the steps s0, s0 + ds, ... below s1.  P planes of B (high, low part) are
-// `plane` elements apart.  bend: columns of B's rows.
-template <class T, bool W4, bool SHIFT, int GJ, int TL, int CT, int P>
-__device__ __forceinline__ void mac(f32x4 (&acc)[TL][CT], const WeightK& w, const RowPtr<W4> (&ap)[TL],
-                                    const uint16_t* const (&bp)[CT], int64_t plane, int bend, int s0, int s1,
-                                    int ds) {
-  constexpr int kCols = Step<W4>::kCols, kMac = Step<W4>::kMac;
-  constexpr bool kStageB = CT == 1;
-  constexpr int kDepth = W4 && GJ == 1 ? 2 : TL == 1 ? 4 : 2;
-  typedef Stage<W4, GJ, TL> St;
-  // B comes from L2: one step ahead for one column tile, at its use for more
-  // (there are no registers for it).
-  u32x4 bs[kStageB ? P : 1][kStageB ? kMac : 1];
-  const u32x4 minus8 = {T::kMinus8, T::kMinus8, T::kMinus8, T::kMinus8};
-  // Bases stay in scalar registers and offsets in one vector register each:
-  // left alone, the compiler keeps a 64-bit vector address per load across
-  // the caller's loop.
+// `plane` elements apart.
+//
+// aim_a / aim_b set the operands and send out the first kDepth steps' loads;
+// run() goes through the steps, each step's loads kDepth steps ahead.  Loads
+// return in the order they were sent, so A and B of a step go out together:
+// were B sent later, the wait for it would be a wait for all of A's loads
+// before it.  For the same reason no branch stands between a load and its use
+// in the main loop: where paths join, the wait for a load becomes a wait for
+// all.
+template <class T, int G, bool SHIFT, int TL, int P>
+struct Mac {
+  static constexpr bool W4 = G != 0;
+  static constexpr int GJ = W4 ? G / 32 : 1;              // matrix instructions per scale group
+  static constexpr int kG = W4 ? 4 / GJ : 1;              // scale groups per step
+  static constexpr int kCols = Step<W4>::kCols, kMac = Step<W4>::kMac;
+  // What 128 registers hold: B is staged as deep as A, or one step deep.
+  static constexpr int kARegs = W4 ? TL * (4 + 2 * kG) : TL * 8, kBRegs = P * kMac * 4;
+  static constexpr bool kDeepB = kARegs + kBRegs <= 32;
+  static constexpr int kDepth = !kDeepB ? 2 : kARegs + kBRegs <= 18 ? 4 : kARegs + kBRegs <= 26 ? 3 : 2;
+
+  struct StageA {
+    u32x4 a[TL][W4 ? 1 : 2];
+    u32x2 sc[W4 ? TL : 1][kG];
+  };
+  struct StageB {
+    u32x4 b[P][kMac];
+  };
+  StageA sa[kDepth];
+  StageB sb[kDeepB ? kDepth : 1];
   const uint8_t* abase[TL];
   const uint16_t* scbase[TL];
-  uint32_t aoff[TL], scoff[TL];
-#pragma unroll
-  for (int t = 0; t < TL; ++t) {
-    abase[t] = ap[t].a;
-    scbase[t] = ap[t].sc;
-    aoff[t] = ap[t].a_off;
-    scoff[t] = ap[t].sc_off;
-    asm volatile("" : "+s"(abase[t]), "+v"(aoff[t]));
-    if constexpr (W4) asm volatile("" : "+s"(scbase[t]), "+v"(scoff[t]));
-  }
-  const int kend = w.cols;
-  // Steps with no column past an end of either row; at most one step follows.
-  const int full = (W4 ? bend : (kend < bend ? kend : bend)) / kCols;
+  uint32_t aoff[TL], scoff[TL], scoff2[TL];
+  int shift[TL];
+  const uint16_t* bp;
+  int64_t plane;
+  int kend, bend, full, s0, s1, ds, count;
 
-  auto load_b = [&](int ct, int pl, int j, int s) -> u32x4 {
-    return load8(bp[ct] + pl * plane + (int64_t)s * kCols + 32 * j);
-  };
-  auto load = [&](St& st, int s) {
+  __device__ __forceinline__ void steps(const WeightK& w, int bend_, int64_t plane_, int s0_, int s1_, int ds_) {
+    kend = w.cols;
+    bend = bend_;
+    plane = plane_;
+    s0 = s0_;
+    s1 = s1_;
+    ds = ds_;
+    // Steps with no column past an end of either row; at most one step follows.
+    full = (W4 ? bend : (kend < bend ? kend : bend)) / kCols;
+    const int last = min(s1, full);
+    count = s0 < last ? (last - s0 + ds - 1) / ds : 0;
+  }
+
+  __device__ __forceinline__ void load_a(StageA& x, int s) {
 #pragma unroll
     for (int t = 0; t < TL; ++t) {
       if constexpr (W4) {
-        st.a[t][0] = *reinterpret_cast<const u32x4*>(abase[t] + (int64_t)s * 1024 + aoff[t]);
+        x.a[t][0] = gload<u32x4>(abase[t] + (int64_t)s * 1024 + aoff[t]);
 #pragma unroll
-        for (int g = 0; g < St::kG; ++g) st.sc[t][g] = load_scales<SHIFT>(scbase[t], scoff[t], ap[t].sc_off2, ap[t].sc_shift, s * St::kG + g);
+        for (int g = 0; g < kG; ++g)
+          x.sc[t][g] = load_scales<SHIFT>(scbase[t], scoff[t], scoff2[t], shift[t], s * kG + g);
       } else {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          st.a[t][h] = load8(reinterpret_cast<const uint16_t*>(abase[t] + ((int64_t)s * kCols + 32 * h) * 2 + aoff[t]));
+        for (int h = 0; h < 2; ++h) x.a[t][h] = load8(abase[t] + ((int64_t)s * kCols + 32 * h) * 2 + aoff[t]);
       }
     }
-  };
-  auto stage_b = [&](int s) {
-    if constexpr (kStageB) {
+  }
+  __device__ __forceinline__ void load_b(StageB& x, int s) {
 #pragma unroll
-      for (int pl = 0; pl < P; ++pl) {
+    for (int pl = 0; pl < P; ++pl) {
 #pragma unroll
-        for (int j = 0; j < kMac; ++j) bs[pl][j] = load_b(0, pl, j, s);
-      }
+      for (int j = 0; j < kMac; ++j) x.b[pl][j] = load8(bp + pl * plane + (int64_t)s * kCols + 32 * j);
     }
-  };
-  auto compute = [&](const St& st, int s) {
+  }
+
+  __device__ __forceinline__ void aim_a(const RowPtr<W4> (&ap)[TL]) {
+#pragma unroll
+    for (int t = 0; t < TL; ++t) {
+      abase[t] = ap[t].a;
+      scbase[t] = ap[t].sc;
+      aoff[t] = ap[t].a_off;
+      scoff[t] = ap[t].sc_off;
+      scoff2[t] = ap[t].sc_off2;
+      shift[t] = ap[t].sc_shift;
+      // Bases in scalar registers, offsets in one vector register each: left
+      // alone, the compiler keeps a 64-bit vector address per load.
+      asm volatile("" : "+s"(abase[t]), "+v"(aoff[t]));
+      if constexpr (W4) asm volatile("" : "+s"(scbase[t]), "+v"(scoff[t]));
+    }
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) {
+      if (d < count) load_a(sa[d], s0 + d * ds);
+    }
+  }
+  __device__ __forceinline__ void aim_b(const uint16_t* b) {
+    bp = b;
+#pragma unroll
+    for (int d = 0; d < (kDeepB ? kDepth : 1); ++d) {
+      if (d < count) load_b(sb[d], s0 + d * ds);
+    }
+  }
+
+  __device__ __forceinline__ void compute(f32x4 (&acc)[TL], const StageA& x, const StageB& y) {
+    const u32x4 minus8 = {T::kMinus8, T::kMinus8, T::kMinus8, T::kMinus8};
     if constexpr (W4) {
 #pragma unroll
-      for (int g = 0; g < St::kG; ++g) {
-        f32x4 sc[TL];
-        u32x4 f[TL][GJ];
+      for (int g = 0; g < kG; ++g) {
+        f32x4 corr = {0, 0, 0, 0}, part[TL];
+#pragma unroll
+        for (int t = 0; t < TL; ++t) part[t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int j = g * GJ; j < (g + 1) * GJ; ++j) {
+          u32x4 f[TL];
+#pragma unroll
+          for (int t = 0; t < TL; ++t) f[t] = decode<T>(x.a[t][0][j]);
+#pragma unroll
+          for (int pl = 0; pl < P; ++pl) {
+            corr = T::mfma(minus8, y.b[pl][j], corr);
+#pragma unroll
+            for (int t = 0; t < TL; ++t) part[t] = T::mfma(f[t], y.b[pl][j], part[t]);
+          }
+        }
 #pragma unroll
         for (int t = 0; t < TL; ++t) {
-          sc[t] = scale_floats<T>(st.sc[t][g]);
+          const f32x4 sc = scale_floats<T>(x.sc[t][g]);
 #pragma unroll
-          for (int i = 0; i < GJ; ++i) f[t][i] = decode<T>(st.a[t][0][g * GJ + i]);
+          for (int r = 0; r < 4; ++r) acc[t][r] = __builtin_fmaf(sc[r], part[t][r] + corr[r], acc[t][r]);
         }
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-          f32x4 corr = {0, 0, 0, 0}, part[TL];
-#pragma unroll
-          for (int t = 0; t < TL; ++t) part[t] = f32x4{0, 0, 0, 0};
-#pragma unroll
-          for (int i = 0; i < GJ; ++i) {
-#pragma unroll
-            for (int pl = 0; pl < P; ++pl) {
-              u32x4 b;
-              if constexpr (kStageB) b = bs[pl][g * GJ + i];
-              else b = load_b(ct, pl, g * GJ + i, s);
-              corr = T::mfma(minus8, b, corr);
-#pragma unroll
-              for (int t = 0; t < TL; ++t) part[t] = T::mfma(f[t][i], b, part[t]);
-            }
-          }
-#pragma unroll
-          for (int t = 0; t < TL; ++t) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              acc[t][ct][r] = __builtin_fmaf(sc[t][r], part[t][r] + corr[r], acc[t][ct][r]);
-          }
-        }
+        // Groups one after another: interleaved they need more registers than there are.
         __builtin_amdgcn_sched_barrier(0);
       }
     } else {
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct) {
+      for (int pl = 0; pl < P; ++pl) {
 #pragma unroll
-        for (int pl = 0; pl < P; ++pl) {
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            u32x4 b;
-            if constexpr (kStageB) b = bs[pl][h];
-            else b = load_b(ct, pl, h, s);
-#pragma unroll
-            for (int t = 0; t < TL; ++t) acc[t][ct] = T::mfma(st.a[t][h], b, acc[t][ct]);
-          }
+          for (int t = 0; t < TL; ++t) acc[t] = T::mfma(x.a[t][h], y.b[pl][h], acc[t]);
         }
       }
     }
-  };
-
-  // The loads of a step go out kDepth steps ahead.  No branch stands between
-  // a load and its use in the main loop: where paths join, the wait for a
-  // load becomes a wait for all of them.
-  const int last = min(s1, full);
-  const int count = s0 < last ? (last - s0 + ds - 1) / ds : 0;
-  if (count > 0) {
-    St st[kDepth];
-#pragma unroll
-    for (int d = 0; d < kDepth; ++d) {
-      if (d < count) load(st[d], s0 + d * ds);
-    }
-    stage_b(s0);
-    int i = 0, s = s0;
-    for (; i + 2 * kDepth <= count; i += kDepth) {
-#pragma unroll
-      for (int d = 0; d < kDepth; ++d) {
-        compute(st[d], s);
-        stage_b(s + ds);
-        load(st[d], s + kDepth * ds);
-        s += ds;
-      }
-    }
-#pragma unroll
-    for (int d = 0; d < 2 * kDepth - 1; ++d) {
-      if (i + d < count) {
-        compute(st[d % kDepth], s);
-        if (i + d + 1 < count) stage_b(s + ds);
-        if (d < kDepth - 1 && i + d + kDepth < count) load(st[d], s + kDepth * ds);
-        s += ds;
-      }
-    }
   }
+
   // The last columns, 32 at a time and element by element where a row ends.
-  if (full < s1 && full >= s0 && (full - s0) % ds == 0) {
+  __device__ __forceinline__ void tail(f32x4 (&acc)[TL]) {
+    const u32x4 minus8 = {T::kMinus8, T::kMinus8, T::kMinus8, T::kMinus8};
     const int q8 = ((threadIdx.x & 63) >> 4) * 8;
 #pragma unroll 1
     for (int j = 0; j < kMac; ++j) {
       const int k = full * kCols + 32 * j;
       if (k >= bend) break;
       u32x4 a[TL];
-      f32x4 sc[TL];
+      f32x4 sc[TL], corr = {0, 0, 0, 0}, part[TL];
 #pragma unroll
       for (int t = 0; t < TL; ++t) {
+        part[t] = f32x4{0, 0, 0, 0};
         if constexpr (W4) {
-          a[t] = decode<T>(*reinterpret_cast<const uint32_t*>(ap[t].a + (int64_t)full * 1024 + ap[t].a_off + 4 * j));
-          sc[t] = scale_floats<T>(load_scales<SHIFT>(scbase[t], scoff[t], ap[t].sc_off2, ap[t].sc_shift, k / (32 * GJ)));
+          a[t] = decode<T>(gload<uint32_t>(abase[t] + (int64_t)full * 1024 + aoff[t] + 4 * j));
+          sc[t] = scale_floats<T>(load_scales<SHIFT>(scbase[t], scoff[t], scoff2[t], shift[t], k / (32 * GJ)));
         } else {
-          a[t] = load8_guarded(reinterpret_cast<const uint16_t*>(ap[t].a + (int64_t)k * 2 + ap[t].a_off), k + q8, kend);
+          a[t] = load8_guarded(abase[t] + (int64_t)k * 2 + aoff[t], k + q8, kend);
         }
       }
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct) {
-        f32x4 corr = {0, 0, 0, 0}, part[TL];
+      for (int pl = 0; pl < P; ++pl) {
+        const u32x4 b = load8_guarded(bp + pl * plane + k, k + q8, bend);
+        if constexpr (W4) corr = T::mfma(minus8, b, corr);
 #pragma unroll
-        for (int t = 0; t < TL; ++t) part[t] = f32x4{0, 0, 0, 0};
+        for (int t = 0; t < TL; ++t) part[t] = T::mfma(a[t], b, part[t]);
+      }
 #pragma unroll
-        for (int pl = 0; pl < P; ++pl) {
-          const u32x4 b = load8_guarded(bp[ct] + pl * plane + k, k + q8, bend);
-          if constexpr (W4) corr = T::mfma(minus8, b, corr);
+      for (int t = 0; t < TL; ++t) {
 #pragma unroll
-          for (int t = 0; t < TL; ++t) part[t] = T::mfma(a[t], b, part[t]);
-        }
-#pragma unroll
-        for (int t = 0; t < TL; ++t) {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            if constexpr (W4) acc[t][ct][r] = __builtin_fmaf(sc[t][r], part[t][r] + corr[r], acc[t][ct][r]);
-            else acc[t][ct][r] += part[t][r];
-          }
+        for (int r = 0; r < 4; ++r) {
+          if constexpr (W4) acc[t][r] = __builtin_fmaf(sc[t][r], part[t][r] + corr[r], acc[t][r]);
+          else acc[t][r] += part[t][r];
         }
       }
     }
   }
-}
+
+  // acc += the product.  The loads that aim_a and aim_b sent are used up.
+  __device__ __forceinline__ void run(f32x4 (&acc)[TL]) {
+    int i = 0, s = s0;
+    for (; i + 2 * kDepth <= count; i += kDepth) {
+#pragma unroll
+      for (int d = 0; d < kDepth; ++d) {
+        compute(acc, sa[d], sb[kDeepB ? d : 0]);
+        if constexpr (!kDeepB) load_b(sb[0], s + ds);
+        load_a(sa[d], s + kDepth * ds);
+        if constexpr (kDeepB) load_b(sb[d], s + kDepth * ds);
+        __builtin_amdgcn_sched_barrier(0);    // loads stay ahead: the scheduler would sink them to their uses
+        s += ds;
+      }
+    }
+#pragma unroll
+    for (int d = 0; d < 2 * kDepth - 1; ++d) {
+      if (i + d < count) {
+        compute(acc, sa[d % kDepth], sb[kDeepB ? d % kDepth : 0]);
+        if constexpr (!kDeepB) {
+          if (i + d + 1 < count) load_b(sb[0], s + ds);
+        }
+        if (d < kDepth - 1 && i + d + kDepth < count) {
+          load_a(sa[d], s + kDepth * ds);
+          if constexpr (kDeepB) load_b(sb[d], s + kDepth * ds);
+        }
+        s += ds;
+      }
+    }
+    if (full < s1 && full >= s0 && (full - s0) % ds == 0) tail(acc);
+  }
+};
 
 constexpr int kThreads = kExpertWaves * 64;
 
-// Block-wide ordered compaction: the position of this thread's item among
-// the items of all threads before it, plus base.  Returns the new total.
-__device__ __forceinline__ int compact(bool have, int base, int* wave_count, int* pos) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const uint64_t m = __ballot(have);
-  if (lane == 0) wave_count[wave] = __popcll(m);
-  __syncthreads();
-  int before = base, total = base;
-#pragma unroll
-  for (int w = 0; w < kExpertWaves; ++w) {
-    const int c = wave_count[w];
-    before += w < wave ? c : 0;
-    total += c;
-  }
-  *pos = before + __popcll(m & ((1ull << lane) - 1));
-  __syncthreads();
-  return total;
-}
-
-__device__ __forceinline__ void store_out(void* out, int64_t i, float v, int f32, uint16_t (*round)(float)) {
+template <class T>
+__device__ __forceinline__ void store_out(void* out, int64_t i, float v, int f32) {
   if (f32) static_cast<float*>(out)[i] = v;
-  else static_cast<uint16_t*>(out)[i] = round(v);
+  else static_cast<uint16_t*>(out)[i] = T::from_float(v);
 }
 
-// A workgroup takes one expert (blockIdx.y) and one tile of 16 output rows
-// (GATED: 16 gate rows and the 16 up rows beside them).  It lists the tokens
-// that chose the expert, in ascending order, and multiplies them 16 CTM at a
-// time.  GATED: silu(gate) * up goes to the workspace in two 16-bit parts
-// (the down product then sees it to 16 bits and more, not rounded to the 8 of
-// a bfloat16), and the tile-0 workgroups leave the plan down_kernel follows.
+// The pairs (token, top-k slot) that name an expert, in ascending order and
+// each token once: list[i] = token << 6 | slot.  Called by a whole workgroup.
+struct Lister {
+  static constexpr int kUnroll = 4;     // loads in flight per thread
+  int count[kUnroll][kExpertWaves];
+  int repeated;                         // a token names the expert twice
+
+  __device__ __forceinline__ int run(const int32_t* ids, int pairs, int top_k, int id, int* list) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    int m = 0;
+    if (tid == 0) repeated = 0;
+    for (int base = 0; base < pairs; base += kThreads * kUnroll) {
+      int v[kUnroll], tok[kUnroll], slot[kUnroll];
+      uint64_t mask[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int p = base + u * kThreads + tid;
+        v[u] = ids[p < pairs ? p : pairs - 1];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int p = base + u * kThreads + tid;
+        bool hit = p < pairs && v[u] == id;
+        mask[u] = __ballot(hit);
+        if (mask[u]) {
+          tok[u] = (int)((uint32_t)p / (uint32_t)top_k);
+          slot[u] = p - tok[u] * top_k;
+          if (hit && slot[u] > 0) {       // an earlier slot of the token: in this wave's lanes, or before them
+            const int here = min(slot[u], lane);
+            bool dup = ((mask[u] >> (lane - here)) & ((1ull << here) - 1)) != 0;
+            for (int i = here + 1; i <= slot[u]; ++i) dup |= ids[p - i] == id;
+            if (dup) repeated = 1;
+            hit = !dup;
+          }
+          mask[u] = __ballot(hit);
+        }
+        if (lane == 0) count[u][wave] = __popcll(mask[u]);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        int before = m;
+#pragma unroll
+        for (int w = 0; w < kExpertWaves; ++w) {
+          const int c = count[u][w];
+          before += w < wave ? c : 0;
+          m += c;
+        }
+        if ((mask[u] >> lane) & 1) list[before + __popcll(mask[u] & ((1ull << lane) - 1))] = tok[u] << 6 | slot[u];
+      }
+    }
+    __syncthreads();
+    return m;
+  }
+};
+
+// One pair as the layer's second kernel reads it.
+struct alignas(8) PairRec {
+  int pair;                             // token << 6 | slot
+  float weight;
+};
+
+// A workgroup takes one expert (blockIdx.y) and a run of tiles of 16 output
+// rows (GATED: 16 gate rows and the 16 up rows beside them), a.split of its
+// waves to a tile.  It lists the tokens that chose the expert and multiplies
+// them 16 at a time.  GATED: silu(gate) * up goes to the workspace in two
+// 16-bit parts (the down product then sees it to 16 bits and more, not
+// rounded to the 8 of a bfloat16), and the first workgroup of an expert
+// leaves the plan down_kernel follows.
 template <class T, int G, bool GATED, bool SHIFT>
 __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const RowsKArgs a) {
   constexpr bool W4 = G != 0;
-  constexpr int GJ = W4 ? G / 32 : 1;
   constexpr int TL = GATED ? 2 : 1;
   __shared__ int list[kPassTokens];
-  __shared__ int wave_count[kExpertWaves];
+  __shared__ Lister lister;
   __shared__ f32x4 red[kExpertWaves][TL][64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int slot = blockIdx.y, tile = blockIdx.x;
-  const int k = a.top_k;
+  const int slot = blockIdx.y, k = a.top_k;
+  const int split = a.split, group = kExpertWaves / split;      // waves to a tile, tiles at once
+  const int part = wave % split, mine = wave / split;
+  const int tiles = (a.inter + 15) >> 4;
+  const int tile0 = blockIdx.x * a.tiles_per_block;
+  const int tile1 = min(tile0 + a.tiles_per_block, tiles);
+
+  Mac<T, G, SHIFT, TL, 1> mac;
+  mac.steps(a.w, a.w.cols, 0, part, (a.w.cols + Step<W4>::kCols - 1) / Step<W4>::kCols, split);
+  int expert = 0;
+  auto aim_a = [&](int tile) {
+    RowPtr<W4> ap[TL];
+    const int at = min(tile, tiles - 1) * 16;
+    ap[0] = row_ptr<W4>(a.w, expert, at);
+    if constexpr (GATED) ap[1] = row_ptr<W4>(a.w, expert, a.inter + at);
+    mac.aim_a(ap);
+  };
 
   // the expert of this slot, and its tokens
-  int m = 0, expert = 0;
+  int m = a.n;
+  bool aimed = false;
   if (a.ids == nullptr) {
-    m = a.n;
     for (int i = tid; i < a.n; i += kThreads) list[i] = i << 6;
     __syncthreads();
   } else {
     const int id = a.by_pair ? a.ids[slot] : a.offset + slot;
     const bool inside = id >= a.offset && (int64_t)id - a.offset < a.num_experts;
-    expert = inside ? id - a.offset : 0;
+    expert = __builtin_amdgcn_readfirstlane(inside ? id - a.offset : 0);
+    m = 0;
     if (inside) {
-      for (int base = 0; base < a.n; base += kThreads) {
-        const int t = base + tid;
-        int first = -1;
-        float weight = 0.0f;
-        if (t < a.n) {
-          for (int j = 0; j < k; ++j) {
-            if (a.ids[(int64_t)t * k + j] == id) {
-              if (first < 0) first = j;
-              if constexpr (GATED) weight += a.topk_weights ? a.topk_weights[(int64_t)t * k + j] : 1.0f;
-            }
-          }
-        }
-        int pos;
-        m = compact(first >= 0, m, wave_count, &pos);
-        if (first >= 0) {
-          list[pos] = t << 6 | first;
-          if constexpr (GATED) {
-            if (tile == 0) {
-              a.plan.pair[(int64_t)slot * a.n + pos] = t << 6 | first;
-              a.plan.weight[(int64_t)slot * a.n + pos] = weight;
-            }
-          }
-        }
+      if (a.by_pair) {      // the first weights are on their way while the tokens are listed
+        aim_a(tile0 + mine);
+        aimed = true;
       }
-      __syncthreads();
+      m = lister.run(a.ids, a.n * k, k, id, list);
       // of the pairs that name the same expert the first one's slot does the work
       if (a.by_pair && (list[0] >> 6) * k + (list[0] & 63) != slot) m = 0;
     }
   }
   if constexpr (GATED) {
-    if (tile == 0) {
-      if (tid == 0) a.plan.expert[slot] = expert;
-      if (tid <= kMaxChunks) {          // the first list entry of each chunk of tokens
+    if (blockIdx.x == 0) {
+      const int chunks = (a.n + kChunkTokens - 1) / kChunkTokens;
+      auto start = [&](int c) {         // the first list entry of chunk c
         int lo = 0, hi = m;
         while (lo < hi) {
           const int mid = (lo + hi) >> 1;
-          if ((list[mid] >> 6) < tid * kChunkTokens) lo = mid + 1;
+          if ((list[mid] >> 6) < c * kChunkTokens) lo = mid + 1;
           else hi = mid;
         }
-        a.plan.off[slot * (kMaxChunks + 1) + tid] = lo;
+        return lo;
+      };
+      if (tid < chunks) {
+        const int o0 = start(tid), o1 = start(tid + 1);
+        a.plan.head[tid * a.plan.slots + slot] = pack_head(o1 - o0, o0, expert);
+      }
+      PairRec* rec = reinterpret_cast<PairRec*>(a.plan.pair) + (int64_t)slot * a.n;
+      for (int i = tid; i < m; i += kThreads) {
+        const int t = list[i] >> 6, j0 = list[i] & 63;
+        float weight = 1.0f;
+        if (a.topk_weights) weight = a.topk_weights[(int64_t)t * k + j0];
+        if (lister.repeated) {
+          for (int j = j0 + 1; j < k; ++j) {
+            if (a.ids[(int64_t)t * k + j] == expert + a.offset)
+              weight += a.topk_weights ? a.topk_weights[(int64_t)t * k + j] : 1.0f;
+          }
+        }
+        rec[i] = PairRec{list[i], weight};
       }
     }
   } else if (a.ids != nullptr && slot == 0) {
     // rows of no expert here: zeros, written by the first slot's workgroups
-    for (int i = tid; i < a.n * 16; i += kThreads) {
-      const int r = i >> 4, col = tile * 16 + (i & 15);
-      const int id = a.ids[r];
-      if ((id < a.offset || (int64_t)id - a.offset >= a.num_experts) && col < a.inter)
-        store_out(a.out, (int64_t)r * a.out_stride + col, 0.0f, a.out_f32, T::from_float);
+    const int c0 = tile0 * 16, width = min(tile1 * 16, a.inter) - c0;
+    for (int i = tid; i < a.n * width; i += kThreads) {
+      const int r = i / width, id = a.ids[r];
+      if (id < a.offset || (int64_t)id - a.offset >= a.num_experts)
+        store_out<T>(a.out, (int64_t)r * a.out_stride + c0 + i % width, 0.0f, a.out_f32);
     }
   }
+  m = __builtin_amdgcn_readfirstlane(m);
   if (m == 0) return;
 
-  const int steps = (a.w.cols + Step<W4>::kCols - 1) / Step<W4>::kCols;
-  RowPtr<W4> ap[TL];
-  expert = __builtin_amdgcn_readfirstlane(expert);
-  ap[0] = row_ptr<W4>(a.w, expert, tile * 16);
-  if constexpr (GATED) ap[1] = row_ptr<W4>(a.w, expert, a.inter + tile * 16);
-
-  auto run = [&](auto ct_c, int c0) {
-    constexpr int CT = decltype(ct_c)::value;
-    const uint16_t* bp[CT];
+  auto aim_b = [&](int c0) {        // columns past the list repeat its last token and are not stored
+    const int i = min(c0 + (lane & 15), m - 1);
+    mac.aim_b(a.x + (int64_t)(list[i] >> 6) * a.x_stride + (lane >> 4) * 8);
+  };
+  if (!aimed) aim_a(tile0 + mine);
+  aim_b(0);
+  for (int t0 = tile0, c0 = 0; t0 < tile1;) {
+    f32x4 acc[TL];
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {   // columns past the list repeat its last token and are not stored
-      const int i = min(c0 + ct * 16 + (lane & 15), m - 1);
-      bp[ct] = a.x + (int64_t)(list[i] >> 6) * a.x_stride + (lane >> 4) * 8;
+    for (int t = 0; t < TL; ++t) acc[t] = f32x4{0, 0, 0, 0};
+    mac.run(acc);
+    // the next product's first loads are on their way while this one is summed
+    int t2 = t0, c2 = c0 + 16;
+    if (c2 >= m) {
+      c2 = 0;
+      t2 += group;
     }
-    f32x4 acc[TL][CT];
-#pragma unroll
-    for (int t = 0; t < TL; ++t) {
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct) acc[t][ct] = f32x4{0, 0, 0, 0};
+    if (t2 < tile1) {
+      aim_a(t2 + mine);
+      aim_b(c2);
     }
-    mac<T, W4, SHIFT, GJ, TL, CT, 1>(acc, a.w, ap, bp, 0, a.w.cols, wave, steps, kExpertWaves);
+    __syncthreads();
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
-      __syncthreads();
+    for (int t = 0; t < TL; ++t) red[wave][t][lane] = acc[t];
+    __syncthreads();
+    const int left = min(m - c0, 16);
+    for (int i = tid; i < group * 256; i += kThreads) {
+      const int g = i >> 8, col = (i >> 4) & 15, row = i & 15, tile = t0 + g;
+      if (col >= left || tile >= tile1) continue;
+      float v[TL];
 #pragma unroll
-      for (int t = 0; t < TL; ++t) red[wave][t][lane] = acc[t][ct];
-      __syncthreads();
-      const int col = tid >> 4, row = tid & 15;
-      const int i = c0 + ct * 16 + col;
-      if (tid < 256 && i < m) {
-        float v[TL];
-#pragma unroll
-        for (int t = 0; t < TL; ++t) {
-          v[t] = 0.0f;
-#pragma unroll
-          for (int w = 0; w < kExpertWaves; ++w) v[t] += red[w][t][(row >> 2) * 16 + col][row & 3];
-        }
-        const int n = tile * 16 + row;
-        const int t = list[i] >> 6;
-        if constexpr (GATED) {
-          // rows past the intermediate size are zeros: the down product reads whole 16-row tiles
-          const float act = n < a.inter ? v[0] / (1.0f + expf(-v[0])) * v[TL - 1] : 0.0f;
-          const int64_t at = ((int64_t)t * k + (list[i] & 63)) * a.plan.act_stride + n;
-          uint16_t hi, lo;
-          T::split(act, &hi, &lo);
-          a.plan.act[at] = hi;
-          a.plan.act[a.plan.act_plane + at] = lo;
-        } else if (n < a.inter) {
-          store_out(a.out, (int64_t)t * a.out_stride + n, v[0], a.out_f32, T::from_float);
-        }
+      for (int t = 0; t < TL; ++t) {
+        v[t] = 0.0f;
+        for (int w = 0; w < split; ++w) v[t] += red[g * split + w][t][(row >> 2) * 16 + col][row & 3];
+      }
+      const int n = tile * 16 + row, at = list[c0 + col], token = at >> 6;
+      if constexpr (GATED) {
+        // rows past the intermediate size are zeros: the down product reads whole 16-row tiles
+        const float act = n < a.inter ? v[0] / (1.0f + expf(-v[0])) * v[TL - 1] : 0.0f;
+        const int64_t o = ((int64_t)token * k + (at & 63)) * a.plan.act_stride + n;
+        uint16_t hi, lo;
+        T::split(act, &hi, &lo);
+        a.plan.act[o] = hi;
+        a.plan.act[a.plan.act_plane + o] = lo;
+      } else if (n < a.inter) {
+        store_out<T>(a.out, (int64_t)token * a.out_stride + n, v[0], a.out_f32);
       }
     }
-  };
-  for (int c0 = 0; c0 < m; c0 += 16) run(std::integral_constant<int, 1>{}, c0);
+    t0 = t2;
+    c0 = c2;
+  }
 }
 
 // A workgroup takes one tile of 16 output columns and one chunk of up to 128
@@ -822,8 +571,8 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const RowsKArgs a) {
 template <class T, int G>
 __global__ void __launch_bounds__(kThreads, 4) down_kernel(const DownKArgs a) {
   constexpr bool W4 = G != 0;
-  constexpr int GJ = W4 ? G / 32 : 1;
-  __shared__ int slots[MOE_EP_MAX_EXPERTS];
+  __shared__ int heads[MOE_EP_MAX_EXPERTS];
+  __shared__ short slots[MOE_EP_MAX_EXPERTS];
   __shared__ int wave_count[kExpertWaves];
   extern __shared__ __attribute__((aligned(16))) float sums[];   // [wave][token of the chunk][16]
   const int tid = threadIdx.x, lane = tid & 63;
@@ -837,67 +586,87 @@ __global__ void __launch_bounds__(kThreads, 4) down_kernel(const DownKArgs a) {
   const int nc = min(a.n - t0, kChunkTokens);
   const PlanK& p = a.plan;
 
-  int used = 0;
+  int used = 0;                     // slots with tokens in this chunk
   for (int base = 0; base < p.slots; base += kThreads) {
     const int s = base + tid;
-    bool have = false;
-    if (s < p.slots) {
-      const int* off = p.off + s * (kMaxChunks + 1) + chunk;
-      have = off[1] > off[0];
+    const int head = s < p.slots ? p.head[chunk * p.slots + s] : 0;
+    const bool have = head_count(head) > 0;
+    const uint64_t mask = __ballot(have);
+    if (base) __syncthreads();
+    if (lane == 0) wave_count[wave] = __popcll(mask);
+    __syncthreads();
+    int pos = used + __popcll(mask & ((1ull << lane) - 1));
+#pragma unroll
+    for (int w = 0; w < kExpertWaves; ++w) {
+      const int c = wave_count[w];
+      pos += w < wave ? c : 0;
+      used += c;
     }
-    int pos;
-    used = compact(have, used, wave_count, &pos);
-    if (have) slots[pos] = s;
+    if (have) {
+      heads[pos] = head;
+      slots[pos] = (short)s;
+    }
   }
   for (int i = tid; i < kExpertWaves * nc * 16; i += kThreads) sums[i] = 0.0f;
   __syncthreads();
 
+  used = __builtin_amdgcn_readfirstlane(used);
   float* mine = sums + wave * nc * 16;
   const int steps = (a.w.cols + Step<W4>::kCols - 1) / Step<W4>::kCols;
   const int64_t all = (int64_t)used * steps;
-  int64_t s = all * wave / kExpertWaves;
-  const int64_t end = all * (wave + 1) / kExpertWaves;
-  while (s < end) {
-    const int slot = __builtin_amdgcn_readfirstlane(slots[s / steps]);
-    const int k0 = (int)(s % steps);
-    const int k1 = (int)min((int64_t)steps, k0 + (end - s));
-    s += k1 - k0;
-    const int expert = __builtin_amdgcn_readfirstlane(p.expert[slot]);
-    const int* off = p.off + slot * (kMaxChunks + 1) + chunk;
-    const int o0 = __builtin_amdgcn_readfirstlane(off[0]);
-    const int m = __builtin_amdgcn_readfirstlane(off[1]) - o0;
-    const int64_t at = (int64_t)slot * a.n + o0;
-    RowPtr<W4> ap[1] = {row_ptr<W4>(a.w, expert, tile * 16)};
-    auto run = [&](auto ct_c, int c0) {
-      constexpr int CT = decltype(ct_c)::value;
-      const uint16_t* bp[CT];
-      int tok[CT];
-      float weight[CT];
+  int s = (int)(all * wave / kExpertWaves);
+  const int end = (int)(all * (wave + 1) / kExpertWaves);
+
+  // One product of the run: an expert's k steps [k0, k1) with 16 of its tokens.
+  struct Item {
+    int expert, k0, k1, left;
+    PairRec rec;
+  };
+  int col0 = 0;
+  auto next = [&](Item& it) -> bool {
+    if (s >= end) return false;
+    const int i = s / steps;
+    const int head = __builtin_amdgcn_readfirstlane(heads[i]), slot = __builtin_amdgcn_readfirstlane((int)slots[i]);
+    const int m = head_count(head);
+    it.expert = head_expert(head);
+    it.k0 = s - i * steps;
+    it.k1 = min(steps, it.k0 + end - s);
+    it.left = m - col0;
+    const int at = head_start(head) + min(col0 + (lane & 15), m - 1);
+    const u32x2 rec = gload<u32x2>(static_cast<const PairRec*>(p.pair) + (int64_t)slot * a.n + at);
+    it.rec = PairRec{(int)rec[0], __uint_as_float(rec[1])};
+    col0 += 16;
+    if (col0 >= m) {
+      col0 = 0;
+      s += it.k1 - it.k0;
+    }
+    return true;
+  };
+  Mac<T, G, false, 1, 2> mac;
+  auto aim = [&](const Item& it) {
+    mac.steps(a.w, p.act_stride, p.act_plane, it.k0, it.k1, 1);
+    const RowPtr<W4> ap[1] = {row_ptr<W4>(a.w, it.expert, tile * 16)};
+    mac.aim_a(ap);
+    mac.aim_b(p.act + ((int64_t)(it.rec.pair >> 6) * a.top_k + (it.rec.pair & 63)) * p.act_stride + (lane >> 4) * 8);
+  };
+  Item cur;
+  bool have = next(cur);
+  if (have) aim(cur);
+  while (have) {
+    Item after;
+    const bool more = next(after);
+    f32x4 acc[1] = {{0, 0, 0, 0}};
+    mac.run(acc);
+    if (more) aim(after);
+    if ((lane & 15) < cur.left) {
+      f32x4* o = reinterpret_cast<f32x4*>(mine + ((cur.rec.pair >> 6) - t0) * 16 + (lane >> 4) * 4);
+      f32x4 v = *o;
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct) {
-        const int col = c0 + ct * 16 + (lane & 15);
-        const int i = min(col, m - 1);
-        const int pair = p.pair[at + i];
-        weight[ct] = p.weight[at + i];
-        tok[ct] = col < m ? (pair >> 6) - t0 : -1;
-        bp[ct] = p.act + ((int64_t)(pair >> 6) * a.top_k + (pair & 63)) * p.act_stride + (lane >> 4) * 8;
-      }
-      f32x4 acc[1][CT];
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct) acc[0][ct] = f32x4{0, 0, 0, 0};
-      mac<T, W4, false, GJ, 1, CT, 2>(acc, a.w, ap, bp, p.act_plane, p.act_stride, k0, k1, 1);
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct) {
-        if (tok[ct] >= 0) {
-          f32x4* o = reinterpret_cast<f32x4*>(mine + tok[ct] * 16 + (lane >> 4) * 4);
-          f32x4 v = *o;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) v[r] += weight[ct] * acc[0][ct][r];
-          *o = v;
-        }
-      }
-    };
-    for (int c0 = 0; c0 < m; c0 += 16) run(std::integral_constant<int, 1>{}, c0);
+      for (int r = 0; r < 4; ++r) v[r] += cur.rec.weight * acc[0][r];
+      *o = v;
+    }
+    cur = after;
+    have = more;
   }
   __syncthreads();
   for (int i = tid; i < nc * 16; i += kThreads) {
@@ -906,14 +675,19 @@ __global__ void __launch_bounds__(kThreads, 4) down_kernel(const DownKArgs a) {
     float v = 0.0f;
 #pragma unroll
     for (int w = 0; w < kExpertWaves; ++w) v += sums[w * nc * 16 + i];
-    store_out(a.out, (int64_t)(t0 + (i >> 4)) * a.out_stride + col, v, a.out_f32, T::from_float);
+    store_out<T>(a.out, (int64_t)(t0 + (i >> 4)) * a.out_stride + col, v, a.out_f32);
   }
 }
 
+// ---- launches ---------------------------------------------------------------
+
 template <class T, int G, bool GATED>
-void start_rows(const RowsKArgs& a, hipStream_t stream) {
+void start_rows(RowsKArgs a, hipStream_t stream) {
   const int slots = a.ids == nullptr ? 1 : a.by_pair ? a.n * a.top_k : a.num_experts;
-  const dim3 grid((a.inter + 15) / 16, slots);
+  const int tiles = (a.inter + 15) / 16;
+  a.split = kExpertWaves;
+  a.tiles_per_block = 1;
+  const dim3 grid((tiles + a.tiles_per_block - 1) / a.tiles_per_block, slots);
   if constexpr (GATED && G != 0) {
     if (a.inter % 4 != 0) {               // the up rows' scales straddle their groups of four
       rows_kernel<T, G, GATED, true><<<grid, kThreads, 0, stream>>>(a);
@@ -953,27 +727,7 @@ hipError_t start_down(const DownKArgs& a, int group, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <typename V, int LPT, bool GROUPS>
-void start_route(const RouteKArgs& a, hipStream_t stream) {
-  constexpr int kPerBlock = kRouteThreads / 64 * (64 / LPT);
-  const int grid = (int)(((int64_t)a.n + kPerBlock - 1) / kPerBlock);
-  const size_t lds = GROUPS ? (size_t)(kRouteThreads / 64) * (a.num_experts + a.num_groups) * sizeof(double) : 0;
-  const int vpl = (a.num_experts + LPT - 1) / LPT;
-  if (vpl <= 1) route_kernel<V, LPT, 1, GROUPS><<<grid, kRouteThreads, lds, stream>>>(a);
-  else if (vpl <= 2) route_kernel<V, LPT, 2, GROUPS><<<grid, kRouteThreads, lds, stream>>>(a);
-  else if (vpl <= 4) route_kernel<V, LPT, 4, GROUPS><<<grid, kRouteThreads, lds, stream>>>(a);
-  else if (vpl <= 8) route_kernel<V, LPT, 8, GROUPS><<<grid, kRouteThreads, lds, stream>>>(a);
-  else route_kernel<V, LPT, 16, GROUPS><<<grid, kRouteThreads, lds, stream>>>(a);
-}
-
 }  // namespace
-
-hipError_t launch_route(const RouteKArgs& a, hipStream_t stream) {
-  if (a.num_groups > 1) start_route<double, 64, true>(a, stream);
-  else if (a.bias) start_route<double, 64, false>(a, stream);
-  else start_route<float, 64, false>(a, stream);
-  return hipGetLastError();
-}
 
 hipError_t launch_expert_linear(const RowsKArgs& a, int dtype, int group, hipStream_t stream) {
   return dtype == MOE_EP_BF16 ? start_rows<BF16, false>(a, group, stream) : start_rows<F16, false>(a, group, stream);
