@@ -163,6 +163,8 @@ int check_experts(int num_experts, int offset) {
 // Largest matrix side: row and column indexes (and two rows of tiles past
 // them) are 32-bit in the kernels, offsets 64-bit.
 constexpr int32_t kMaxSide = 1 << 24;
+// Fewest elements of a row that the kernels read eight at a time.
+constexpr int32_t kMinRow = 8;
 
 // Workspace of one pass: [ids][weights] with a router, the plan, the
 // activations.  Every part starts on 256 bytes.
@@ -178,8 +180,9 @@ int make_space(const moe_ep_layer_args* a, LayerSpace* s) {
   if (a->num_tokens < 0) return report(MOE_EP_ERR_INVALID_ARG, "num_tokens %d < 0", a->num_tokens);
   if (a->top_k < 1 || a->top_k > MOE_EP_MAX_TOPK)
     return report(MOE_EP_ERR_INVALID_ARG, "top_k %d outside [1, %d]", a->top_k, MOE_EP_MAX_TOPK);
-  if (a->intermediate_size < 1 || a->intermediate_size > kMaxSide)
-    return report(MOE_EP_ERR_INVALID_ARG, "intermediate_size %d outside [1, %d]", a->intermediate_size, kMaxSide);
+  if (a->intermediate_size < kMinRow || a->intermediate_size > kMaxSide)
+    return report(MOE_EP_ERR_INVALID_ARG, "intermediate_size %d outside [%d, %d]", a->intermediate_size, kMinRow,
+                  kMaxSide);
   s->n = std::min(a->num_tokens, kPassTokens);
   const int64_t pairs = (int64_t)s->n * a->top_k;
   s->by_pair = pairs <= a->num_experts;
@@ -231,9 +234,10 @@ int moe_ep_expert_linear(const moe_ep_linear_args* a, void* stream) {
   if (st == MOE_EP_OK) st = check_experts(a->num_experts, a->expert_offset);
   if (st != MOE_EP_OK) return st;
   if (a->num_rows < 0) return report(MOE_EP_ERR_INVALID_ARG, "num_rows %d < 0", a->num_rows);
-  if (a->in_features < 1 || a->in_features > kMaxSide || a->out_features < 1 || a->out_features > kMaxSide)
-    return report(MOE_EP_ERR_INVALID_ARG, "in_features %d or out_features %d outside [1, %d]", a->in_features,
-                  a->out_features, kMaxSide);
+  if (a->in_features < kMinRow || a->in_features > kMaxSide)
+    return report(MOE_EP_ERR_INVALID_ARG, "in_features %d outside [%d, %d]", a->in_features, kMinRow, kMaxSide);
+  if (a->out_features < 1 || a->out_features > kMaxSide)
+    return report(MOE_EP_ERR_INVALID_ARG, "out_features %d outside [1, %d]", a->out_features, kMaxSide);
   const int out_esz = elem_bytes(a->out_dtype);
   st = check_rows("x", a->x, a->x_stride, a->in_features, a->num_rows, 2, true);
   if (st == MOE_EP_OK) st = check_rows("out", a->out, a->out_stride, a->out_features, a->num_rows, out_esz, false);
@@ -283,8 +287,8 @@ int moe_ep_layer(const moe_ep_layer_args* a, void* stream) {
   st = make_space(a, &s);
   if (st != MOE_EP_OK) return st;
   const int n = a->num_tokens;
-  if (a->hidden_size < 1 || a->hidden_size > kMaxSide)
-    return report(MOE_EP_ERR_INVALID_ARG, "hidden_size %d outside [1, %d]", a->hidden_size, kMaxSide);
+  if (a->hidden_size < kMinRow || a->hidden_size > kMaxSide)
+    return report(MOE_EP_ERR_INVALID_ARG, "hidden_size %d outside [%d, %d]", a->hidden_size, kMinRow, kMaxSide);
   const int out_esz = elem_bytes(a->out_dtype);
   st = check_rows("hidden", a->hidden, a->hidden_stride, a->hidden_size, n, 2, true);
   if (st == MOE_EP_OK) st = check_rows("out", a->out, a->out_stride, a->hidden_size, n, out_esz, false);

@@ -43,21 +43,22 @@ struct __attribute__((packed, aligned(2))) Elems8 {
 __device__ __forceinline__ u32x4 load8(const void* p) {
   return reinterpret_cast<const __attribute__((address_space(1))) Elems8*>(reinterpret_cast<uintptr_t>(p))->v;
 }
-// The same where only elements k < end of a row exist: zeros beyond.
-__device__ __forceinline__ u32x4 load8_guarded(const void* p, int k, int end) {
-  if (k + 8 <= end) return load8(p);
-  u32x4 v = {0, 0, 0, 0};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (k + i < end) v[i >> 1] |= (uint32_t)static_cast<const uint16_t*>(p)[i] << (16 * (i & 1));
-  }
-  return v;
+// Eight elements of a row of which only `have` exist (none: <= 0).  v was
+// loaded so as to end with the row: the existing ones are its last.
+__device__ __forceinline__ u32x4 cut8(const u32x4& v, int have) {
+  typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
+  const u64x2 w = __builtin_bit_cast(u64x2, v);
+  const int gone = 16 * (8 - max(min(have, 8), 0));     // bits
+  u64x2 r;
+  r[0] = gone == 0 ? w[0] : gone < 64 ? w[0] >> gone | w[1] << (64 - gone) : gone < 128 ? w[1] >> (gone - 64) : 0;
+  r[1] = gone < 64 ? w[1] >> gone : 0;
+  return __builtin_bit_cast(u32x4, r);
 }
 
-// How many columns (k) a step covers, and matrix instructions per step.
+// How many columns (k) a step covers.
 template <bool W4> struct Step;
-template <> struct Step<false> { static constexpr int kCols = 64, kMac = 2; };
-template <> struct Step<true> { static constexpr int kCols = 128, kMac = 4; };
+template <> struct Step<false> { static constexpr int kCols = 64; };
+template <> struct Step<true> { static constexpr int kCols = 128; };
 
 // Where a wave finds 16 weight rows that start at row `first`: bases that are
 // the same for all lanes (kept in scalar registers) and each lane's 32-bit
@@ -129,81 +130,111 @@ __device__ __forceinline__ u32x4 decode(uint32_t w) {
                T::template nibbles<true>(hi)};
 }
 
-// One wave's product of TL tiles of 16 weight rows with 16 columns of B over
-// the steps s0, s0 + ds, ... below s1.  P planes of B (high, low part) are
-// `plane` elements apart.
+// One wave's products of TL tiles of 16 weight rows with up to kCols columns
+// of B, one item after another.  An item is count steps s0, s0 + ds, ...; P
+// planes of B (high, low part) are `plane` elements apart.
 //
-// aim_a / aim_b set the operands and send out the first kDepth steps' loads;
-// run() goes through the steps, each step's loads kDepth steps ahead.  Loads
-// return in the order they were sent, so A and B of a step go out together:
-// were B sent later, the wait for it would be a wait for all of A's loads
-// before it.  For the same reason no branch stands between a load and its use
-// in the main loop: where paths join, the wait for a load becomes a wait for
-// all.
-template <class T, int G, bool SHIFT, int TL, int P>
+// aim() points the loads at an item, prime() sends out its first kDepth
+// steps' loads, run() goes through the steps, each step's loads kDepth steps
+// ahead, and in its last steps sends out the next item's, so that the stream
+// of weights never stops.  Loads return in the order they were sent, so A and
+// B of a step go out together: were B sent later, the wait for it would be a
+// wait for all of A's loads before it.  For the same reason no branch with a
+// load stands between a load and its use: where paths join, the wait for a
+// load becomes a wait for all.
+//
+// Only kCols of the matrix instruction's 16 columns are loaded, one 16-byte
+// load a lane: as operands they would hold four times the registers, and the
+// weights' prefetch needs those.  At its use a step of B goes through the
+// wave's own piece of LDS, which hands it out as operands; the lanes of the
+// columns beyond repeat the last one and are not stored.
+//
+// CUT: rows end inside a step.
+template <class T, int G, bool SHIFT, bool CUT, int TL, int P>
 struct Mac {
   static constexpr bool W4 = G != 0;
   static constexpr int GJ = W4 ? G / 32 : 1;              // matrix instructions per scale group
   static constexpr int kG = W4 ? 4 / GJ : 1;              // scale groups per step
-  static constexpr int kCols = Step<W4>::kCols, kMac = Step<W4>::kMac;
-  // What 128 registers hold: B is staged as deep as A, or one step deep.
-  static constexpr int kARegs = W4 ? TL * (4 + 2 * kG) : TL * 8, kBRegs = P * kMac * 4;
-  static constexpr bool kDeepB = kARegs + kBRegs <= 32;
-  static constexpr int kDepth = !kDeepB ? 2 : kARegs + kBRegs <= 18 ? 4 : kARegs + kBRegs <= 26 ? 3 : 2;
+  static constexpr int kStep = Step<W4>::kCols;
+  static constexpr int kUnits = kStep / 8;                // 16-byte units of a column in a step
+  static constexpr int kCols = 64 / kUnits;               // columns of a pass: 4 (4-bit) or 8 (dense)
+  static constexpr int kPitch = P * kUnits * 16 + 16;     // bytes from column to column in LDS
+  static constexpr int kLds = kCols * kPitch;             // a wave's piece
+  static constexpr int kStageRegs = (W4 ? TL * (4 + 2 * kG) : TL * 8) + P * 4;
+  static constexpr int kDepth = TL == 2 ? (W4 ? 2 : 3) : 64 / kStageRegs;   // within 128 registers
 
-  struct StageA {
+  struct Stage {
     u32x4 a[TL][W4 ? 1 : 2];
     u32x2 sc[W4 ? TL : 1][kG];
+    u32x4 b[P];
   };
-  struct StageB {
-    u32x4 b[P][kMac];
+  struct Item {
+    int s0, ds, count;
   };
-  StageA sa[kDepth];
-  StageB sb[kDeepB ? kDepth : 1];
+  Stage st[kDepth];
   const uint8_t* abase[TL];
   const uint16_t* scbase[TL];
   uint32_t aoff[TL], scoff[TL], scoff2[TL];
   int shift[TL];
-  const uint16_t* bp;
+  const uint16_t* bp;         // B's row of column load_col()
   int64_t plane;
-  int kend, bend, full, s0, s1, ds, count;
+  char* lds_write;
+  const char* lds_read;
+  int unit8, q8;              // the lane's first element in a step's column, as loaded and as operand
+  int kend, bend, full;
 
-  __device__ __forceinline__ void steps(const WeightK& w, int bend_, int64_t plane_, int s0_, int s1_, int ds_) {
+  // lds: the wave's piece.  bend: columns of B's rows.
+  __device__ __forceinline__ void init(char* lds, const WeightK& w, int bend_, int64_t plane_) {
+    const int lane = threadIdx.x & 63;
+    lds_write = lds + (lane / kUnits) * kPitch + (lane % kUnits) * 16;
+    lds_read = lds + min(lane & 15, kCols - 1) * kPitch + (lane >> 4) * 16;
+    unit8 = lane % kUnits * 8;
+    q8 = (lane >> 4) * 8;
     kend = w.cols;
     bend = bend_;
     plane = plane_;
-    s0 = s0_;
-    s1 = s1_;
-    ds = ds_;
-    // Steps with no column past an end of either row; at most one step follows.
-    full = (W4 ? bend : (kend < bend ? kend : bend)) / kCols;
-    const int last = min(s1, full);
-    count = s0 < last ? (last - s0 + ds - 1) / ds : 0;
+    // steps with no column past an end of either row; at most one step follows
+    full = (W4 ? bend : min(kend, bend)) / kStep;
   }
+  __device__ __forceinline__ Item item(int s0, int s1, int ds) const {
+    // one without steps still loads: step 0
+    return s0 < s1 ? Item{s0, ds, (s1 - s0 + ds - 1) / ds} : Item{0, 0, 0};
+  }
+  // The column whose row this lane loads.
+  static __device__ __forceinline__ int load_col() { return (threadIdx.x & 63) / kUnits; }
 
-  __device__ __forceinline__ void load_a(StageA& x, int s) {
+  __device__ __forceinline__ void load(Stage& x, int s) {
+    // Past the end of a row: its last eight elements (there are eight);
+    // compute() cuts them.
+    const int k = CUT ? min(s * kStep + unit8, bend - 8) : s * kStep + unit8;
+#pragma unroll
+    for (int pl = 0; pl < P; ++pl) x.b[pl] = load8(bp + pl * plane + k);
 #pragma unroll
     for (int t = 0; t < TL; ++t) {
       if constexpr (W4) {
         x.a[t][0] = gload<u32x4>(abase[t] + (int64_t)s * 1024 + aoff[t]);
 #pragma unroll
-        for (int g = 0; g < kG; ++g)
-          x.sc[t][g] = load_scales<SHIFT>(scbase[t], scoff[t], scoff2[t], shift[t], s * kG + g);
+        for (int g = 0; g < kG; ++g) {          // past the end the last group's scale: it meets zeros of B
+          const int group = CUT ? min(s * kG + g, (kend - 1) / (32 * GJ)) : s * kG + g;
+          x.sc[t][g] = load_scales<SHIFT>(scbase[t], scoff[t], scoff2[t], shift[t], group);
+        }
       } else {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) x.a[t][h] = load8(abase[t] + ((int64_t)s * kCols + 32 * h) * 2 + aoff[t]);
+        for (int h = 0; h < 2; ++h) {
+          const int at = s * kStep + 32 * h;
+          if constexpr (CUT) {
+            const int back = max(at + q8 + 8 - kend, 0);
+            x.a[t][h] = load8(abase[t] + (int64_t)at * 2 + (int32_t)(aoff[t] - back * 2));
+          } else {
+            x.a[t][h] = load8(abase[t] + (int64_t)at * 2 + aoff[t]);
+          }
+        }
       }
     }
   }
-  __device__ __forceinline__ void load_b(StageB& x, int s) {
-#pragma unroll
-    for (int pl = 0; pl < P; ++pl) {
-#pragma unroll
-      for (int j = 0; j < kMac; ++j) x.b[pl][j] = load8(bp + pl * plane + (int64_t)s * kCols + 32 * j);
-    }
-  }
 
-  __device__ __forceinline__ void aim_a(const RowPtr<W4> (&ap)[TL]) {
+  __device__ __forceinline__ void aim(const RowPtr<W4> (&ap)[TL], const uint16_t* row) {
+    bp = row;
 #pragma unroll
     for (int t = 0; t < TL; ++t) {
       abase[t] = ap[t].a;
@@ -217,21 +248,45 @@ struct Mac {
       asm volatile("" : "+s"(abase[t]), "+v"(aoff[t]));
       if constexpr (W4) asm volatile("" : "+s"(scbase[t]), "+v"(scoff[t]));
     }
+    asm volatile("" : "+v"(unit8), "+v"(bp));
+  }
+  // s, with nothing computed from it kept across the caller's loop.
+  static __device__ __forceinline__ int unhoisted(int s) {
+    asm volatile("" : "+s"(s));
+    return s;
+  }
+  __device__ __forceinline__ void prime(const Item& it) {
+    const int first = unhoisted(it.s0), last = max(it.count - 1, 0);
 #pragma unroll
     for (int d = 0; d < kDepth; ++d) {
-      if (d < count) load_a(sa[d], s0 + d * ds);
-    }
-  }
-  __device__ __forceinline__ void aim_b(const uint16_t* b) {
-    bp = b;
-#pragma unroll
-    for (int d = 0; d < (kDeepB ? kDepth : 1); ++d) {
-      if (d < count) load_b(sb[d], s0 + d * ds);
+      load(st[d], first + min(d, last) * it.ds);
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
 
-  __device__ __forceinline__ void compute(f32x4 (&acc)[TL], const StageA& x, const StageB& y) {
+  __device__ __forceinline__ void store_b(const u32x4 (&b)[P]) {
+#pragma unroll
+    for (int pl = 0; pl < P; ++pl) *reinterpret_cast<u32x4*>(lds_write + pl * kUnits * 16) = b[pl];
+    // The wave's lanes read what its other lanes wrote: LDS operations of one
+    // wave keep their order, the compiler has to as well.
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  }
+  __device__ __forceinline__ u32x4 operand_b(int pl, int j) const {
+    return *reinterpret_cast<const u32x4*>(lds_read + pl * kUnits * 16 + j * 64);
+  }
+
+  __device__ __forceinline__ void compute(f32x4 (&acc)[TL], const Stage& x, int s) {
     const u32x4 minus8 = {T::kMinus8, T::kMinus8, T::kMinus8, T::kMinus8};
+    if (!CUT || s < full) {
+      store_b(x.b);
+    } else {
+      u32x4 b[P];
+#pragma unroll
+      for (int pl = 0; pl < P; ++pl) b[pl] = cut8(x.b[pl], bend - s * kStep - unit8);
+      store_b(b);
+    }
     if constexpr (W4) {
 #pragma unroll
       for (int g = 0; g < kG; ++g) {
@@ -245,9 +300,10 @@ struct Mac {
           for (int t = 0; t < TL; ++t) f[t] = decode<T>(x.a[t][0][j]);
 #pragma unroll
           for (int pl = 0; pl < P; ++pl) {
-            corr = T::mfma(minus8, y.b[pl][j], corr);
+            const u32x4 b = operand_b(pl, j);
+            corr = T::mfma(minus8, b, corr);
 #pragma unroll
-            for (int t = 0; t < TL; ++t) part[t] = T::mfma(f[t], y.b[pl][j], part[t]);
+            for (int t = 0; t < TL; ++t) part[t] = T::mfma(f[t], b, part[t]);
           }
         }
 #pragma unroll
@@ -257,87 +313,58 @@ struct Mac {
           for (int r = 0; r < 4; ++r) acc[t][r] = __builtin_fmaf(sc[r], part[t][r] + corr[r], acc[t][r]);
         }
         // Groups one after another: interleaved they need more registers than there are.
-        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (kG > 1) __builtin_amdgcn_sched_barrier(0);
       }
     } else {
 #pragma unroll
       for (int pl = 0; pl < P; ++pl) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+          const u32x4 b = operand_b(pl, h);
+          if (!CUT || s < full) {
 #pragma unroll
-          for (int t = 0; t < TL; ++t) acc[t] = T::mfma(x.a[t][h], y.b[pl][h], acc[t]);
+            for (int t = 0; t < TL; ++t) acc[t] = T::mfma(x.a[t][h], b, acc[t]);
+          } else {
+#pragma unroll
+            for (int t = 0; t < TL; ++t)
+              acc[t] = T::mfma(cut8(x.a[t][h], kend - s * kStep - 32 * h - q8), b, acc[t]);
+          }
         }
       }
     }
+    __builtin_amdgcn_wave_barrier();
   }
 
-  // The last columns, 32 at a time and element by element where a row ends.
-  __device__ __forceinline__ void tail(f32x4 (&acc)[TL]) {
-    const u32x4 minus8 = {T::kMinus8, T::kMinus8, T::kMinus8, T::kMinus8};
-    const int q8 = ((threadIdx.x & 63) >> 4) * 8;
-#pragma unroll 1
-    for (int j = 0; j < kMac; ++j) {
-      const int k = full * kCols + 32 * j;
-      if (k >= bend) break;
-      u32x4 a[TL];
-      f32x4 sc[TL], corr = {0, 0, 0, 0}, part[TL];
-#pragma unroll
-      for (int t = 0; t < TL; ++t) {
-        part[t] = f32x4{0, 0, 0, 0};
-        if constexpr (W4) {
-          a[t] = decode<T>(gload<uint32_t>(abase[t] + (int64_t)full * 1024 + aoff[t] + 4 * j));
-          sc[t] = scale_floats<T>(load_scales<SHIFT>(scbase[t], scoff[t], scoff2[t], shift[t], k / (32 * GJ)));
-        } else {
-          a[t] = load8_guarded(abase[t] + (int64_t)k * 2 + aoff[t], k + q8, kend);
-        }
-      }
-#pragma unroll
-      for (int pl = 0; pl < P; ++pl) {
-        const u32x4 b = load8_guarded(bp + pl * plane + k, k + q8, bend);
-        if constexpr (W4) corr = T::mfma(minus8, b, corr);
-#pragma unroll
-        for (int t = 0; t < TL; ++t) part[t] = T::mfma(a[t], b, part[t]);
-      }
-#pragma unroll
-      for (int t = 0; t < TL; ++t) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          if constexpr (W4) acc[t][r] = __builtin_fmaf(sc[t][r], part[t][r] + corr[r], acc[t][r]);
-          else acc[t][r] += part[t][r];
-        }
-      }
-    }
-  }
-
-  // acc += the product.  The loads that aim_a and aim_b sent are used up.
-  __device__ __forceinline__ void run(f32x4 (&acc)[TL]) {
-    int i = 0, s = s0;
-    for (; i + 2 * kDepth <= count; i += kDepth) {
+  // acc += the item that was aimed at and primed.  aim_next(): points the
+  // loads at the next item and returns it; called once if more is set.
+  template <class F>
+  __device__ __forceinline__ void run(f32x4 (&acc)[TL], const Item& it, bool more, F aim_next) {
+    int i = 0;
+    const int s0 = it.s0;
+    for (; i + kDepth < it.count; i += kDepth) {
 #pragma unroll
       for (int d = 0; d < kDepth; ++d) {
-        compute(acc, sa[d], sb[kDeepB ? d : 0]);
-        if constexpr (!kDeepB) load_b(sb[0], s + ds);
-        load_a(sa[d], s + kDepth * ds);
-        if constexpr (kDeepB) load_b(sb[d], s + kDepth * ds);
+        compute(acc, st[d], s0 + (i + d) * it.ds);
+        load(st[d], s0 + min(i + d + kDepth, it.count - 1) * it.ds);
         __builtin_amdgcn_sched_barrier(0);    // loads stay ahead: the scheduler would sink them to their uses
-        s += ds;
       }
     }
+    if (more) {
+      const Item nx = aim_next();
+      const int first = unhoisted(nx.s0), last = max(nx.count - 1, 0);
 #pragma unroll
-    for (int d = 0; d < 2 * kDepth - 1; ++d) {
-      if (i + d < count) {
-        compute(acc, sa[d % kDepth], sb[kDeepB ? d % kDepth : 0]);
-        if constexpr (!kDeepB) {
-          if (i + d + 1 < count) load_b(sb[0], s + ds);
-        }
-        if (d < kDepth - 1 && i + d + kDepth < count) {
-          load_a(sa[d], s + kDepth * ds);
-          if constexpr (kDeepB) load_b(sb[d], s + kDepth * ds);
-        }
-        s += ds;
+      for (int d = 0; d < kDepth; ++d) {
+        if (i + d < it.count) compute(acc, st[d], s0 + (i + d) * it.ds);
+        load(st[d], first + min(d, last) * nx.ds);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    } else {
+#pragma unroll
+      for (int d = 0; d < kDepth; ++d) {
+        if (i + d < it.count) compute(acc, st[d], s0 + (i + d) * it.ds);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
-    if (full < s1 && full >= s0 && (full - s0) % ds == 0) tail(acc);
   }
 };
 
@@ -355,6 +382,23 @@ struct Lister {
   static constexpr int kUnroll = 4;     // loads in flight per thread
   int count[kUnroll][kExpertWaves];
   int repeated;                         // a token names the expert twice
+
+  // At most 64 pairs, whose ids each wave holds one a lane: every wave lists
+  // them for itself (they all write the same list).
+  __device__ __forceinline__ int run_few(int v, int pairs, int top_k, int id, int* list) {
+    const int lane = threadIdx.x & 63;
+    const bool hit = lane < pairs && v == id;
+    const uint64_t named = __ballot(hit);
+    const int tok = (int)((uint32_t)lane / (uint32_t)top_k), slot = lane - tok * top_k;
+    const bool first = hit && ((named >> (lane - slot)) & ((1ull << slot) - 1)) == 0;
+    const uint64_t mask = __ballot(first);
+    if (lane == 0) repeated = mask != named;
+    if (first) list[__popcll(mask & ((1ull << lane) - 1))] = tok << 6 | slot;
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    return __popcll(mask);
+  }
 
   __device__ __forceinline__ int run(const int32_t* ids, int pairs, int top_k, int id, int* list) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -419,13 +463,13 @@ struct alignas(8) PairRec {
 // 16-bit parts (the down product then sees it to 16 bits and more, not
 // rounded to the 8 of a bfloat16), and the first workgroup of an expert
 // leaves the plan down_kernel follows.
-template <class T, int G, bool GATED, bool SHIFT>
+template <class T, int G, bool GATED, bool SHIFT, bool CUT>
 __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const RowsKArgs a) {
   constexpr bool W4 = G != 0;
   constexpr int TL = GATED ? 2 : 1;
   __shared__ int list[kPassTokens];
   __shared__ Lister lister;
-  __shared__ f32x4 red[kExpertWaves][TL][64];
+  __shared__ f32x4 red[kExpertWaves][TL][80];    // accumulator quarters 20 apart: no bank conflicts for rows
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int slot = blockIdx.y, k = a.top_k;
@@ -435,37 +479,45 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const RowsKArgs a) {
   const int tile0 = blockIdx.x * a.tiles_per_block;
   const int tile1 = min(tile0 + a.tiles_per_block, tiles);
 
-  Mac<T, G, SHIFT, TL, 1> mac;
-  mac.steps(a.w, a.w.cols, 0, part, (a.w.cols + Step<W4>::kCols - 1) / Step<W4>::kCols, split);
-  int expert = 0;
-  auto aim_a = [&](int tile) {
-    RowPtr<W4> ap[TL];
-    const int at = min(tile, tiles - 1) * 16;
-    ap[0] = row_ptr<W4>(a.w, expert, at);
-    if constexpr (GATED) ap[1] = row_ptr<W4>(a.w, expert, a.inter + at);
-    mac.aim_a(ap);
-  };
+  typedef Mac<T, G, SHIFT, CUT, TL, 1> M;
+  __shared__ __attribute__((aligned(16))) char bmem[kExpertWaves][M::kLds];
+  M mac;
+  mac.init(bmem[wave], a.w, a.w.cols, 0);
 
   // the expert of this slot, and its tokens
-  int m = a.n;
-  bool aimed = false;
+  int m = a.n, expert = 0;
   if (a.ids == nullptr) {
     for (int i = tid; i < a.n; i += kThreads) list[i] = i << 6;
     __syncthreads();
   } else {
-    const int id = a.by_pair ? a.ids[slot] : a.offset + slot;
+    const int pairs = a.n * k;
+    const bool few = pairs <= 64;
+    const int v = few ? gload<int>(a.ids + min(lane, pairs - 1)) : 0;
+    const int id = !a.by_pair ? a.offset + slot
+                   : few ? __builtin_amdgcn_readlane(v, slot) : __builtin_amdgcn_readfirstlane(a.ids[slot]);
     const bool inside = id >= a.offset && (int64_t)id - a.offset < a.num_experts;
-    expert = __builtin_amdgcn_readfirstlane(inside ? id - a.offset : 0);
+    expert = inside ? id - a.offset : 0;
     m = 0;
     if (inside) {
-      if (a.by_pair) {      // the first weights are on their way while the tokens are listed
-        aim_a(tile0 + mine);
-        aimed = true;
-      }
-      m = lister.run(a.ids, a.n * k, k, id, list);
+      m = few ? lister.run_few(v, pairs, k, id, list) : lister.run(a.ids, pairs, k, id, list);
       // of the pairs that name the same expert the first one's slot does the work
       if (a.by_pair && (list[0] >> 6) * k + (list[0] & 63) != slot) m = 0;
     }
+  }
+  m = __builtin_amdgcn_readfirstlane(m);
+
+  const typename M::Item it = mac.item(part, (a.w.cols + Step<W4>::kCols - 1) / Step<W4>::kCols, split);
+  auto aim = [&](int tile, int c0) {        // columns past the list repeat its last token and are not stored
+    RowPtr<W4> ap[TL];
+    const int at = min(tile, tiles - 1) * 16;
+    ap[0] = row_ptr<W4>(a.w, expert, at);
+    if constexpr (GATED) ap[1] = row_ptr<W4>(a.w, expert, a.inter + at);
+    const int i = min(c0 + M::load_col(), m - 1);
+    mac.aim(ap, a.x + (int64_t)(list[i] >> 6) * a.x_stride);
+  };
+  if (m > 0) {
+    aim(tile0 + mine, 0);
+    mac.prime(it);
   }
   if constexpr (GATED) {
     if (blockIdx.x == 0) {
@@ -506,35 +558,26 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const RowsKArgs a) {
         store_out<T>(a.out, (int64_t)r * a.out_stride + c0 + i % width, 0.0f, a.out_f32);
     }
   }
-  m = __builtin_amdgcn_readfirstlane(m);
   if (m == 0) return;
 
-  auto aim_b = [&](int c0) {        // columns past the list repeat its last token and are not stored
-    const int i = min(c0 + (lane & 15), m - 1);
-    mac.aim_b(a.x + (int64_t)(list[i] >> 6) * a.x_stride + (lane >> 4) * 8);
-  };
-  if (!aimed) aim_a(tile0 + mine);
-  aim_b(0);
   for (int t0 = tile0, c0 = 0; t0 < tile1;) {
-    f32x4 acc[TL];
-#pragma unroll
-    for (int t = 0; t < TL; ++t) acc[t] = f32x4{0, 0, 0, 0};
-    mac.run(acc);
-    // the next product's first loads are on their way while this one is summed
-    int t2 = t0, c2 = c0 + 16;
+    int t2 = t0, c2 = c0 + M::kCols;        // the item after this one
     if (c2 >= m) {
       c2 = 0;
       t2 += group;
     }
-    if (t2 < tile1) {
-      aim_a(t2 + mine);
-      aim_b(c2);
-    }
+    f32x4 acc[TL];
+#pragma unroll
+    for (int t = 0; t < TL; ++t) acc[t] = f32x4{0, 0, 0, 0};
+    mac.run(acc, it, t2 < tile1, [&]() {
+      aim(t2 + mine, c2);
+      return it;
+    });
     __syncthreads();
 #pragma unroll
-    for (int t = 0; t < TL; ++t) red[wave][t][lane] = acc[t];
+    for (int t = 0; t < TL; ++t) red[wave][t][(lane >> 4) * 20 + (lane & 15)] = acc[t];
     __syncthreads();
-    const int left = min(m - c0, 16);
+    const int left = min(m - c0, M::kCols);
     for (int i = tid; i < group * 256; i += kThreads) {
       const int g = i >> 8, col = (i >> 4) & 15, row = i & 15, tile = t0 + g;
       if (col >= left || tile >= tile1) continue;
@@ -542,7 +585,10 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const RowsKArgs a) {
 #pragma unroll
       for (int t = 0; t < TL; ++t) {
         v[t] = 0.0f;
-        for (int w = 0; w < split; ++w) v[t] += red[g * split + w][t][(row >> 2) * 16 + col][row & 3];
+#pragma unroll
+        for (int w = 0; w < kExpertWaves; ++w) {
+          if (w < split) v[t] += red[g * split + w][t][(row >> 2) * 20 + col][row & 3];
+        }
       }
       const int n = tile * 16 + row, at = list[c0 + col], token = at >> 6;
       if constexpr (GATED) {
@@ -568,9 +614,11 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const RowsKArgs a) {
 // weight * product into its own copy of the chunk's output tile in LDS (each
 // token at most once per expert, so lanes never meet), and the copies are
 // added in wave order at the end.
-template <class T, int G>
+template <class T, int G, bool CUT>
 __global__ void __launch_bounds__(kThreads, 4) down_kernel(const DownKArgs a) {
   constexpr bool W4 = G != 0;
+  typedef Mac<T, G, false, CUT, 1, 2> M;
+  __shared__ __attribute__((aligned(16))) char bmem[kExpertWaves][M::kLds];
   __shared__ int heads[MOE_EP_MAX_EXPERTS];
   __shared__ short slots[MOE_EP_MAX_EXPERTS];
   __shared__ int wave_count[kExpertWaves];
@@ -631,33 +679,39 @@ __global__ void __launch_bounds__(kThreads, 4) down_kernel(const DownKArgs a) {
     it.expert = head_expert(head);
     it.k0 = s - i * steps;
     it.k1 = min(steps, it.k0 + end - s);
-    it.left = m - col0;
+    it.left = min(m - col0, M::kCols);
     const int at = head_start(head) + min(col0 + (lane & 15), m - 1);
     const u32x2 rec = gload<u32x2>(static_cast<const PairRec*>(p.pair) + (int64_t)slot * a.n + at);
     it.rec = PairRec{(int)rec[0], __uint_as_float(rec[1])};
-    col0 += 16;
+    col0 += M::kCols;
     if (col0 >= m) {
       col0 = 0;
       s += it.k1 - it.k0;
     }
     return true;
   };
-  Mac<T, G, false, 1, 2> mac;
+  M mac;
+  mac.init(bmem[wave], a.w, p.act_stride, p.act_plane);
   auto aim = [&](const Item& it) {
-    mac.steps(a.w, p.act_stride, p.act_plane, it.k0, it.k1, 1);
     const RowPtr<W4> ap[1] = {row_ptr<W4>(a.w, it.expert, tile * 16)};
-    mac.aim_a(ap);
-    mac.aim_b(p.act + ((int64_t)(it.rec.pair >> 6) * a.top_k + (it.rec.pair & 63)) * p.act_stride + (lane >> 4) * 8);
+    // lane c < kCols has column c's record; the lanes that load the column need it
+    const int pair = __shfl(it.rec.pair, M::load_col());
+    mac.aim(ap, p.act + ((int64_t)(pair >> 6) * a.top_k + (pair & 63)) * p.act_stride);
+    return mac.item(it.k0, it.k1, 1);
   };
   Item cur;
+  typename M::Item now;
   bool have = next(cur);
-  if (have) aim(cur);
+  if (have) {
+    now = aim(cur);
+    mac.prime(now);
+  }
   while (have) {
     Item after;
     const bool more = next(after);
     f32x4 acc[1] = {{0, 0, 0, 0}};
-    mac.run(acc);
-    if (more) aim(after);
+    typename M::Item then = now;
+    mac.run(acc, now, more, [&]() { return then = aim(after); });
     if ((lane & 15) < cur.left) {
       f32x4* o = reinterpret_cast<f32x4*>(mine + ((cur.rec.pair >> 6) - t0) * 16 + (lane >> 4) * 4);
       f32x4 v = *o;
@@ -666,6 +720,7 @@ __global__ void __launch_bounds__(kThreads, 4) down_kernel(const DownKArgs a) {
       *o = v;
     }
     cur = after;
+    now = then;
     have = more;
   }
   __syncthreads();
@@ -685,16 +740,28 @@ template <class T, int G, bool GATED>
 void start_rows(RowsKArgs a, hipStream_t stream) {
   const int slots = a.ids == nullptr ? 1 : a.by_pair ? a.n * a.top_k : a.num_experts;
   const int tiles = (a.inter + 15) / 16;
+  // Waves to a tile.  Eight read a dense row in pieces of 1 KiB, which DRAM
+  // likes best (64 experts of 4096 x 2048, 32 tokens: 194 us; 217 at four).
+  // 4-bit tiles lie in 1 KiB pieces anyway: fewer waves to a tile mean longer
+  // streams and fewer sums (32 experts of 4096 x 7168: 131 us at eight, 123 at
+  // four, 118 at two) while there are tiles enough for all compute units (256
+  // tiles of one matrix: 7.2 us at eight, 8.8 at four).  A wave without a step
+  // only waits.
+  const int steps = (a.w.cols + Step<G != 0>::kCols - 1) / Step<G != 0>::kCols;
+  const int64_t work = (int64_t)tiles * slots;
   a.split = kExpertWaves;
-  a.tiles_per_block = 1;
+  if (G != 0 && work >= 1024) a.split = work >= 4096 ? 2 : 4;
+  while (a.split > 1 && steps < a.split) a.split /= 2;
+  a.tiles_per_block = kExpertWaves / a.split;
   const dim3 grid((tiles + a.tiles_per_block - 1) / a.tiles_per_block, slots);
   if constexpr (GATED && G != 0) {
     if (a.inter % 4 != 0) {               // the up rows' scales straddle their groups of four
-      rows_kernel<T, G, GATED, true><<<grid, kThreads, 0, stream>>>(a);
+      rows_kernel<T, G, GATED, true, true><<<grid, kThreads, 0, stream>>>(a);
       return;
     }
   }
-  rows_kernel<T, G, GATED, false><<<grid, kThreads, 0, stream>>>(a);
+  if (a.w.cols % Step<G != 0>::kCols != 0) rows_kernel<T, G, GATED, false, true><<<grid, kThreads, 0, stream>>>(a);
+  else rows_kernel<T, G, GATED, false, false><<<grid, kThreads, 0, stream>>>(a);
 }
 
 template <class T, bool GATED>
@@ -713,7 +780,8 @@ void start_down(const DownKArgs& a, hipStream_t stream) {
   const int grid = (a.tiles + 7) / 8 * 8 * a.chunks;
   const int nc = std::min(a.n, kChunkTokens);
   const size_t lds = (size_t)kExpertWaves * nc * 16 * sizeof(float);
-  down_kernel<T, G><<<grid, kThreads, lds, stream>>>(a);
+  if (a.w.cols % Step<G != 0>::kCols != 0) down_kernel<T, G, true><<<grid, kThreads, lds, stream>>>(a);
+  else down_kernel<T, G, false><<<grid, kThreads, lds, stream>>>(a);
 }
 
 template <class T>

@@ -401,8 +401,8 @@ typedef struct moe_ep_linear_args {
   int32_t num_rows;
   int32_t num_experts;            /* 1..MOE_EP_MAX_EXPERTS */
   int32_t expert_offset;          /* expert_ids of the first expert, >= 0 */
-  int32_t in_features;
-  int32_t out_features;
+  int32_t in_features;            /* 8..2^24 */
+  int32_t out_features;           /* 1..2^24 */
 } moe_ep_linear_args;
 
 /* out[r] = W[expert_ids[r] - expert_offset] x[r].  Rows whose id is outside
@@ -432,8 +432,8 @@ typedef struct moe_ep_layer_args {
   int32_t top_k;                  /* 1..MOE_EP_MAX_TOPK; the router's with router */
   int32_t num_experts;            /* experts whose weights are here, 1..MOE_EP_MAX_EXPERTS */
   int32_t expert_offset;          /* id of the first of them, >= 0 */
-  int32_t hidden_size;
-  int32_t intermediate_size;
+  int32_t hidden_size;            /* 8..2^24 */
+  int32_t intermediate_size;      /* 8..2^24 */
 } moe_ep_layer_args;
 
 /* Bytes of device workspace moe_ep_layer needs for these sizes (num_tokens,

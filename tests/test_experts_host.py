@@ -114,7 +114,7 @@ def test_linear_refusals():
     assert linear(num_rows=0, x=None, out=None) == _lib.MOE_EP_OK
     for kw in (dict(dtype=_lib.MOE_EP_F32), dict(dtype=9), dict(out_dtype=_lib.MOE_EP_F16), dict(num_rows=-1),
                dict(num_experts=0), dict(num_experts=1025), dict(expert_offset=-1), dict(expert_offset=2 ** 31 - 2),
-               dict(in_features=0), dict(out_features=0), dict(in_features=(1 << 24) + 1), dict(x=None),
+               dict(in_features=0), dict(in_features=7), dict(out_features=0), dict(in_features=(1 << 24) + 1), dict(x=None),
                dict(out=None), dict(x_stride=63), dict(x_stride=-1), dict(out_stride=31), dict(out_stride=0),
                dict(x_stride=1 << 62), dict(weight=W(None, None, 0)), dict(weight=W(FAKE, None, 32)),
                dict(weight=W(FAKE, FAKE, 16)), dict(weight=W(FAKE, FAKE, -32)),
@@ -151,7 +151,7 @@ def test_layer_refusals():
     assert layer(**dict(r, num_tokens=0)) == _lib.MOE_EP_OK
     for kw in (dict(dtype=_lib.MOE_EP_F32), dict(out_dtype=_lib.MOE_EP_F16), dict(num_tokens=-1), dict(top_k=0),
                dict(top_k=65), dict(num_experts=0), dict(num_experts=1025), dict(expert_offset=-1),
-               dict(hidden_size=0), dict(intermediate_size=0), dict(hidden=None), dict(out=None),
+               dict(hidden_size=7), dict(intermediate_size=7), dict(hidden=None), dict(out=None),
                dict(topk_ids=None), dict(hidden_stride=63), dict(out_stride=63), dict(out_stride=0),
                dict(gate_up=W(None, None, 0)), dict(down=W(FAKE, None, 64)), dict(down=W(FAKE, FAKE, 48)),
                dict(workspace=None), dict(workspace_bytes=100), dict(out=FAKE + 64), dict(out=FAKE, out_stride=128),

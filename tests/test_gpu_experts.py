@@ -160,7 +160,7 @@ def test_route_strided_rows_and_given_outputs():
 @pytest.mark.parametrize("g", [0, 32, 64, 128])
 @pytest.mark.parametrize("n,E,N,K", [(1, 1, 16, 128), (1, 4, 100, 64), (3, 2, 17, 72), (16, 5, 33, 513),
                                      (17, 3, 48, 200), (40, 2, 64, 1000), (70, 1, 40, 256), (130, 3, 20, 33),
-                                     (5, 7, 1, 1), (2, 2, 31, 2049)])
+                                     (5, 7, 1, 9), (6, 2, 5, 8), (2, 2, 31, 2049)])
 def test_linear(dtype, g, n, E, N, K):
     print(f"[linear] {dtype} g={g} n={n} E={E} N={N} K={K}", flush=True)
     x = rand(n, n, K, dtype=dtype)
@@ -252,7 +252,7 @@ def make_ids(seed, n, E, k, offset=0, extra=0):
 @pytest.mark.parametrize("g", [0, 32, 64, 128])
 @pytest.mark.parametrize("n,E,k,H,I", [(1, 8, 2, 64, 32), (1, 16, 8, 129, 40), (2, 4, 4, 200, 100), (7, 3, 2, 56, 17),
                                        (17, 8, 2, 128, 64), (33, 4, 3, 48, 130), (70, 2, 1, 40, 48),
-                                       (131, 5, 2, 24, 20), (3, 2, 2, 1, 1)])
+                                       (131, 5, 2, 24, 20), (3, 2, 2, 9, 8), (2, 3, 2, 8, 11)])
 def test_layer(dtype, g, n, E, k, H, I):
     print(f"[layer] {dtype} g={g} n={n} E={E} k={k} H={H} I={I}", flush=True)
     x = rand(n, n, H, dtype=dtype)
