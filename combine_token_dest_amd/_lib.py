@@ -47,6 +47,7 @@ MOE_EP_NOALLOC_MAX_ROWS = 65536
 
 MOE_EP_MAX_EXPERTS = 1024
 MOE_EP_MAX_TOPK = 64
+MOE_EP_MAX_GROUPS = 64
 
 MOE_EP_SCORE_SOFTMAX = 0
 MOE_EP_SCORE_SIGMOID = 1
@@ -281,12 +282,16 @@ def moe_ep_active_rank_mask(ranks: Sequence[int]) -> int:
 
 def moe_ep_route(router: moe_ep_router, logits: int, logits_dtype: int, logits_stride: int, num_tokens: int,
                  topk_ids: int, topk_weights: int, stream: int) -> None:
-    _check(load().moe_ep_route(byref(router), logits, logits_dtype, logits_stride, num_tokens, topk_ids,
-                               topk_weights, stream), "moe_ep_route")
+    st = (_lib or load()).moe_ep_route(byref(router), logits, logits_dtype, logits_stride, num_tokens, topk_ids,
+                                       topk_weights, stream)
+    if st:
+        _check(st, "moe_ep_route")
 
 
 def moe_ep_expert_linear(args: moe_ep_linear_args, stream: int) -> None:
-    _check(load().moe_ep_expert_linear(byref(args), stream), "moe_ep_expert_linear")
+    st = (_lib or load()).moe_ep_expert_linear(byref(args), stream)
+    if st:
+        _check(st, "moe_ep_expert_linear")
 
 
 def moe_ep_layer_workspace_bytes(args: moe_ep_layer_args) -> int:
@@ -296,4 +301,6 @@ def moe_ep_layer_workspace_bytes(args: moe_ep_layer_args) -> int:
 
 
 def moe_ep_layer(args: moe_ep_layer_args, stream: int) -> None:
-    _check(load().moe_ep_layer(byref(args), stream), "moe_ep_layer")
+    st = (_lib or load()).moe_ep_layer(byref(args), stream)
+    if st:
+        _check(st, "moe_ep_layer")

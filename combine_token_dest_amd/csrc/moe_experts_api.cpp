@@ -55,8 +55,9 @@ int check_router(const moe_ep_router& r) {
                   r.num_experts);
   if (r.score != MOE_EP_SCORE_SOFTMAX && r.score != MOE_EP_SCORE_SIGMOID)
     return report(MOE_EP_ERR_INVALID_ARG, "router score %d unknown", r.score);
-  if (r.num_groups < 1 || r.num_experts % r.num_groups != 0)
-    return report(MOE_EP_ERR_INVALID_ARG, "num_groups %d does not divide %d experts", r.num_groups, r.num_experts);
+  if (r.num_groups < 1 || r.num_groups > MOE_EP_MAX_GROUPS || r.num_experts % r.num_groups != 0)
+    return report(MOE_EP_ERR_INVALID_ARG, "num_groups %d is above %d or does not divide %d experts", r.num_groups,
+                  MOE_EP_MAX_GROUPS, r.num_experts);
   if (r.top_groups < 1 || r.top_groups > r.num_groups)
     return report(MOE_EP_ERR_INVALID_ARG, "top_groups %d outside [1, %d]", r.top_groups, r.num_groups);
   if (r.top_groups * (r.num_experts / r.num_groups) < r.top_k)

@@ -24,14 +24,13 @@ __device__ __forceinline__ float clean_logit(float l) {
   return l == l ? __builtin_fminf(l, FLT_MAX) : -INFINITY;
 }
 
-template <typename V>
-__device__ __forceinline__ bool better(V v1, int e1, V v0, int e0) {
-  return v1 > v0 || (v1 == v0 && e1 < e0);
-}
-
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp(uint32_t x) {
-  return __builtin_amdgcn_update_dpp(x, x, CTRL, 0xf, 0xf, false);
+  return __builtin_amdgcn_mov_dpp(x, CTRL, 0xf, 0xf, false);
+}
+template <int CTRL>
+__device__ __forceinline__ int dpp(int x) {
+  return (int)dpp<CTRL>((uint32_t)x);
 }
 template <int CTRL>
 __device__ __forceinline__ float dpp(float x) {
@@ -45,8 +44,8 @@ __device__ __forceinline__ double dpp(double x) {
   return __builtin_bit_cast(double, u);
 }
 
-// x of both halves of a pair of 16-lane rows (W = 16) or of a pair of 32-lane
-// halves (W = 32): the two results are the pair's first and second member.
+// x of both members of a pair of 16-lane rows (W = 16) or of the pair of
+// 32-lane halves (W = 32), in every lane of the pair.
 template <int W>
 __device__ __forceinline__ void both(uint32_t x, uint32_t* a, uint32_t* b) {
   if constexpr (W == 16) {
@@ -58,6 +57,13 @@ __device__ __forceinline__ void both(uint32_t x, uint32_t* a, uint32_t* b) {
     *a = r[0];
     *b = r[1];
   }
+}
+template <int W>
+__device__ __forceinline__ void both(int x, int* a, int* b) {
+  uint32_t u, v;
+  both<W>((uint32_t)x, &u, &v);
+  *a = (int)u;
+  *b = (int)v;
 }
 template <int W>
 __device__ __forceinline__ void both(float x, float* a, float* b) {
@@ -81,57 +87,35 @@ __device__ __forceinline__ void both(double x, double* a, double* b) {
   *b = __builtin_bit_cast(double, q);
 }
 
-// All-reductions over the LPT (16 or 64) lanes of a token.
-template <int CTRL, typename V>
-__device__ __forceinline__ void best_step(V& v, int& e) {
-  const V ov = dpp<CTRL>(v);
-  const int oe = (int)dpp<CTRL>((uint32_t)e);
-  if (better(ov, oe, v, e)) {
-    v = ov;
-    e = oe;
-  }
-}
-template <int W, typename V>
-__device__ __forceinline__ void best_pair(V& v, int& e) {
-  V a, b;
-  uint32_t ea, eb;
-  both<W>(v, &a, &b);
-  both<W>((uint32_t)e, &ea, &eb);
-  const bool second = better(b, (int)eb, a, (int)ea);
-  v = second ? b : a;
-  e = second ? (int)eb : (int)ea;
-}
-template <int LPT, typename V>
-__device__ __forceinline__ void reduce_best(V& v, int& e) {
-  best_step<0x128>(v, e);   // row_ror:8, 4, 2, 1
-  best_step<0x124>(v, e);
-  best_step<0x122>(v, e);
-  best_step<0x121>(v, e);
-  if constexpr (LPT == 64) {
-    best_pair<16>(v, e);
-    best_pair<32>(v, e);
-  }
-}
-template <int LPT, typename V>
-__device__ __forceinline__ V reduce_sum(V v) {
-  v += dpp<0x128>(v);
-  v += dpp<0x124>(v);
-  v += dpp<0x122>(v);
-  v += dpp<0x121>(v);
+// All-reduction over the LPT (16 or 64) lanes of a token, in a fixed order.
+template <int LPT, typename V, typename F>
+__device__ __forceinline__ V reduce(V v, F op) {
+  v = op(v, dpp<0x128>(v));             // row_ror:8, 4, 2, 1
+  v = op(v, dpp<0x124>(v));
+  v = op(v, dpp<0x122>(v));
+  v = op(v, dpp<0x121>(v));
   if constexpr (LPT == 64) {
     V a, b;
     both<16>(v, &a, &b);
-    v = a + b;
+    v = op(a, b);
     both<32>(v, &a, &b);
-    v = a + b;
+    v = op(a, b);
   }
   return v;
 }
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_fmaxf(a, b); }
+__device__ __forceinline__ double larger(double a, double b) { return __builtin_fmax(a, b); }
+template <int LPT, typename V>
+__device__ __forceinline__ V reduce_max(V v) {
+  return reduce<LPT>(v, [](V a, V b) { return larger(a, b); });
+}
 template <int LPT>
-__device__ __forceinline__ float reduce_max(float v) {
-  int e = 0;
-  reduce_best<LPT>(v, e);
-  return v;
+__device__ __forceinline__ int reduce_min(int v) {
+  return reduce<LPT>(v, [](int a, int b) { return min(a, b); });
+}
+template <int LPT, typename V>
+__device__ __forceinline__ V reduce_sum(V v) {
+  return reduce<LPT>(v, [](V a, V b) { return a + b; });
 }
 
 __device__ __forceinline__ double score64(int score, float l, float top) {
@@ -141,14 +125,20 @@ __device__ __forceinline__ double score64(int score, float l, float top) {
 constexpr int kRouteThreads = 256;
 
 // One token per LPT lanes, expert e = v * LPT + lane in register v.  The
-// selection is top_k rounds of an all-lane maximum of (choice, lowest index).
-// Without a bias or groups the choice is the logit itself (V = float): it
-// orders the experts as the score does, without the ties of a saturated
-// score.  Otherwise it is the score in float64 (V = double), so that a
-// near-tie is decided by the values and not by a float32 rounding.
-// Weights are computed in float64 by one lane per slot and rounded once.
+// selection is top_k rounds of a maximum over the lanes, then the lowest index
+// among the lanes that hold it.  Without a bias or groups the choice is the
+// logit itself (V = float): it orders the experts as the score does, without
+// the ties of a saturated score.  Otherwise it is the score in float64 (V =
+// double), so that a near-tie is decided by the values and not by a float32
+// rounding.  Weights are computed in float64 by one lane per slot and rounded
+// once.
+//
+// A token costs some 60 instructions a round, so few tokens are bound by
+// latency (one load, top_k rounds, one exponential) and many by issue: 16
+// lanes to a token then do four tokens with the instructions of one.
 template <typename V, int LPT, int VPL, bool GROUPS>
 __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteKArgs a) {
+  constexpr bool kScores = std::is_same<V, double>::value;
   constexpr int kTokens = 64 / LPT;
   const int lane = threadIdx.x & 63;
   const int wave = threadIdx.x >> 6;
@@ -158,11 +148,12 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteKArgs a
   const int E = a.num_experts;
   const int64_t row = t * a.logits_stride;
 
-  float l[VPL];
+  float l[VPL], bias[kScores ? VPL : 1];
 #pragma unroll
   for (int v = 0; v < VPL; ++v) {
-    const int e = v * LPT + sub;
-    l[v] = load_logit(a.logits, row + (e < E ? e : E - 1), a.logits_dtype);
+    const int e = v * LPT + sub, at = e < E ? e : E - 1;
+    l[v] = load_logit(a.logits, row + at, a.logits_dtype);
+    if constexpr (kScores) bias[v] = a.bias ? a.bias[at] : 0.0f;
   }
 #pragma unroll
   for (int v = 0; v < VPL; ++v) l[v] = v * LPT + sub < E ? clean_logit(l[v]) : -INFINITY;
@@ -170,7 +161,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteKArgs a
   V c[VPL];
   float top = 0.0f;
   double total = 1.0;
-  if constexpr (std::is_same<V, double>::value) {
+  if constexpr (kScores) {
     if (a.score == MOE_EP_SCORE_SOFTMAX) {
       float m = l[0];
 #pragma unroll
@@ -183,51 +174,55 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteKArgs a
         s += c[v];
       }
       total = reduce_sum<LPT>(s);
+#pragma unroll
+      for (int v = 0; v < VPL; ++v) c[v] /= total;
+    } else {
+#pragma unroll
+      for (int v = 0; v < VPL; ++v) c[v] = score64(MOE_EP_SCORE_SIGMOID, l[v], 0.0f);
     }
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
-      const int e = v * LPT + sub;
-      double x = a.score == MOE_EP_SCORE_SOFTMAX ? c[v] / total : score64(MOE_EP_SCORE_SIGMOID, l[v], 0.0f);
-      if (a.bias) x += (double)a.bias[e < E ? e : E - 1];
+      const double x = c[v] + (double)bias[v];
       c[v] = l[v] > -INFINITY && x > -INFINITY ? x : -INFINITY;   // a NaN bias closes too
     }
     if constexpr (GROUPS) {
-      // LPT is 64 here: one token per wave.
+      // LPT is 64 here, one token per wave: the choices go through LDS so that
+      // `per` lanes side by side read a group's.
       extern __shared__ double lds[];
-      const int G = a.num_groups;
-      const int size = E / G;
-      double* cs = lds + wave * (E + G);
-      double* gv = cs + E;
+      double* cs = lds + wave * E;
 #pragma unroll
       for (int v = 0; v < VPL; ++v) {
         const int e = v * LPT + sub;
         if (e < E) cs[e] = c[v];
       }
       __syncthreads();
-      for (int g = sub; g < G; g += LPT) {
-        double b1 = -INFINITY, b2 = -INFINITY;
-        for (int i = 0; i < size; ++i) {
-          const double x = cs[g * size + i];
-          if (x > b1) {
-            b2 = b1;
-            b1 = x;
-          } else if (x > b2) {
-            b2 = x;
-          }
+      const int G = a.num_groups, size = E / G;
+      const int per = 64 >> (32 - __builtin_clz(G - 1));     // lanes to a group, a power of two
+      const int group = sub / per;
+      double b1 = -INFINITY, b2 = -INFINITY;
+      if (group < G) {
+        for (int i = sub % per; i < size; i += per) {
+          const double x = cs[group * size + i];
+          b2 = larger(b2, x < b1 ? x : b1);
+          b1 = larger(b1, x);
         }
-        gv[g] = a.group_top > 1 && b2 > -INFINITY ? b1 + b2 : b1;
       }
-      __syncthreads();
+      for (int d = 1; d < per; d *= 2) {
+        const double o1 = __shfl_xor(b1, d), o2 = __shfl_xor(b2, d);
+        b2 = larger(larger(b2, o2), b1 < o1 ? b1 : o1);
+        b1 = larger(b1, o1);
+      }
+      const double value = a.group_top > 1 && b2 > -INFINITY ? b1 + b2 : b1;
+      int ahead = 0;
+      for (int h = 0; h < G; ++h) {
+        const double o = __shfl(value, h * per);
+        ahead += o > value || (o == value && h < group) ? 1 : 0;
+      }
+      const uint64_t open = __ballot(ahead < a.top_groups);
 #pragma unroll
       for (int v = 0; v < VPL; ++v) {
         const int e = v * LPT + sub;
-        if (e < E) {
-          const int g = e / size;
-          const double mine = gv[g];
-          int ahead = 0;
-          for (int h = 0; h < G; ++h) ahead += better(gv[h], h, mine, g) ? 1 : 0;
-          if (ahead >= a.top_groups) c[v] = -INFINITY;
-        }
+        if (!((open >> ((e < E ? e / size : 0) * per)) & 1)) c[v] = -INFINITY;
       }
     }
   } else {
@@ -235,27 +230,34 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteKArgs a
     for (int v = 0; v < VPL; ++v) c[v] = l[v];
   }
 
-  int mine = INT_MAX;       // the expert of slot `sub`
+  int mine = INT_MAX;       // slot `sub`: its expert, and that one's logit
+  float mine_l = -INFINITY;
   for (int r = 0; r < a.top_k; ++r) {
-    V bv = -INFINITY;
+    V bv = c[0];
+#pragma unroll
+    for (int v = 1; v < VPL; ++v) bv = larger(bv, c[v]);
+    const V best = reduce_max<LPT>(bv);
     int be = INT_MAX;
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) {
-      if (c[v] > bv) {
-        bv = c[v];
-        be = v * LPT + sub;
-      }
-    }
-    reduce_best<LPT>(bv, be);
-    if (std::is_same<V, float>::value && r == 0) top = (float)bv;
-    if (sub == r) mine = be;
+    for (int v = VPL - 1; v >= 0; --v) be = c[v] == best ? v * LPT + sub : be;
+    be = best > (V)-INFINITY ? reduce_min<LPT>(be) : INT_MAX;
+    float bl = 0.0f;
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
-      if (be == v * LPT + sub) c[v] = -INFINITY;
+      if (be == v * LPT + sub) {
+        c[v] = (V)-INFINITY;
+        bl = l[v];
+      }
+    }
+    bl = __shfl(bl, (lane & ~(LPT - 1)) + (be & (LPT - 1)));
+    if (!kScores && r == 0) top = bl;
+    if (sub == r) {
+      mine = be;
+      mine_l = bl;
     }
   }
 
-  if constexpr (std::is_same<V, float>::value) {
+  if constexpr (!kScores) {
     if (a.score == MOE_EP_SCORE_SOFTMAX && !a.renormalize) {
       float s = 0.0f;
 #pragma unroll
@@ -264,8 +266,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteKArgs a
     }
   }
   const bool open = mine != INT_MAX && sub < a.top_k;
-  double s = 0.0;
-  if (open) s = score64(a.score, clean_logit(load_logit(a.logits, row + mine, a.logits_dtype)), top);
+  const double s = open ? score64(a.score, mine_l, top) : 0.0;
   const double z = a.renormalize ? reduce_sum<LPT>(s) : total;
   if (token < a.n && sub < a.top_k) {
     a.ids[token * a.top_k + sub] = open ? mine : a.invalid_id;
@@ -277,7 +278,7 @@ template <typename V, int LPT, bool GROUPS>
 void start_route(const RouteKArgs& a, hipStream_t stream) {
   constexpr int kPerBlock = kRouteThreads / 64 * (64 / LPT);
   const int grid = (int)(((int64_t)a.n + kPerBlock - 1) / kPerBlock);
-  const size_t lds = GROUPS ? (size_t)(kRouteThreads / 64) * (a.num_experts + a.num_groups) * sizeof(double) : 0;
+  const size_t lds = GROUPS ? (size_t)(kRouteThreads / 64) * a.num_experts * sizeof(double) : 0;
   const int vpl = (a.num_experts + LPT - 1) / LPT;
   if (vpl <= 1) route_kernel<V, LPT, 1, GROUPS><<<grid, kRouteThreads, lds, stream>>>(a);
   else if (vpl <= 2) route_kernel<V, LPT, 2, GROUPS><<<grid, kRouteThreads, lds, stream>>>(a);
@@ -291,6 +292,7 @@ void start_route(const RouteKArgs& a, hipStream_t stream) {
 hipError_t launch_route(const RouteKArgs& a, hipStream_t stream) {
   if (a.num_groups > 1) start_route<double, 64, true>(a, stream);
   else if (a.bias) start_route<double, 64, false>(a, stream);
+  else if (a.n >= 2048 && a.num_experts <= 256 && a.top_k <= 16) start_route<float, 16, false>(a, stream);
   else start_route<float, 64, false>(a, stream);
   return hipGetLastError();
 }

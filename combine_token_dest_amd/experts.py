@@ -205,7 +205,7 @@ def _output(out, shape, dtype, out_dtype, x) -> torch.Tensor:
         odt = x.dtype if out_dtype is None else out_dtype
         if odt != x.dtype and odt != torch.float32:
             raise TypeError(f"out_dtype must be {x.dtype} or float32, got {odt}")
-        return torch.empty(shape, dtype=odt, device=x.device)
+        return x.new_empty(shape, dtype=odt)
     if out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
     if tuple(out.shape) != tuple(shape) or (out.dtype != dtype and out.dtype != torch.float32):
@@ -253,21 +253,15 @@ def _logits(logits: torch.Tensor) -> Tuple[int, int, int]:
     return dev, _DTYPES[logits.dtype], logits.stride(0)
 
 
-class _Device:
-    """The tensors' device made current for a call, where it is not already."""
-
-    def __init__(self, dev: int):
-        self.dev = dev
-
-    def __enter__(self):
-        self.before = torch.cuda.current_device()
-        if self.before != self.dev:
-            torch.cuda.set_device(self.dev)
-        return torch.cuda.current_stream(self.dev).cuda_stream
-
-    def __exit__(self, *exc):
-        if self.before != self.dev:
-            torch.cuda.set_device(self.before)
+def _call(entry, dev: int, *args) -> None:
+    """entry(*args, stream) on the current stream of GPU ``dev``, with that
+    device current.  (The raw accessors: torch.cuda.current_stream() builds a
+    Stream object, a tenth of a call's host time.)"""
+    if torch._C._cuda_getDevice() == dev:
+        entry(*args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        with torch.cuda.device(dev):
+            entry(*args, torch._C._cuda_getCurrentRawStream(dev))
 
 
 def route(logits: torch.Tensor, router: Router, *, topk_ids: Optional[torch.Tensor] = None,
@@ -283,17 +277,16 @@ def route(logits: torch.Tensor, router: Router, *, topk_ids: Optional[torch.Tens
     r = _router(router, E, dev)
     shape = (n, router.top_k)
     if topk_ids is None:
-        topk_ids = torch.empty(shape, dtype=torch.int32, device=logits.device)
+        topk_ids = logits.new_empty(shape, dtype=torch.int32)
     elif topk_ids.dtype != torch.int32 or tuple(topk_ids.shape) != shape or not topk_ids.is_contiguous():
         raise ValueError(f"topk_ids must be a contiguous int32 {list(shape)}")
     if topk_weights is None:
-        topk_weights = torch.empty(shape, dtype=torch.float32, device=logits.device)
+        topk_weights = logits.new_empty(shape, dtype=torch.float32)
     elif topk_weights.dtype != torch.float32 or tuple(topk_weights.shape) != shape \
             or not topk_weights.is_contiguous():
         raise ValueError(f"topk_weights must be a contiguous float32 {list(shape)}")
-    with _Device(dev) as stream:
-        _lib.moe_ep_route(r, logits.data_ptr(), dtype, stride, n, _on(topk_ids, dev, "topk_ids"),
-                          _on(topk_weights, dev, "topk_weights"), stream)
+    _call(_lib.moe_ep_route, dev, r, logits.data_ptr(), dtype, stride, n, _on(topk_ids, dev, "topk_ids"),
+          _on(topk_weights, dev, "topk_weights"))
     return topk_ids, topk_weights
 
 
@@ -323,8 +316,7 @@ def expert_linear(x: torch.Tensor, weight: Weight, expert_ids: Optional[torch.Te
     a.dtype, a.out_dtype = _DTYPES[x.dtype], _DTYPES[out.dtype]
     a.num_rows, a.num_experts, a.expert_offset = n, E, expert_offset
     a.in_features, a.out_features = K, N
-    with _Device(dev) as stream:
-        _lib.moe_ep_expert_linear(a, stream)
+    _call(_lib.moe_ep_expert_linear, dev, a)
     return out
 
 
@@ -384,14 +376,15 @@ def moe_layer(hidden: torch.Tensor, gate_up: Weight, down: Weight, topk_ids: Opt
     a.dtype, a.out_dtype = _DTYPES[dtype], _DTYPES[out.dtype]
     a.num_tokens, a.top_k, a.num_experts, a.expert_offset = n, top_k, E, expert_offset
     a.hidden_size, a.intermediate_size = H, inter
-    with _Device(dev) as stream:
-        if workspace is None:
-            workspace = torch.empty(_lib.moe_ep_layer_workspace_bytes(a), dtype=torch.uint8, device=hidden.device)
-        elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+    if workspace is None:
+        nbytes = _lib.moe_ep_layer_workspace_bytes(a)
+        workspace = hidden.new_empty((nbytes,), dtype=torch.uint8)
+    else:
+        if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous uint8 tensor")
-        a.workspace = _on(workspace, dev, "workspace")
-        a.workspace_bytes = workspace.numel()
-        _lib.moe_ep_layer(a, stream)
+        nbytes = workspace.numel()
+    a.workspace, a.workspace_bytes = _on(workspace, dev, "workspace"), nbytes
+    _call(_lib.moe_ep_layer, dev, a)
     return out
 
 

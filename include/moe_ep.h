@@ -323,6 +323,8 @@ MOE_EP_API int moe_ep_active_rank_mask(const int32_t* ranks, int32_t n, uint64_t
 #define MOE_EP_MAX_EXPERTS 1024
 /* Most experts per token of a router or a layer. */
 #define MOE_EP_MAX_TOPK 64
+/* Most groups of a router. */
+#define MOE_EP_MAX_GROUPS 64
 
 typedef enum moe_ep_score {
   MOE_EP_SCORE_SOFTMAX = 0,       /* softmax over the experts */
@@ -350,7 +352,7 @@ typedef struct moe_ep_router {
   int32_t num_experts;            /* 1..MOE_EP_MAX_EXPERTS */
   int32_t top_k;                  /* 1..min(num_experts, MOE_EP_MAX_TOPK) */
   int32_t score;                  /* moe_ep_score */
-  int32_t num_groups;             /* divides num_experts; 1 = no groups */
+  int32_t num_groups;             /* 1..MOE_EP_MAX_GROUPS, divides num_experts; 1 = no groups */
   int32_t top_groups;             /* 1..num_groups, holding at least top_k experts */
   int32_t group_top;              /* 1 or 2 */
   int32_t renormalize;

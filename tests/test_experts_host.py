@@ -40,7 +40,7 @@ def status(fn, *args):
 def test_struct_layouts_and_constants(tmp_path):
     structs = {n: getattr(_lib, n) for n in ("moe_ep_router", "moe_ep_weight", "moe_ep_linear_args",
                                              "moe_ep_layer_args")}
-    consts = ["MOE_EP_MAX_EXPERTS", "MOE_EP_MAX_TOPK", "MOE_EP_SCORE_SOFTMAX", "MOE_EP_SCORE_SIGMOID"]
+    consts = ["MOE_EP_MAX_EXPERTS", "MOE_EP_MAX_TOPK", "MOE_EP_MAX_GROUPS", "MOE_EP_SCORE_SOFTMAX", "MOE_EP_SCORE_SIGMOID"]
     lines = ['#include <stdio.h>', '#include <stddef.h>', '#include "moe_ep.h"', "int main(void) {"]
     for name, cls in structs.items():
         lines.append(f'printf("{name} sizeof %zu\\n", sizeof({name}));')
@@ -75,7 +75,7 @@ def route(r, logits=FAKE, dtype=_lib.MOE_EP_F32, stride=16, n=4, ids=FAKE, w=FAK
 def test_route_refusals():
     assert route(router(), n=0) == _lib.MOE_EP_OK
     for kw in (dict(num_experts=0), dict(num_experts=1025), dict(top_k=0), dict(top_k=17),
-               dict(num_experts=128, top_k=65), dict(score=2), dict(num_groups=0), dict(num_groups=3),
+               dict(num_experts=128, top_k=65), dict(score=2), dict(num_groups=0), dict(num_groups=3), dict(num_experts=128, num_groups=128, top_groups=64),
                dict(num_groups=4, top_groups=0), dict(num_groups=4, top_groups=5),
                dict(num_groups=8, top_groups=1, top_k=4), dict(group_top=0), dict(group_top=3)):
         assert route(router(**kw), n=0) == INVALID, kw
