@@ -167,12 +167,25 @@ constexpr int32_t kMaxSide = 1 << 24;
 // Fewest elements of a row that the kernels read eight at a time.
 constexpr int32_t kMinRow = 8;
 
+// Whether the kernels for many tokens to an expert take a pass of n tokens
+// with top_k experts each.  The narrow ones take four (4-bit) or eight (dense)
+// tokens at a time and read the weights again for each such pass, from L2 at
+// best; the wide ones read them once per 64 tokens, but a workgroup covers
+// `rows` of the weights' rows, and below some 512 workgroups the card is not
+// full.  (The experts' tokens are counted as if all of them were chosen here.)
+bool is_wide(int64_t n, int top_k, int64_t num_experts, int64_t rows_of_tiles, int rows, int group) {
+  const int64_t pairs = n * top_k, cols = group ? 4 : 8;
+  const int64_t passes = (pairs + num_experts * cols - 1) / (num_experts * cols);
+  const int64_t blocks = (rows_of_tiles + rows - 1) / rows * std::min(pairs, num_experts);
+  return passes > 1 && passes * blocks >= 512;
+}
+
 // Workspace of one pass: [ids][weights] with a router, the plan, the
 // activations.  Every part starts on 256 bytes.
 struct LayerSpace {
-  int64_t ids, weights, head, pair, act, total;
+  int64_t ids, weights, head, pair, act, pair_out, pair_stride, total;
   int32_t n, slots, act_stride;
-  bool by_pair;
+  bool by_pair, wide;
 };
 
 int make_space(const moe_ep_layer_args* a, LayerSpace* s) {
@@ -181,6 +194,8 @@ int make_space(const moe_ep_layer_args* a, LayerSpace* s) {
   if (a->num_tokens < 0) return report(MOE_EP_ERR_INVALID_ARG, "num_tokens %d < 0", a->num_tokens);
   if (a->top_k < 1 || a->top_k > MOE_EP_MAX_TOPK)
     return report(MOE_EP_ERR_INVALID_ARG, "top_k %d outside [1, %d]", a->top_k, MOE_EP_MAX_TOPK);
+  if (a->hidden_size < kMinRow || a->hidden_size > kMaxSide)
+    return report(MOE_EP_ERR_INVALID_ARG, "hidden_size %d outside [%d, %d]", a->hidden_size, kMinRow, kMaxSide);
   if (a->intermediate_size < kMinRow || a->intermediate_size > kMaxSide)
     return report(MOE_EP_ERR_INVALID_ARG, "intermediate_size %d outside [%d, %d]", a->intermediate_size, kMinRow,
                   kMaxSide);
@@ -200,6 +215,9 @@ int make_space(const moe_ep_layer_args* a, LayerSpace* s) {
   s->head = take((int64_t)s->slots * kMaxChunks * 4);
   s->pair = take((int64_t)s->slots * s->n * 8);
   s->act = take(2 * pairs * s->act_stride * 2);
+  s->wide = is_wide(s->n, a->top_k, a->num_experts, a->intermediate_size, kWideWaves * 16, a->gate_up.group_size);
+  s->pair_stride = up(a->hidden_size, 16);
+  s->pair_out = take(s->wide ? pairs * s->pair_stride * 4 : 0);
   s->total = std::max<int64_t>(off, 256);
   return MOE_EP_OK;
 }
@@ -265,6 +283,7 @@ int moe_ep_expert_linear(const moe_ep_linear_args* a, void* stream) {
     k.out = static_cast<uint8_t*>(a->out) + t * a->out_stride * out_esz;
     k.ids = a->expert_ids ? a->expert_ids + t : nullptr;
     k.by_pair = k.n <= a->num_experts;
+    k.wide = is_wide(k.n, 1, k.ids ? a->num_experts : 1, a->out_features, kWideWaves * 32, a->weight.group_size);
     const hipError_t e = launch_expert_linear(k, a->dtype, a->weight.group_size, static_cast<hipStream_t>(stream));
     if (e != hipSuccess) return report(MOE_EP_ERR_HIP, "expert_linear launch failed: %s", hipGetErrorString(e));
   }
@@ -288,8 +307,6 @@ int moe_ep_layer(const moe_ep_layer_args* a, void* stream) {
   st = make_space(a, &s);
   if (st != MOE_EP_OK) return st;
   const int n = a->num_tokens;
-  if (a->hidden_size < kMinRow || a->hidden_size > kMaxSide)
-    return report(MOE_EP_ERR_INVALID_ARG, "hidden_size %d outside [%d, %d]", a->hidden_size, kMinRow, kMaxSide);
   const int out_esz = elem_bytes(a->out_dtype);
   st = check_rows("hidden", a->hidden, a->hidden_stride, a->hidden_size, n, 2, true);
   if (st == MOE_EP_OK) st = check_rows("out", a->out, a->out_stride, a->hidden_size, n, out_esz, false);
@@ -362,8 +379,21 @@ int moe_ep_layer(const moe_ep_layer_args* a, void* stream) {
     r.plan = d.plan = p;
     d.out = static_cast<uint8_t*>(a->out) + t * a->out_stride * out_esz;
     d.chunks = (m + kChunkTokens - 1) / kChunkTokens;
+    r.wide = s.wide;
     hipError_t e = launch_gate_up(r, a->dtype, a->gate_up.group_size, hs);
-    if (e == hipSuccess) e = launch_down(d, a->dtype, a->down.group_size, hs);
+    if (e == hipSuccess && s.wide) {
+      RowsKArgs y = r;
+      y.w = d.w;
+      y.inter = a->hidden_size;
+      y.pair_out = reinterpret_cast<float*>(ws + s.pair_out);
+      y.pair_stride = s.pair_stride;
+      y.out = d.out;
+      y.out_stride = d.out_stride;
+      y.out_f32 = d.out_f32;
+      e = launch_wide_down(y, a->dtype, a->down.group_size, hs);
+    } else if (e == hipSuccess) {
+      e = launch_down(d, a->dtype, a->down.group_size, hs);
+    }
     if (e != hipSuccess) return report(MOE_EP_ERR_HIP, "layer launch failed: %s", hipGetErrorString(e));
   }
   return MOE_EP_OK;

@@ -25,6 +25,9 @@ constexpr int kMaxChunks = kPassTokens / kChunkTokens;
 // Waves of a workgroup of the expert kernels; they share the sum over k.
 constexpr int kExpertWaves = 8;
 
+// Waves of a workgroup of the kernels for many tokens to an expert.
+constexpr int kWideWaves = 4;
+
 struct RouteKArgs {
   const void* logits;
   int64_t logits_stride;      // elements
@@ -99,7 +102,10 @@ struct RowsKArgs {
   int32_t offset;             // first expert id
   int32_t num_experts;
   int32_t by_pair;            // slots are (token, k) pairs, else experts
-  int32_t inter;              // layer: intermediate size; linear: out features
+  int32_t inter;              // gate and up: intermediate size; else the rows of w
+  int32_t wide;               // many tokens to an expert (wide_kernel)
+  float* pair_out;            // wide down product: [n * top_k, pair_stride], each pair's weighted product
+  int64_t pair_stride;
   int32_t split;              // waves that share a tile (set by the launcher)
   int32_t tiles_per_block;    // (set by the launcher)
 };
@@ -122,5 +128,7 @@ hipError_t launch_route(const RouteKArgs& a, hipStream_t stream);
 hipError_t launch_expert_linear(const RowsKArgs& a, int dtype, int group, hipStream_t stream);
 hipError_t launch_gate_up(const RowsKArgs& a, int dtype, int group, hipStream_t stream);
 hipError_t launch_down(const DownKArgs& a, int dtype, int group, hipStream_t stream);
+// The down product for many tokens to an expert, and the sum over each token's pairs.
+hipError_t launch_wide_down(const RowsKArgs& a, int dtype, int group, hipStream_t stream);
 
 }  // namespace moe_ep_detail

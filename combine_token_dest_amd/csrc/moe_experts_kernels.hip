@@ -378,9 +378,10 @@ __device__ __forceinline__ void store_out(void* out, int64_t i, float v, int f32
 
 // The pairs (token, top-k slot) that name an expert, in ascending order and
 // each token once: list[i] = token << 6 | slot.  Called by a whole workgroup.
+template <int W>                         // waves of the workgroup
 struct Lister {
   static constexpr int kUnroll = 4;     // loads in flight per thread
-  int count[kUnroll][kExpertWaves];
+  int count[kUnroll][W];
   int repeated;                         // a token names the expert twice
 
   // At most 64 pairs, whose ids each wave holds one a lane: every wave lists
@@ -404,18 +405,18 @@ struct Lister {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     int m = 0;
     if (tid == 0) repeated = 0;
-    for (int base = 0; base < pairs; base += kThreads * kUnroll) {
+    for (int base = 0; base < pairs; base += W * 64 * kUnroll) {
       int v[kUnroll], tok[kUnroll], slot[kUnroll];
       uint64_t mask[kUnroll];
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        const int p = base + u * kThreads + tid;
+        const int p = base + u * W * 64 + tid;
         v[u] = ids[p < pairs ? p : pairs - 1];
       }
       __syncthreads();
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        const int p = base + u * kThreads + tid;
+        const int p = base + u * W * 64 + tid;
         bool hit = p < pairs && v[u] == id;
         mask[u] = __ballot(hit);
         if (mask[u]) {
@@ -437,7 +438,7 @@ struct Lister {
       for (int u = 0; u < kUnroll; ++u) {
         int before = m;
 #pragma unroll
-        for (int w = 0; w < kExpertWaves; ++w) {
+        for (int w = 0; w < W; ++w) {
           const int c = count[u][w];
           before += w < wave ? c : 0;
           m += c;
@@ -456,6 +457,19 @@ struct alignas(8) PairRec {
   float weight;
 };
 
+// The weight of a listed pair: the sum of its token's weights for the expert.
+__device__ __forceinline__ float pair_weight(const RowsKArgs& a, int pair, int expert, int repeated) {
+  const int64_t row = (int64_t)(pair >> 6) * a.top_k;
+  const int j0 = pair & 63;
+  float weight = a.topk_weights ? a.topk_weights[row + j0] : 1.0f;
+  if (repeated) {
+    for (int j = j0 + 1; j < a.top_k; ++j) {
+      if (a.ids[row + j] == expert + a.offset) weight += a.topk_weights ? a.topk_weights[row + j] : 1.0f;
+    }
+  }
+  return weight;
+}
+
 // A workgroup takes one expert (blockIdx.y) and a run of tiles of 16 output
 // rows (GATED: 16 gate rows and the 16 up rows beside them), a.split of its
 // waves to a tile.  It lists the tokens that chose the expert and multiplies
@@ -468,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const RowsKArgs a) {
   constexpr bool W4 = G != 0;
   constexpr int TL = GATED ? 2 : 1;
   __shared__ int list[kPassTokens];
-  __shared__ Lister lister;
+  __shared__ Lister<kExpertWaves> lister;
   __shared__ f32x4 red[kExpertWaves][TL][80];    // accumulator quarters 20 apart: no bank conflicts for rows
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -537,16 +551,7 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const RowsKArgs a) {
       }
       PairRec* rec = reinterpret_cast<PairRec*>(a.plan.pair) + (int64_t)slot * a.n;
       for (int i = tid; i < m; i += kThreads) {
-        const int t = list[i] >> 6, j0 = list[i] & 63;
-        float weight = 1.0f;
-        if (a.topk_weights) weight = a.topk_weights[(int64_t)t * k + j0];
-        if (lister.repeated) {
-          for (int j = j0 + 1; j < k; ++j) {
-            if (a.ids[(int64_t)t * k + j] == expert + a.offset)
-              weight += a.topk_weights ? a.topk_weights[(int64_t)t * k + j] : 1.0f;
-          }
-        }
-        rec[i] = PairRec{list[i], weight};
+        rec[i] = PairRec{list[i], pair_weight(a, list[i], expert, lister.repeated)};
       }
     }
   } else if (a.ids != nullptr && slot == 0) {
@@ -734,6 +739,332 @@ __global__ void __launch_bounds__(kThreads, 4) down_kernel(const DownKArgs a) {
   }
 }
 
+// ---- many tokens to an expert ------------------------------------------------
+
+constexpr int kWideThreads = kWideWaves * 64;
+
+// What a wide workgroup computes.
+enum WideOp { kWideLinear, kWideGated, kWideDown };
+
+// One pass of a workgroup: kWideWaves * TL tiles of 16 weight rows, TL to a
+// wave over all of k, times 16 CT columns of B.  All waves need the same B:
+// each step of it is loaded once by the whole workgroup and handed out through
+// LDS, in two buffers with one barrier a step.  A and B go out kDepth steps
+// ahead, as in Mac.
+template <class T, int G, bool SHIFT, bool CUT, int P, int CT>
+struct WideMac {
+  static constexpr bool W4 = G != 0;
+  static constexpr int GJ = W4 ? G / 32 : 1;
+  static constexpr int kG = W4 ? 4 / GJ : 1;
+  static constexpr int kStep = Step<W4>::kCols, kMac = kStep / 32;
+  static constexpr int TL = 2;
+  static constexpr int kUnits = kStep / 8;                // 16-byte units of a column in a step
+  static constexpr int kPitch = P * kUnits * 16 + 16;     // bytes from column to column in LDS
+  static constexpr int kBuffer = 16 * CT * kPitch;
+  static constexpr int kLoads = (16 * CT * kUnits + kWideThreads - 1) / kWideThreads;   // units a thread loads, per plane
+  static constexpr int kDepth = 2;
+
+  struct Stage {
+    u32x4 a[TL][W4 ? 1 : 2];
+    u32x2 sc[W4 ? TL : 1][kG];
+    u32x4 b[kLoads][P];
+  };
+
+  // col_row(c): B's row of column c.  Two buffers at lds.
+  template <class F>
+  static __device__ __forceinline__ void run(f32x4 (&acc)[TL][CT], const WeightK& w, const RowPtr<W4> (&ap)[TL],
+                                             F col_row, int64_t plane, int bend, char* lds) {
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int q8 = (lane >> 4) * 8, unit8 = tid % kUnits * 8;
+    const int kend = w.cols;
+    const int full = (W4 ? bend : min(kend, bend)) / kStep;
+    const int steps = (kend + kStep - 1) / kStep;
+    const uint8_t* abase[TL];
+    const uint16_t* scbase[TL];
+    uint32_t aoff[TL], scoff[TL];
+#pragma unroll
+    for (int t = 0; t < TL; ++t) {
+      abase[t] = ap[t].a;
+      scbase[t] = ap[t].sc;
+      aoff[t] = ap[t].a_off;
+      scoff[t] = ap[t].sc_off;
+      asm volatile("" : "+s"(abase[t]), "+v"(aoff[t]));
+      if constexpr (W4) asm volatile("" : "+s"(scbase[t]), "+v"(scoff[t]));
+    }
+    const uint16_t* row[kLoads];
+    char* write[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int col = (tid + i * kWideThreads) / kUnits;
+      row[i] = col_row(min(col, 16 * CT - 1));
+      write[i] = lds + min(col, 16 * CT - 1) * kPitch + unit8 * 2;
+    }
+    const char* read = lds + (lane & 15) * kPitch + q8 * 2;
+
+    auto load = [&](Stage& x, int s) {
+      const int k = CUT ? min(s * kStep + unit8, bend - 8) : s * kStep + unit8;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+#pragma unroll
+        for (int pl = 0; pl < P; ++pl) x.b[i][pl] = load8(row[i] + pl * plane + k);
+      }
+#pragma unroll
+      for (int t = 0; t < TL; ++t) {
+        if constexpr (W4) {
+          x.a[t][0] = gload<u32x4>(abase[t] + (int64_t)s * 1024 + aoff[t]);
+#pragma unroll
+          for (int g = 0; g < kG; ++g) {
+            const int group = CUT ? min(s * kG + g, (kend - 1) / (32 * GJ)) : s * kG + g;
+            x.sc[t][g] = load_scales<SHIFT>(scbase[t], scoff[t], ap[t].sc_off2, ap[t].sc_shift, group);
+          }
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int at = s * kStep + 32 * h;
+            const int back = CUT ? max(at + q8 + 8 - kend, 0) : 0;
+            x.a[t][h] = load8(abase[t] + (int64_t)at * 2 + (int32_t)(aoff[t] - back * 2));
+          }
+        }
+      }
+    };
+    auto compute = [&](const Stage& x, int s) {
+      const int buffer = (s & 1) * kBuffer;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+#pragma unroll
+        for (int pl = 0; pl < P; ++pl) {
+          u32x4 b = x.b[i][pl];
+          if (CUT && s >= full) b = cut8(b, bend - s * kStep - unit8);
+          *reinterpret_cast<u32x4*>(write[i] + buffer + pl * kUnits * 16) = b;
+        }
+      }
+      // The loads in flight stay in flight: only the LDS writes have to be done.
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+      auto operand_b = [&](int ct, int pl, int j) {
+        return *reinterpret_cast<const u32x4*>(read + buffer + ct * 16 * kPitch + pl * kUnits * 16 + j * 64);
+      };
+      if constexpr (W4) {
+        const u32x4 minus8 = {T::kMinus8, T::kMinus8, T::kMinus8, T::kMinus8};
+#pragma unroll
+        for (int g = 0; g < kG; ++g) {
+          u32x4 f[TL][GJ];
+          f32x4 sc[TL];
+#pragma unroll
+          for (int t = 0; t < TL; ++t) {
+            sc[t] = scale_floats<T>(x.sc[t][g]);
+#pragma unroll
+            for (int i = 0; i < GJ; ++i) f[t][i] = decode<T>(x.a[t][0][g * GJ + i]);
+          }
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) {
+            f32x4 corr = {0, 0, 0, 0}, part[TL];
+#pragma unroll
+            for (int t = 0; t < TL; ++t) part[t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < GJ; ++i) {
+#pragma unroll
+              for (int pl = 0; pl < P; ++pl) {
+                const u32x4 b = operand_b(ct, pl, g * GJ + i);
+                corr = T::mfma(minus8, b, corr);
+#pragma unroll
+                for (int t = 0; t < TL; ++t) part[t] = T::mfma(f[t][i], b, part[t]);
+              }
+            }
+#pragma unroll
+            for (int t = 0; t < TL; ++t) {
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                acc[t][ct][r] = __builtin_fmaf(sc[t][r], part[t][r] + corr[r], acc[t][ct][r]);
+            }
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      } else {
+        u32x4 f[TL][2];
+#pragma unroll
+        for (int t = 0; t < TL; ++t) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            f[t][h] = x.a[t][h];
+            if (CUT && s >= full) f[t][h] = cut8(f[t][h], kend - s * kStep - 32 * h - q8);
+          }
+        }
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+#pragma unroll
+          for (int pl = 0; pl < P; ++pl) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const u32x4 b = operand_b(ct, pl, h);
+#pragma unroll
+              for (int t = 0; t < TL; ++t) acc[t][ct] = T::mfma(f[t][h], b, acc[t][ct]);
+            }
+          }
+        }
+      }
+    };
+    Stage st[kDepth];
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) load(st[d], min(d, steps - 1));
+    for (int s = 0; s < steps; s += kDepth) {
+#pragma unroll
+      for (int d = 0; d < kDepth; ++d) {
+        if (s + d < steps) compute(st[d], s + d);
+        load(st[d], min(s + d + kDepth, steps - 1));      // past the last step: again, unused
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    __syncthreads();      // the buffers are free for the next pass
+  }
+};
+
+template <class T>
+__device__ __forceinline__ void store4(void* out, int64_t i, const f32x4& v, int f32, int have) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    if (r < have) store_out<T>(out, i + r, v[r], f32);
+  }
+}
+
+// A workgroup takes one expert (blockIdx.y) and kWideWaves * 2 tiles of 16
+// weight rows (kWideGated: as many gate as up tiles, a pair to a wave), lists
+// the expert's tokens and multiplies them 64 at a time (kWideDown, whose B has
+// two planes: 48), with as many columns as are left in the last pass.
+// kWideDown reads the activations of kWideGated and writes each pair's
+// weighted product, in float32, for sum_kernel.
+template <class T, int G, WideOp OP, bool SHIFT, bool CUT>
+__global__ void __launch_bounds__(kWideThreads, 2) wide_kernel(const RowsKArgs a) {
+  constexpr bool W4 = G != 0;
+  constexpr int TL = 2, P = OP == kWideDown ? 2 : 1, kMost = OP == kWideDown ? 3 : 4;
+  __shared__ int list[kPassTokens];
+  __shared__ Lister<kWideWaves> lister;
+  __shared__ __attribute__((aligned(16))) char bmem[2 * WideMac<T, G, SHIFT, CUT, P, kMost>::kBuffer];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int slot = blockIdx.y, k = a.top_k;
+  const int tiles = (a.inter + 15) >> 4;
+
+  int m = a.n, expert = 0;
+  if (a.ids == nullptr) {
+    for (int i = tid; i < a.n; i += kWideThreads) list[i] = i << 6;
+    __syncthreads();
+  } else {
+    const int id = a.by_pair ? __builtin_amdgcn_readfirstlane(a.ids[slot]) : a.offset + slot;
+    const bool inside = id >= a.offset && (int64_t)id - a.offset < a.num_experts;
+    expert = inside ? id - a.offset : 0;
+    m = 0;
+    if (inside) {
+      m = lister.run(a.ids, a.n * k, k, id, list);
+      if (a.by_pair && (list[0] >> 6) * k + (list[0] & 63) != slot) m = 0;
+    }
+  }
+  if (OP == kWideLinear && a.ids != nullptr && slot == 0) {
+    // rows of no expert here: zeros, written by the first slot's workgroups
+    const int c0 = blockIdx.x * kWideWaves * TL * 16, width = min(c0 + kWideWaves * TL * 16, a.inter) - c0;
+    for (int i = tid; i < a.n * width; i += kWideThreads) {
+      const int r = i / width, id = a.ids[r];
+      if (id < a.offset || (int64_t)id - a.offset >= a.num_experts)
+        store_out<T>(a.out, (int64_t)r * a.out_stride + c0 + i % width, 0.0f, a.out_f32);
+    }
+  }
+  m = __builtin_amdgcn_readfirstlane(m);
+  if (m == 0) return;
+
+  RowPtr<W4> ap[TL];
+  int tile[TL];           // of the output; past the last one: not stored
+#pragma unroll
+  for (int t = 0; t < TL; ++t) {
+    tile[t] = OP == kWideGated ? blockIdx.x * kWideWaves + wave : (blockIdx.x * kWideWaves + wave) * TL + t;
+    const int at = min(tile[t], tiles - 1) * 16;
+    ap[t] = row_ptr<W4>(a.w, expert, OP == kWideGated && t == 1 ? a.inter + at : at);
+  }
+  auto pass = [&](auto ct_c, int c0) {
+    constexpr int CT = decltype(ct_c)::value;
+    f32x4 acc[TL][CT];
+#pragma unroll
+    for (int t = 0; t < TL; ++t) {
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) acc[t][ct] = f32x4{0, 0, 0, 0};
+    }
+    auto col_row = [&](int c) -> const uint16_t* {      // columns past the list repeat its last token
+      const int at = list[min(c0 + c, m - 1)];
+      if constexpr (OP == kWideDown) return a.plan.act + ((int64_t)(at >> 6) * k + (at & 63)) * a.plan.act_stride;
+      else return a.x + (int64_t)(at >> 6) * a.x_stride;
+    };
+    WideMac<T, G, SHIFT, CUT, P, CT>::run(acc, a.w, ap, col_row, a.plan.act_plane,
+                                          OP == kWideDown ? a.plan.act_stride : a.w.cols, bmem);
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+      const int i = c0 + ct * 16 + (lane & 15);
+      if (i >= m) continue;
+      const int at = list[i];
+      const int64_t pair = (int64_t)(at >> 6) * k + (at & 63);
+      if constexpr (OP == kWideGated) {
+        if (tile[0] >= tiles) continue;
+        const int n = tile[0] * 16 + (lane >> 4) * 4;
+        uint16_t hi[4], lo[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float g = acc[0][ct][r], u = acc[1][ct][r];
+          // rows past the intermediate size are zeros: the down product reads whole 16-row tiles
+          T::split(n + r < a.inter ? g / (1.0f + expf(-g)) * u : 0.0f, &hi[r], &lo[r]);
+        }
+        uint16_t* o = a.plan.act + pair * a.plan.act_stride + n;      // a multiple of four elements
+        *reinterpret_cast<u32x2*>(o) = u32x2{hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16};
+        *reinterpret_cast<u32x2*>(o + a.plan.act_plane) =
+            u32x2{lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16};
+      } else {
+        float weight = 1.0f;
+        if constexpr (OP == kWideDown) weight = pair_weight(a, at, expert, lister.repeated);
+#pragma unroll
+        for (int t = 0; t < TL; ++t) {
+          const int n = tile[t] * 16 + (lane >> 4) * 4;
+          const int have = tile[t] < tiles ? a.inter - n : 0;
+          f32x4 v = acc[t][ct];
+          if constexpr (OP == kWideDown) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] *= weight;
+            float* o = a.pair_out + pair * a.pair_stride + n;         // a multiple of four elements
+            if (have > 0) *reinterpret_cast<f32x4*>(o) = v;           // pair_stride has room for a whole tile
+          } else {
+            store4<T>(a.out, (int64_t)(at >> 6) * a.out_stride + n, v, a.out_f32, have);
+          }
+        }
+      }
+    }
+  };
+  for (int c0 = 0; c0 < m; c0 += 16 * kMost) {
+    const int left = m - c0;
+    if (left <= 16) pass(std::integral_constant<int, 1>{}, c0);
+    else if (left <= 32) pass(std::integral_constant<int, 2>{}, c0);
+    else if (kMost == 3 || left <= 48) pass(std::integral_constant<int, 3>{}, c0);
+    else pass(std::integral_constant<int, kMost>{}, c0);
+  }
+}
+
+// out[t] = the sum of its pairs' products in slot order: those that name an
+// expert here, each expert once.
+template <class T>
+__global__ void __launch_bounds__(256) sum_kernel(const RowsKArgs a, int hidden) {
+  const int64_t t = blockIdx.y;
+  const int h = (blockIdx.x * 256 + threadIdx.x) * 4;
+  if (h >= hidden) return;
+  const int32_t* ids = a.ids + t * a.top_k;
+  f32x4 v = {0, 0, 0, 0};
+  for (int j = 0; j < a.top_k; ++j) {
+    const int id = ids[j];
+    bool have = id >= a.offset && (int64_t)id - a.offset < a.num_experts;
+    for (int i = 0; i < j; ++i) have &= ids[i] != id;
+    if (!have) continue;
+    const f32x4 y = *reinterpret_cast<const f32x4*>(a.pair_out + (t * a.top_k + j) * a.pair_stride + h);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r] += y[r];
+  }
+  store4<T>(a.out, t * a.out_stride + h, v, a.out_f32, hidden - h);
+}
+
 // ---- launches ---------------------------------------------------------------
 
 template <class T, int G, bool GATED>
@@ -762,6 +1093,40 @@ void start_rows(RowsKArgs a, hipStream_t stream) {
   }
   if (a.w.cols % Step<G != 0>::kCols != 0) rows_kernel<T, G, GATED, false, true><<<grid, kThreads, 0, stream>>>(a);
   else rows_kernel<T, G, GATED, false, false><<<grid, kThreads, 0, stream>>>(a);
+}
+
+template <class T, int G, WideOp OP>
+void start_wide(const RowsKArgs& a, hipStream_t stream) {
+  const int slots = a.ids == nullptr ? 1 : a.by_pair ? a.n * a.top_k : a.num_experts;
+  const int tiles = (a.inter + 15) / 16;
+  const int per = kWideWaves * (OP == kWideGated ? 1 : 2);
+  const dim3 grid((tiles + per - 1) / per, slots);
+  if constexpr (OP == kWideGated && G != 0) {
+    if (a.inter % 4 != 0) {
+      wide_kernel<T, G, OP, true, true><<<grid, kWideThreads, 0, stream>>>(a);
+      return;
+    }
+  }
+  if (a.w.cols % Step<G != 0>::kCols != 0) wide_kernel<T, G, OP, false, true><<<grid, kWideThreads, 0, stream>>>(a);
+  else wide_kernel<T, G, OP, false, false><<<grid, kWideThreads, 0, stream>>>(a);
+}
+
+template <class T, WideOp OP>
+hipError_t start_wide(const RowsKArgs& a, int group, hipStream_t stream) {
+  switch (group) {
+    case 0: start_wide<T, 0, OP>(a, stream); break;
+    case 32: start_wide<T, 32, OP>(a, stream); break;
+    case 64: start_wide<T, 64, OP>(a, stream); break;
+    default: start_wide<T, 128, OP>(a, stream); break;
+  }
+  return hipGetLastError();
+}
+
+template <class T>
+hipError_t start_sum(const RowsKArgs& a, int hidden, hipStream_t stream) {
+  const dim3 grid((hidden + 1023) / 1024, a.n);
+  sum_kernel<T><<<grid, 256, 0, stream>>>(a, hidden);
+  return hipGetLastError();
 }
 
 template <class T, bool GATED>
@@ -798,15 +1163,28 @@ hipError_t start_down(const DownKArgs& a, int group, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_expert_linear(const RowsKArgs& a, int dtype, int group, hipStream_t stream) {
+  if (a.wide)
+    return dtype == MOE_EP_BF16 ? start_wide<BF16, kWideLinear>(a, group, stream)
+                                : start_wide<F16, kWideLinear>(a, group, stream);
   return dtype == MOE_EP_BF16 ? start_rows<BF16, false>(a, group, stream) : start_rows<F16, false>(a, group, stream);
 }
 
 hipError_t launch_gate_up(const RowsKArgs& a, int dtype, int group, hipStream_t stream) {
+  if (a.wide)
+    return dtype == MOE_EP_BF16 ? start_wide<BF16, kWideGated>(a, group, stream)
+                                : start_wide<F16, kWideGated>(a, group, stream);
   return dtype == MOE_EP_BF16 ? start_rows<BF16, true>(a, group, stream) : start_rows<F16, true>(a, group, stream);
 }
 
 hipError_t launch_down(const DownKArgs& a, int dtype, int group, hipStream_t stream) {
   return dtype == MOE_EP_BF16 ? start_down<BF16>(a, group, stream) : start_down<F16>(a, group, stream);
+}
+
+hipError_t launch_wide_down(const RowsKArgs& a, int dtype, int group, hipStream_t stream) {
+  const hipError_t e = dtype == MOE_EP_BF16 ? start_wide<BF16, kWideDown>(a, group, stream)
+                                            : start_wide<F16, kWideDown>(a, group, stream);
+  if (e != hipSuccess) return e;
+  return dtype == MOE_EP_BF16 ? start_sum<BF16>(a, a.inter, stream) : start_sum<F16>(a, a.inter, stream);
 }
 
 }  // namespace moe_ep_detail

@@ -388,12 +388,14 @@ def moe_layer(hidden: torch.Tensor, gate_up: Weight, down: Weight, topk_ids: Opt
     return out
 
 
-def moe_layer_workspace_bytes(tokens: int, top_k: int, num_experts: int, intermediate: int,
-                              routed: bool = False) -> int:
-    """Bytes of workspace ``moe_layer`` takes for these sizes; ``routed``
-    when it is given router logits."""
+def moe_layer_workspace_bytes(tokens: int, top_k: int, num_experts: int, hidden: int, intermediate: int, *,
+                              group_size: int = 0, routed: bool = False) -> int:
+    """Bytes of workspace ``moe_layer`` takes for these sizes; ``group_size``
+    is that of a 4-bit ``gate_up`` (0: dense), ``routed`` when it is given
+    router logits."""
     a = _lib.moe_ep_layer_args()
-    a.num_tokens, a.top_k, a.num_experts, a.intermediate_size = tokens, top_k, num_experts, intermediate
+    a.num_tokens, a.top_k, a.num_experts = tokens, top_k, num_experts
+    a.hidden_size, a.intermediate_size, a.gate_up.group_size = hidden, intermediate, group_size
     if routed:
         a.router = ctypes.pointer(_lib.moe_ep_router())
     return _lib.moe_ep_layer_workspace_bytes(a)

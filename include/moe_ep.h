@@ -438,9 +438,9 @@ typedef struct moe_ep_layer_args {
   int32_t intermediate_size;      /* 8..2^24 */
 } moe_ep_layer_args;
 
-/* Bytes of device workspace moe_ep_layer needs for these sizes (num_tokens,
- * top_k, num_experts, intermediate_size and whether a router is set are
- * read; pointers are not followed). */
+/* Bytes of device workspace moe_ep_layer needs for these sizes (the sizes,
+ * gate_up.group_size and whether a router is set are read; pointers are not
+ * followed). */
 MOE_EP_API int moe_ep_layer_workspace_bytes(const moe_ep_layer_args* args, size_t* out_bytes);
 
 /* The experts of a mixture-of-experts layer, whole:
@@ -452,9 +452,8 @@ MOE_EP_API int moe_ep_layer_workspace_bytes(const moe_ep_layer_args* args, size_
  * rows dispatch left that rank it is the expert computation between
  * dispatch and combine, and out may be the rank's combine input buffer.
  *
- * Made for few tokens: each used expert's weights are read once per 2048
- * tokens (the down weights once per 128).  Two kernel launches per 2048
- * tokens, and a third for the router's choice.  out may be hidden itself
+ * Two kernel launches for few tokens, three for many to an expert (per 2048
+ * tokens), and one more for the router's choice.  out may be hidden itself
  * (same address, stride and type) but not overlap it otherwise.  The
  * workspace holds nothing between calls; calls that may overlap in time
  * (other streams, graphs replayed side by side) need one each.

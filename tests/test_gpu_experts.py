@@ -333,7 +333,7 @@ def test_layer_in_place_strides_and_workspace():
     want, tol = ref.layer(big[:, 3:3 + H], rg, rd, ids, w, 0, BF16, BF16)
     dev = big.cuda()
     x = dev[:, 3:3 + H]
-    nbytes = pkg.moe_layer_workspace_bytes(n, k, E, I)
+    nbytes = pkg.moe_layer_workspace_bytes(n, k, E, H, I)
     ws = torch.full((nbytes + 256,), 0xFF, dtype=torch.uint8, device="cuda")   # NaN bits in every type
     got = moe_layer(x, gu, dn, ids.cuda(), w.cuda(), workspace=ws[:nbytes])
     close(got, want, tol)
