@@ -168,16 +168,24 @@ constexpr int32_t kMaxSide = 1 << 24;
 constexpr int32_t kMinRow = 8;
 
 // Whether the kernels for many tokens to an expert take a pass of n tokens
-// with top_k experts each.  The narrow ones take four (4-bit) or eight (dense)
-// tokens at a time and read the weights again for each such pass, from L2 at
-// best; the wide ones read them once per 64 tokens, but a workgroup covers
-// `rows` of the weights' rows, and below some 512 workgroups the card is not
-// full.  (The experts' tokens are counted as if all of them were chosen here.)
-bool is_wide(int64_t n, int top_k, int64_t num_experts, int64_t rows_of_tiles, int rows, int group) {
-  const int64_t pairs = n * top_k, cols = group ? 4 : 8;
-  const int64_t passes = (pairs + num_experts * cols - 1) / (num_experts * cols);
-  const int64_t blocks = (rows_of_tiles + rows - 1) / rows * std::min(pairs, num_experts);
-  return passes > 1 && passes * blocks >= 512;
+// with top_k experts each (moe_experts_kernels.hip, wide_kernel).  The narrow
+// ones take four (4-bit) or eight (dense) tokens at a time and read the
+// weights again for each such pass, from L2 at best, but share a row's sum
+// over k between waves; the wide ones read the weights once per 64 tokens, but
+// a workgroup covers `tile_rows` of the weights' rows and goes through all of
+// k alone.  Measured, narrow / wide in us:
+//   layer, 64 experts, top-8, 4096 x 1024, 4 bits: 16 tokens 108 / 110, 32: 137 / 115, 128: 369 / 146
+//   the same dense:                                32 tokens 280 / 315, 64: 399 / 336, 128: 623 / 343
+//   one 4-bit matrix 4096 x 4096: 48 rows 27 / 33, 96: 50 / 37;  4096 x 1024: 12 rows 7.3 / 6.7, 48: 21 / 11
+//   one dense matrix 4096 x 4096: 48 rows 34 / 51, 96: 64 / 53;  4096 x 1024: 24 rows 10 / 13, 48: 18 / 14
+// (The experts' tokens are counted as if all of them were chosen here.)
+bool is_wide(int64_t n, int top_k, int64_t num_experts, int64_t rows, int tile_rows, int64_t cols, int group) {
+  const int64_t pairs = n * top_k;
+  const int64_t blocks = (rows + tile_rows - 1) / tile_rows * std::min(pairs, num_experts);
+  if (pairs >= num_experts * (group ? 3 : 6) && blocks >= 128) return true;
+  const int64_t at_once = num_experts * (group ? 4 : 8), passes = (pairs + at_once - 1) / at_once;
+  const int64_t steps = (cols + 63) / (group ? 128 : 64);
+  return passes > 1 && passes * blocks >= steps * (group ? 16 : 6);
 }
 
 // Workspace of one pass: [ids][weights] with a router, the plan, the
@@ -215,7 +223,8 @@ int make_space(const moe_ep_layer_args* a, LayerSpace* s) {
   s->head = take((int64_t)s->slots * kMaxChunks * 4);
   s->pair = take((int64_t)s->slots * s->n * 8);
   s->act = take(2 * pairs * s->act_stride * 2);
-  s->wide = is_wide(s->n, a->top_k, a->num_experts, a->intermediate_size, kWideWaves * 16, a->gate_up.group_size);
+  s->wide = is_wide(s->n, a->top_k, a->num_experts, a->intermediate_size, kWideWaves * 16,
+                    a->hidden_size, a->gate_up.group_size);
   s->pair_stride = up(a->hidden_size, 16);
   s->pair_out = take(s->wide ? pairs * s->pair_stride * 4 : 0);
   s->total = std::max<int64_t>(off, 256);
@@ -283,7 +292,8 @@ int moe_ep_expert_linear(const moe_ep_linear_args* a, void* stream) {
     k.out = static_cast<uint8_t*>(a->out) + t * a->out_stride * out_esz;
     k.ids = a->expert_ids ? a->expert_ids + t : nullptr;
     k.by_pair = k.n <= a->num_experts;
-    k.wide = is_wide(k.n, 1, k.ids ? a->num_experts : 1, a->out_features, kWideWaves * 32, a->weight.group_size);
+    k.wide = is_wide(k.n, 1, k.ids ? a->num_experts : 1, a->out_features, kWideWaves * 32, a->in_features,
+                     a->weight.group_size);
     const hipError_t e = launch_expert_linear(k, a->dtype, a->weight.group_size, static_cast<hipStream_t>(stream));
     if (e != hipSuccess) return report(MOE_EP_ERR_HIP, "expert_linear launch failed: %s", hipGetErrorString(e));
   }

@@ -457,6 +457,22 @@ struct alignas(8) PairRec {
   float weight;
 };
 
+// Columns [c0, c1) of the rows of no expert here are zeros; written by the
+// first slot's workgroups of W waves.
+template <class T, int W>
+__device__ __forceinline__ void zero_rows(const RowsKArgs& a, int c0, int c1) {
+  const int lane = threadIdx.x & 63;
+  for (int base = (threadIdx.x >> 6) * 64; base < a.n; base += W * 64) {
+    const int id = a.ids[min(base + lane, a.n - 1)];
+    uint64_t left = __ballot(base + lane < a.n && (id < a.offset || (int64_t)id - a.offset >= a.num_experts));
+    while (left) {
+      const int64_t row = base + __builtin_ctzll(left);
+      left &= left - 1;
+      for (int c = c0 + lane; c < c1; c += 64) store_out<T>(a.out, row * a.out_stride + c, 0.0f, a.out_f32);
+    }
+  }
+}
+
 // The weight of a listed pair: the sum of its token's weights for the expert.
 __device__ __forceinline__ float pair_weight(const RowsKArgs& a, int pair, int expert, int repeated) {
   const int64_t row = (int64_t)(pair >> 6) * a.top_k;
@@ -555,13 +571,7 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const RowsKArgs a) {
       }
     }
   } else if (a.ids != nullptr && slot == 0) {
-    // rows of no expert here: zeros, written by the first slot's workgroups
-    const int c0 = tile0 * 16, width = min(tile1 * 16, a.inter) - c0;
-    for (int i = tid; i < a.n * width; i += kThreads) {
-      const int r = i / width, id = a.ids[r];
-      if (id < a.offset || (int64_t)id - a.offset >= a.num_experts)
-        store_out<T>(a.out, (int64_t)r * a.out_stride + c0 + i % width, 0.0f, a.out_f32);
-    }
+    zero_rows<T, kExpertWaves>(a, tile0 * 16, min(tile1 * 16, a.inter));
   }
   if (m == 0) return;
 
@@ -920,12 +930,27 @@ struct WideMac {
   }
 };
 
+// Four elements of a row, `have` of which exist; whole: rows and their starts
+// are on multiples of four elements.
 template <class T>
-__device__ __forceinline__ void store4(void* out, int64_t i, const f32x4& v, int f32, int have) {
+__device__ __forceinline__ void store4(void* out, int64_t i, const f32x4& v, int f32, int have, bool whole) {
+  if (whole && have >= 4) {
+    if (f32) {
+      *reinterpret_cast<f32x4*>(static_cast<float*>(out) + i) = v;
+    } else {
+      *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(out) + i) =
+          u32x2{T::from_float(v[0]) | (uint32_t)T::from_float(v[1]) << 16,
+                T::from_float(v[2]) | (uint32_t)T::from_float(v[3]) << 16};
+    }
+    return;
+  }
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     if (r < have) store_out<T>(out, i + r, v[r], f32);
   }
+}
+__device__ __forceinline__ bool whole_rows(const RowsKArgs& a) {
+  return ((reinterpret_cast<uintptr_t>(a.out) / (a.out_f32 ? 4 : 2)) | (uintptr_t)a.out_stride) % 4 == 0;
 }
 
 // A workgroup takes one expert (blockIdx.y) and kWideWaves * 2 tiles of 16
@@ -961,17 +986,13 @@ __global__ void __launch_bounds__(kWideThreads, 2) wide_kernel(const RowsKArgs a
     }
   }
   if (OP == kWideLinear && a.ids != nullptr && slot == 0) {
-    // rows of no expert here: zeros, written by the first slot's workgroups
-    const int c0 = blockIdx.x * kWideWaves * TL * 16, width = min(c0 + kWideWaves * TL * 16, a.inter) - c0;
-    for (int i = tid; i < a.n * width; i += kWideThreads) {
-      const int r = i / width, id = a.ids[r];
-      if (id < a.offset || (int64_t)id - a.offset >= a.num_experts)
-        store_out<T>(a.out, (int64_t)r * a.out_stride + c0 + i % width, 0.0f, a.out_f32);
-    }
+    const int c0 = blockIdx.x * kWideWaves * TL * 16;
+    zero_rows<T, kWideWaves>(a, c0, min(c0 + kWideWaves * TL * 16, a.inter));
   }
   m = __builtin_amdgcn_readfirstlane(m);
   if (m == 0) return;
 
+  const bool whole = whole_rows(a);
   RowPtr<W4> ap[TL];
   int tile[TL];           // of the output; past the last one: not stored
 #pragma unroll
@@ -1029,13 +1050,14 @@ __global__ void __launch_bounds__(kWideThreads, 2) wide_kernel(const RowsKArgs a
             float* o = a.pair_out + pair * a.pair_stride + n;         // a multiple of four elements
             if (have > 0) *reinterpret_cast<f32x4*>(o) = v;           // pair_stride has room for a whole tile
           } else {
-            store4<T>(a.out, (int64_t)(at >> 6) * a.out_stride + n, v, a.out_f32, have);
+            store4<T>(a.out, (int64_t)(at >> 6) * a.out_stride + n, v, a.out_f32, have, whole);
           }
         }
       }
     }
   };
-  for (int c0 = 0; c0 < m; c0 += 16 * kMost) {
+  // (one expert for all rows: its passes are workgroups of their own)
+  for (int c0 = blockIdx.z * 16 * kMost; c0 < m; c0 += gridDim.z * 16 * kMost) {
     const int left = m - c0;
     if (left <= 16) pass(std::integral_constant<int, 1>{}, c0);
     else if (left <= 32) pass(std::integral_constant<int, 2>{}, c0);
@@ -1062,7 +1084,7 @@ __global__ void __launch_bounds__(256) sum_kernel(const RowsKArgs a, int hidden)
 #pragma unroll
     for (int r = 0; r < 4; ++r) v[r] += y[r];
   }
-  store4<T>(a.out, t * a.out_stride + h, v, a.out_f32, hidden - h);
+  store4<T>(a.out, t * a.out_stride + h, v, a.out_f32, hidden - h, whole_rows(a));
 }
 
 // ---- launches ---------------------------------------------------------------
@@ -1100,7 +1122,7 @@ void start_wide(const RowsKArgs& a, hipStream_t stream) {
   const int slots = a.ids == nullptr ? 1 : a.by_pair ? a.n * a.top_k : a.num_experts;
   const int tiles = (a.inter + 15) / 16;
   const int per = kWideWaves * (OP == kWideGated ? 1 : 2);
-  const dim3 grid((tiles + per - 1) / per, slots);
+  const dim3 grid((tiles + per - 1) / per, slots, a.ids == nullptr ? (a.n + 63) / 64 : 1);
   if constexpr (OP == kWideGated && G != 0) {
     if (a.inter % 4 != 0) {
       wide_kernel<T, G, OP, true, true><<<grid, kWideThreads, 0, stream>>>(a);
