@@ -35,6 +35,10 @@ __device__ __forceinline__ V gload(const void* p) {
   return *reinterpret_cast<const __attribute__((address_space(1))) V*>(reinterpret_cast<uintptr_t>(p));
 }
 
+// A value that is the same in all lanes, as a scalar (the compiler divides in
+// vector registers).
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
 // A 16-byte load of 16-bit elements from any element address (gfx950 takes
 // unaligned global loads; aligned ones cost nothing extra).
 struct __attribute__((packed, aligned(2))) Elems8 {
@@ -161,7 +165,7 @@ struct Mac {
   static constexpr int kPitch = P * kUnits * 16 + 16;     // bytes from column to column in LDS
   static constexpr int kLds = kCols * kPitch;             // a wave's piece
   static constexpr int kStageRegs = (W4 ? TL * (4 + 2 * kG) : TL * 8) + P * 4;
-  static constexpr int kDepth = TL == 2 ? (W4 ? 2 : 3) : 64 / kStageRegs;   // within 128 registers
+  static constexpr int kDepth = TL == 2 ? (W4 ? 2 : 3) : (CUT ? 48 : 64) / kStageRegs;   // within 128 registers
 
   struct Stage {
     u32x4 a[TL][W4 ? 1 : 2];
@@ -198,7 +202,7 @@ struct Mac {
   }
   __device__ __forceinline__ Item item(int s0, int s1, int ds) const {
     // one without steps still loads: step 0
-    return s0 < s1 ? Item{s0, ds, (s1 - s0 + ds - 1) / ds} : Item{0, 0, 0};
+    return s0 < s1 ? Item{s0, ds, uniform((s1 - s0 + ds - 1) / ds)} : Item{0, 0, 0};
   }
   // The column whose row this lane loads.
   static __device__ __forceinline__ int load_col() { return (threadIdx.x & 63) / kUnits; }
@@ -290,27 +294,33 @@ struct Mac {
     if constexpr (W4) {
 #pragma unroll
       for (int g = 0; g < kG; ++g) {
+        // -8 times the columns' sums, then the nibbles on top of it
         f32x4 corr = {0, 0, 0, 0}, part[TL];
+        u32x4 b[GJ][P];
 #pragma unroll
-        for (int t = 0; t < TL; ++t) part[t] = f32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int j = g * GJ; j < (g + 1) * GJ; ++j) {
-          u32x4 f[TL];
-#pragma unroll
-          for (int t = 0; t < TL; ++t) f[t] = decode<T>(x.a[t][0][j]);
+        for (int i = 0; i < GJ; ++i) {
 #pragma unroll
           for (int pl = 0; pl < P; ++pl) {
-            const u32x4 b = operand_b(pl, j);
-            corr = T::mfma(minus8, b, corr);
+            b[i][pl] = operand_b(pl, g * GJ + i);
+            corr = T::mfma(minus8, b[i][pl], corr);
+          }
+        }
 #pragma unroll
-            for (int t = 0; t < TL; ++t) part[t] = T::mfma(f[t], b, part[t]);
+        for (int t = 0; t < TL; ++t) part[t] = corr;
+#pragma unroll
+        for (int i = 0; i < GJ; ++i) {
+#pragma unroll
+          for (int t = 0; t < TL; ++t) {
+            const u32x4 f = decode<T>(x.a[t][0][g * GJ + i]);
+#pragma unroll
+            for (int pl = 0; pl < P; ++pl) part[t] = T::mfma(f, b[i][pl], part[t]);
           }
         }
 #pragma unroll
         for (int t = 0; t < TL; ++t) {
           const f32x4 sc = scale_floats<T>(x.sc[t][g]);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc[t][r] = __builtin_fmaf(sc[r], part[t][r] + corr[r], acc[t][r]);
+          for (int r = 0; r < 4; ++r) acc[t][r] = __builtin_fmaf(sc[r], part[t][r], acc[t][r]);
         }
         // Groups one after another: interleaved they need more registers than there are.
         if constexpr (kG > 1) __builtin_amdgcn_sched_barrier(0);
@@ -503,8 +513,8 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const RowsKArgs a) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int slot = blockIdx.y, k = a.top_k;
-  const int split = a.split, group = kExpertWaves / split;      // waves to a tile, tiles at once
-  const int part = wave % split, mine = wave / split;
+  const int split = a.split, group = uniform(kExpertWaves / split);      // waves to a tile, tiles at once
+  const int part = uniform(wave % split), mine = uniform(wave / split);
   const int tiles = (a.inter + 15) >> 4;
   const int tile0 = blockIdx.x * a.tiles_per_block;
   const int tile1 = min(tile0 + a.tiles_per_block, tiles);
@@ -643,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 4) down_kernel(const DownKArgs a) {
   // Workgroups go round the 8 XCDs in turn: the chunks of one tile follow one
   // another on one XCD, where they find the tile's weights in its L2.
   const int xcd = blockIdx.x & 7, seq = blockIdx.x >> 3;
-  const int chunk = seq % a.chunks, tile = (seq / a.chunks) * 8 + xcd;
+  const int chunk = uniform(seq % a.chunks), tile = uniform(seq / a.chunks) * 8 + xcd;
   if (tile >= a.tiles) return;
   const int t0 = chunk * kChunkTokens;
   const int nc = min(a.n - t0, kChunkTokens);
@@ -677,8 +687,8 @@ __global__ void __launch_bounds__(kThreads, 4) down_kernel(const DownKArgs a) {
   float* mine = sums + wave * nc * 16;
   const int steps = (a.w.cols + Step<W4>::kCols - 1) / Step<W4>::kCols;
   const int64_t all = (int64_t)used * steps;
-  int s = (int)(all * wave / kExpertWaves);
-  const int end = (int)(all * (wave + 1) / kExpertWaves);
+  int s = uniform((int)(all * wave / kExpertWaves));
+  const int end = uniform((int)(all * (wave + 1) / kExpertWaves));
 
   // One product of the run: an expert's k steps [k0, k1) with 16 of its tokens.
   struct Item {
@@ -688,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 4) down_kernel(const DownKArgs a) {
   int col0 = 0;
   auto next = [&](Item& it) -> bool {
     if (s >= end) return false;
-    const int i = s / steps;
+    const int i = uniform(s / steps);
     const int head = __builtin_amdgcn_readfirstlane(heads[i]), slot = __builtin_amdgcn_readfirstlane((int)slots[i]);
     const int m = head_count(head);
     it.expert = head_expert(head);
@@ -870,23 +880,29 @@ struct WideMac {
 #pragma unroll
           for (int ct = 0; ct < CT; ++ct) {
             f32x4 corr = {0, 0, 0, 0}, part[TL];
-#pragma unroll
-            for (int t = 0; t < TL; ++t) part[t] = f32x4{0, 0, 0, 0};
+            u32x4 b[GJ][P];
 #pragma unroll
             for (int i = 0; i < GJ; ++i) {
 #pragma unroll
               for (int pl = 0; pl < P; ++pl) {
-                const u32x4 b = operand_b(ct, pl, g * GJ + i);
-                corr = T::mfma(minus8, b, corr);
+                b[i][pl] = operand_b(ct, pl, g * GJ + i);
+                corr = T::mfma(minus8, b[i][pl], corr);
+              }
+            }
 #pragma unroll
-                for (int t = 0; t < TL; ++t) part[t] = T::mfma(f[t][i], b, part[t]);
+            for (int t = 0; t < TL; ++t) part[t] = corr;
+#pragma unroll
+            for (int i = 0; i < GJ; ++i) {
+#pragma unroll
+              for (int pl = 0; pl < P; ++pl) {
+#pragma unroll
+                for (int t = 0; t < TL; ++t) part[t] = T::mfma(f[t][i], b[i][pl], part[t]);
               }
             }
 #pragma unroll
             for (int t = 0; t < TL; ++t) {
 #pragma unroll
-              for (int r = 0; r < 4; ++r)
-                acc[t][ct][r] = __builtin_fmaf(sc[t][r], part[t][r] + corr[r], acc[t][ct][r]);
+              for (int r = 0; r < 4; ++r) acc[t][ct][r] = __builtin_fmaf(sc[t][r], part[t][r], acc[t][ct][r]);
             }
           }
           __builtin_amdgcn_sched_barrier(0);
@@ -917,7 +933,10 @@ struct WideMac {
     };
     Stage st[kDepth];
 #pragma unroll
-    for (int d = 0; d < kDepth; ++d) load(st[d], min(d, steps - 1));
+    for (int d = 0; d < kDepth; ++d) {
+      load(st[d], min(d, steps - 1));
+      __builtin_amdgcn_sched_barrier(0);      // one step's loads after another's, as in the loop
+    }
     for (int s = 0; s < steps; s += kDepth) {
 #pragma unroll
       for (int d = 0; d < kDepth; ++d) {
@@ -1056,7 +1075,6 @@ __global__ void __launch_bounds__(kWideThreads, 2) wide_kernel(const RowsKArgs a
       }
     }
   };
-  // (one expert for all rows: its passes are workgroups of their own)
   for (int c0 = blockIdx.z * 16 * kMost; c0 < m; c0 += gridDim.z * 16 * kMost) {
     const int left = m - c0;
     if (left <= 16) pass(std::integral_constant<int, 1>{}, c0);
@@ -1071,15 +1089,16 @@ __global__ void __launch_bounds__(kWideThreads, 2) wide_kernel(const RowsKArgs a
 template <class T>
 __global__ void __launch_bounds__(256) sum_kernel(const RowsKArgs a, int hidden) {
   const int64_t t = blockIdx.y;
+  const int lane = threadIdx.x & 63;
+  const int id = a.ids[t * a.top_k + min(lane, a.top_k - 1)];
+  bool first = lane < a.top_k && id >= a.offset && (int64_t)id - a.offset < a.num_experts;
+  for (int i = 0; i < a.top_k; ++i) first &= i >= lane || __builtin_amdgcn_readlane(id, i) != id;
+  const uint64_t mask = __ballot(first);        // the slots to sum
   const int h = (blockIdx.x * 256 + threadIdx.x) * 4;
   if (h >= hidden) return;
-  const int32_t* ids = a.ids + t * a.top_k;
   f32x4 v = {0, 0, 0, 0};
-  for (int j = 0; j < a.top_k; ++j) {
-    const int id = ids[j];
-    bool have = id >= a.offset && (int64_t)id - a.offset < a.num_experts;
-    for (int i = 0; i < j; ++i) have &= ids[i] != id;
-    if (!have) continue;
+  for (uint64_t left = mask; left; left &= left - 1) {
+    const int j = __builtin_ctzll(left);
     const f32x4 y = *reinterpret_cast<const f32x4*>(a.pair_out + (t * a.top_k + j) * a.pair_stride + h);
 #pragma unroll
     for (int r = 0; r < 4; ++r) v[r] += y[r];
@@ -1122,7 +1141,14 @@ void start_wide(const RowsKArgs& a, hipStream_t stream) {
   const int slots = a.ids == nullptr ? 1 : a.by_pair ? a.n * a.top_k : a.num_experts;
   const int tiles = (a.inter + 15) / 16;
   const int per = kWideWaves * (OP == kWideGated ? 1 : 2);
-  const dim3 grid((tiles + per - 1) / per, slots, a.ids == nullptr ? (a.n + 63) / 64 : 1);
+  // The passes over an expert's tokens go to workgroups of their own (they
+  // meet in L2) as long as the card has room: as many as all experts' tokens
+  // evenly spread would take (layer, 695 tokens of 4 of 8 experts, 1784 x 200, 4
+  // bits: 98 us; 258 us with one workgroup for all passes).
+  const int64_t blocks = (int64_t)((tiles + per - 1) / per) * slots;
+  const int64_t experts = a.ids == nullptr ? 1 : a.num_experts;
+  const int64_t passes = ((int64_t)a.n * a.top_k + experts * 64 - 1) / (experts * 64);
+  const dim3 grid((tiles + per - 1) / per, slots, (unsigned)std::max<int64_t>(1, std::min(passes, 2048 / blocks)));
   if constexpr (OP == kWideGated && G != 0) {
     if (a.inter % 4 != 0) {
       wide_kernel<T, G, OP, true, true><<<grid, kWideThreads, 0, stream>>>(a);
