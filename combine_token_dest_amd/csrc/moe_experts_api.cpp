@@ -171,21 +171,21 @@ constexpr int32_t kMinRow = 8;
 // with top_k experts each (moe_experts_kernels.hip, wide_kernel).  The narrow
 // ones take four (4-bit) or eight (dense) tokens at a time and read the
 // weights again for each such pass, from L2 at best, but share a row's sum
-// over k between waves; the wide ones read the weights once per 64 tokens, but
+// over k between waves; the wide ones read the weights once per 48 tokens, but
 // a workgroup covers `tile_rows` of the weights' rows and goes through all of
 // k alone.  Measured, narrow / wide in us:
-//   layer, 64 experts, top-8, 4096 x 1024, 4 bits: 16 tokens 108 / 110, 32: 137 / 115, 128: 369 / 146
-//   the same dense:                                32 tokens 280 / 315, 64: 399 / 336, 128: 623 / 343
-//   one 4-bit matrix 4096 x 4096: 48 rows 27 / 33, 96: 50 / 37;  4096 x 1024: 12 rows 7.3 / 6.7, 48: 21 / 11
-//   one dense matrix 4096 x 4096: 48 rows 34 / 51, 96: 64 / 53;  4096 x 1024: 24 rows 10 / 13, 48: 18 / 14
+//   layer, 64 experts, top-8, 4096 x 1024, 4 bits: 8 tokens 78 / 82, 16: 90 / 90, 32: 138 / 104, 128: 379 / 134
+//   the same dense:                                32 tokens 284 / 315, 64: 382 / 325, 128: 628 / 339
+//   one 4-bit matrix 4096 x 4096: 24 rows 15 / 20, 48: 27 / 27, 96: 50 / 27;  4096 x 1024: 12 rows 7.3 / 6.0
+//   one dense matrix 4096 x 4096: 48 rows 33 / 35, 96: 63 / 35;  4096 x 1024: 12 rows 7.6 / 11, 48: 17 / 11
 // (The experts' tokens are counted as if all of them were chosen here.)
 bool is_wide(int64_t n, int top_k, int64_t num_experts, int64_t rows, int tile_rows, int64_t cols, int group) {
   const int64_t pairs = n * top_k;
   const int64_t blocks = (rows + tile_rows - 1) / tile_rows * std::min(pairs, num_experts);
-  if (pairs >= num_experts * (group ? 3 : 6) && blocks >= 128) return true;
+  if (pairs >= num_experts * (group ? 2 : 6) && blocks >= 128) return true;
   const int64_t at_once = num_experts * (group ? 4 : 8), passes = (pairs + at_once - 1) / at_once;
-  const int64_t steps = (cols + 63) / (group ? 128 : 64);
-  return passes > 1 && passes * blocks >= steps * (group ? 16 : 6);
+  const int64_t steps = group ? (cols + 127) / 128 : (cols + 63) / 64;
+  return passes > (group ? 1 : 2) && passes * blocks >= steps * (group ? 12 : 4);
 }
 
 // Workspace of one pass: [ids][weights] with a router, the plan, the

@@ -388,6 +388,11 @@ __device__ __forceinline__ void store_out(void* out, int64_t i, float v, int f32
 
 // The pairs (token, top-k slot) that name an expert, in ascending order and
 // each token once: list[i] = token << 6 | slot.  Called by a whole workgroup.
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+struct __attribute__((packed, aligned(4))) Ints4 {
+  i32x4 v;
+};
+
 template <int W>                         // waves of the workgroup
 struct Lister {
   static constexpr int kUnroll = 4;     // loads in flight per thread
@@ -411,10 +416,79 @@ struct Lister {
     return __popcll(mask);
   }
 
+  // Any number of pairs.  More than one round of run_by_one: 16 a thread at a
+  // time (8192 pairs, four waves: two rounds for eight); where a token names the
+  // expert twice then (rare), or more pairs name it than there are tokens, the
+  // list is made again by run_by_one.
   __device__ __forceinline__ int run(const int32_t* ids, int pairs, int top_k, int id, int* list) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const uint64_t below = (1ull << lane) - 1;
     int m = 0;
     if (tid == 0) repeated = 0;
+    if (pairs <= W * 64 * kUnroll) return run_by_one(ids, pairs, top_k, id, list);
+    for (int base = 0; base < pairs; base += W * 64 * 4 * kUnroll) {
+      int v[kUnroll][4];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int p = base + (u * W * 64 + tid) * 4;
+        if (p + 4 <= pairs) {
+          const i32x4 w = reinterpret_cast<const Ints4*>(ids + p)->v;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) v[u][c] = w[c];
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) v[u][c] = ids[min(p + c, pairs - 1)];
+        }
+      }
+      __syncthreads();
+      int ahead[kUnroll];             // hits of lower lanes
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int p = base + (u * W * 64 + tid) * 4;
+        int all = 0;
+        ahead[u] = 0;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          v[u][c] = p + c < pairs && v[u][c] == id;
+          const uint64_t mask = __ballot(v[u][c]);
+          all += __popcll(mask);
+          ahead[u] += __popcll(mask & below);
+        }
+        if (lane == 0) count[u][wave] = all;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        int pos = m + ahead[u];
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          const int c = count[u][w];
+          pos += w < wave ? c : 0;
+          m += c;
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (!v[u][c]) continue;
+          const int p = base + (u * W * 64 + tid) * 4 + c;
+          const int tok = (int)((uint32_t)p / (uint32_t)top_k);
+          if (pos < kPassTokens) list[pos] = tok << 6 | (p - tok * top_k);
+          ++pos;
+        }
+      }
+    }
+    __syncthreads();
+    bool twice = m > kPassTokens;
+    if (top_k > 1 && !twice) {
+      for (int i = tid + 1; i < m; i += W * 64) twice |= list[i] >> 6 == list[i - 1] >> 6;
+    }
+    if (!__syncthreads_or(twice)) return m;
+    return run_by_one(ids, pairs, top_k, id, list);
+  }
+
+  // One pair a thread at a time, each token once.
+  __device__ __forceinline__ int run_by_one(const int32_t* ids, int pairs, int top_k, int id, int* list) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    int m = 0;
     for (int base = 0; base < pairs; base += W * 64 * kUnroll) {
       int v[kUnroll], tok[kUnroll], slot[kUnroll];
       uint64_t mask[kUnroll];
@@ -764,6 +838,11 @@ __global__ void __launch_bounds__(kThreads, 4) down_kernel(const DownKArgs a) {
 constexpr int kWideThreads = kWideWaves * 64;
 
 // What a wide workgroup computes.
+// Most tiles of 16 columns in a pass: 48 columns leave registers for three
+// workgroups on a compute unit, 64 for two (gate and up of 32 experts, 4096 x
+// 7168, 4 bits, 32 tokens each: 208 and 212 us).
+constexpr int kWideTiles = 3;
+
 enum WideOp { kWideLinear, kWideGated, kWideDown };
 
 // One pass of a workgroup: kWideWaves * TL tiles of 16 weight rows, TL to a
@@ -974,14 +1053,14 @@ __device__ __forceinline__ bool whole_rows(const RowsKArgs& a) {
 
 // A workgroup takes one expert (blockIdx.y) and kWideWaves * 2 tiles of 16
 // weight rows (kWideGated: as many gate as up tiles, a pair to a wave), lists
-// the expert's tokens and multiplies them 64 at a time (kWideDown, whose B has
-// two planes: 48), with as many columns as are left in the last pass.
+// the expert's tokens and multiplies them 48 at a time, with as many columns as
+// are left in the last pass.
 // kWideDown reads the activations of kWideGated and writes each pair's
 // weighted product, in float32, for sum_kernel.
 template <class T, int G, WideOp OP, bool SHIFT, bool CUT>
-__global__ void __launch_bounds__(kWideThreads, 2) wide_kernel(const RowsKArgs a) {
+__global__ void __launch_bounds__(kWideThreads, OP == kWideDown ? 2 : 3) wide_kernel(const RowsKArgs a) {
   constexpr bool W4 = G != 0;
-  constexpr int TL = 2, P = OP == kWideDown ? 2 : 1, kMost = OP == kWideDown ? 3 : 4;
+  constexpr int TL = 2, P = OP == kWideDown ? 2 : 1, kMost = kWideTiles;
   __shared__ int list[kPassTokens];
   __shared__ Lister<kWideWaves> lister;
   __shared__ __attribute__((aligned(16))) char bmem[2 * WideMac<T, G, SHIFT, CUT, P, kMost>::kBuffer];
@@ -1079,7 +1158,6 @@ __global__ void __launch_bounds__(kWideThreads, 2) wide_kernel(const RowsKArgs a
     const int left = m - c0;
     if (left <= 16) pass(std::integral_constant<int, 1>{}, c0);
     else if (left <= 32) pass(std::integral_constant<int, 2>{}, c0);
-    else if (kMost == 3 || left <= 48) pass(std::integral_constant<int, 3>{}, c0);
     else pass(std::integral_constant<int, kMost>{}, c0);
   }
 }
@@ -1141,14 +1219,17 @@ void start_wide(const RowsKArgs& a, hipStream_t stream) {
   const int slots = a.ids == nullptr ? 1 : a.by_pair ? a.n * a.top_k : a.num_experts;
   const int tiles = (a.inter + 15) / 16;
   const int per = kWideWaves * (OP == kWideGated ? 1 : 2);
-  // The passes over an expert's tokens go to workgroups of their own (they
-  // meet in L2) as long as the card has room: as many as all experts' tokens
-  // evenly spread would take (layer, 695 tokens of 4 of 8 experts, 1784 x 200, 4
-  // bits: 98 us; 258 us with one workgroup for all passes).
+  // The passes over an expert's tokens go to workgroups of their own while
+  // these fill the card (they meet in L2; layer, 695 tokens of 4 of 8 experts,
+  // 1784 x 200, 4 bits: 98 us, and 258 with one workgroup for all passes), as
+  // many as all experts' tokens evenly spread would take.  Once the card is
+  // full they would only come too late to find the weights in L2 (32 dense
+  // matrices 2048 x 2048, 96 rows each: 139 us, and 103 in one workgroup).
   const int64_t blocks = (int64_t)((tiles + per - 1) / per) * slots;
   const int64_t experts = a.ids == nullptr ? 1 : a.num_experts;
-  const int64_t passes = ((int64_t)a.n * a.top_k + experts * 64 - 1) / (experts * 64);
-  const dim3 grid((tiles + per - 1) / per, slots, (unsigned)std::max<int64_t>(1, std::min(passes, 2048 / blocks)));
+  const int64_t at_once = experts * kWideTiles * 16;
+  const int64_t passes = ((int64_t)a.n * a.top_k + at_once - 1) / at_once;
+  const dim3 grid((tiles + per - 1) / per, slots, (unsigned)std::max<int64_t>(1, std::min(passes, 512 / blocks)));
   if constexpr (OP == kWideGated && G != 0) {
     if (a.inter % 4 != 0) {
       wide_kernel<T, G, OP, true, true><<<grid, kWideThreads, 0, stream>>>(a);

@@ -292,7 +292,7 @@ def test_layer_of_one_rank(g):
     assert torch.equal(got64, moe_layer(x.cuda(), gu, dn, ids.cuda().clamp(-1, 2 ** 30), w.cuda(), expert_offset=offset))
 
 
-@pytest.mark.parametrize("n,E,k", [(2100, 4, 2), (300, 300, 3)])
+@pytest.mark.parametrize("n,E,k", [(2100, 4, 2), (300, 300, 3), (1000, 20, 9)])
 def test_layer_many_tokens(n, E, k):
     """More tokens than a pass, and more experts than a block has threads' worth of slots."""
     H, I = 40, 24
@@ -303,6 +303,23 @@ def test_layer_many_tokens(n, E, k):
     w = torch.rand(n, k, generator=gen(6))
     want, tol = ref.layer(x, rg, rd, ids, w, 0, BF16, BF16)
     close(moe_layer(x.cuda(), gu, dn, ids.cuda(), w.cuda()), want, tol)
+
+
+@pytest.mark.parametrize("g", [0, 32])
+@pytest.mark.parametrize("n,k", [(3, 4), (20, 8), (600, 4)])
+def test_layer_ids_named_by_every_slot(n, k, g):
+    """One expert in all slots of all tokens: more pairs than tokens, each token once."""
+    E, H, I = 3, 40, 24
+    x = rand(1, n, H)
+    rg, gu = make_weight(3, E, 2 * I, H, BF16, g)
+    rd, dn = make_weight(4, E, H, I, BF16, g)
+    ids = torch.full((n, k), 1, dtype=torch.int32)
+    w = torch.rand(n, k, generator=gen(6))
+    want, tol = ref.layer(x, rg, rd, ids[:, :1], w.double().sum(1, keepdim=True), 0, BF16, BF16)
+    # the k weights are added in float32 first
+    tol = tol + k * 2.0 ** -24 * want.abs()
+    close(moe_layer(x.cuda(), gu, dn, ids.cuda(), w.cuda()), want, tol)
+    assert torch.equal(moe_layer(x.cuda(), gu, dn, ids.cuda() + 7, w.cuda()), torch.zeros(n, H, dtype=BF16, device="cuda"))
 
 
 @pytest.mark.parametrize("n", [1, 6, 40])
@@ -340,6 +357,49 @@ def test_layer_in_place_strides_and_workspace():
     assert (ws[nbytes:] == 0xFF).all()
     close(moe_layer(x, gu, dn, ids.cuda(), w.cuda(), out=x), want, tol, "in place")
     assert torch.equal(dev[:, :3].cpu(), big[:, :3]) and torch.equal(dev[:, 3 + H:].cpu(), big[:, 3 + H:])
+
+
+def test_no_tokens():
+    """Zero rows: nothing is launched, the results are empty."""
+    w = rand(2, 2, 32, 64).cuda()
+    dn = rand(4, 2, 64, 16).cuda()
+    x = torch.empty(0, 64, dtype=BF16, device="cuda")
+    ids = torch.empty(0, 2, dtype=torch.int32, device="cuda")
+    assert tuple(expert_linear(x, w).shape) == (0, 32)
+    assert tuple(expert_linear(x, w, ids[:, 0].contiguous()).shape) == (0, 32)
+    assert tuple(moe_layer(x, w, dn, ids).shape) == (0, 64)
+    assert tuple(moe_layer(x, w, dn, router_logits=torch.empty(0, 2, device="cuda"), router=Router(1)).shape) == (0, 64)
+
+
+@pytest.mark.parametrize("g", [0, 32])
+def test_offsets_past_32_bits(g):
+    """The last of experts whose weights, and rows whose inputs and outputs, lie beyond 4 GiB."""
+    E, N, K = (40, 8192, 8192) if g == 0 else (130, 8192, 8192)
+    dense = rand(1, 1, N, K)[0]
+    if g == 0:
+        w = torch.empty(E, N, K, dtype=BF16, device="cuda")
+        w[E - 1] = dense.cuda()
+        rw = ref.Dense(dense.unsqueeze(0))
+        assert w.numel() * 2 > 2 ** 32
+    else:
+        rw, one = make_weight(5, 1, N, K, BF16, g)
+        data = torch.empty(E, *one.data.shape[1:], dtype=torch.uint8, device="cuda")
+        sc = torch.empty(E, *one.scales.shape[1:], dtype=BF16, device="cuda")
+        data[E - 1], sc[E - 1] = one.data[0], one.scales[0]
+        w = W4Weights(data, sc, N, K)
+        assert data.numel() > 2 ** 32
+    far = torch.zeros(3, 2 ** 30, dtype=BF16, device="cuda")          # rows 2 GiB apart
+    x = far[:, 5:5 + K]
+    host = rand(2, 3, K)
+    x.copy_(host)
+    out = far[:, 2 ** 20:2 ** 20 + N]
+    ids = torch.full((3,), E - 1, dtype=torch.int32, device="cuda")
+    want, tol = ref.linear(host, rw, torch.zeros(3, dtype=torch.int32), 0, BF16)
+    # (x and out interleave, which the overlap check refuses)
+    with pytest.raises(pkg.MoeEpError, match="overlap"):
+        expert_linear(x, w, ids, out=out)
+    close(expert_linear(x, w, ids), want, tol, "x")
+    close(expert_linear(host.cuda(), w, ids, out=out), want, tol, "out")
 
 
 def test_layer_large_float16_activations():
