@@ -193,7 +193,7 @@ bool is_wide(int64_t n, int top_k, int64_t num_experts, int64_t rows, int tile_r
 struct LayerSpace {
   int64_t ids, weights, head, pair, act, pair_out, pair_stride, total;
   int32_t n, slots, act_stride;
-  bool by_pair, wide;
+  bool wide;
 };
 
 int make_space(const moe_ep_layer_args* a, LayerSpace* s) {
@@ -209,7 +209,6 @@ int make_space(const moe_ep_layer_args* a, LayerSpace* s) {
                   kMaxSide);
   s->n = std::min(a->num_tokens, kPassTokens);
   const int64_t pairs = (int64_t)s->n * a->top_k;
-  s->by_pair = pairs <= a->num_experts;
   s->slots = (int32_t)std::min<int64_t>(pairs, a->num_experts);
   s->act_stride = (int32_t)up(a->intermediate_size, 16);
   int64_t off = 0;
@@ -372,12 +371,18 @@ int moe_ep_layer(const moe_ep_layer_args* a, void* stream) {
   for (int64_t t = 0; t < n; t += kPassTokens) {
     const int m = (int)std::min<int64_t>(kPassTokens, n - t);
     const int64_t pairs = (int64_t)m * a->top_k;
+    // A few tokens are routed by the first product's kernel itself.
+    const bool routed = a->router && !s.wide && m <= kRoutedTokens && pairs <= kFewPairs &&
+                        a->router->num_experts <= kRoutedExperts;
+    RouteKArgs choice = {};
     if (a->router) {
       const uint8_t* logits =
           static_cast<const uint8_t*>(a->router_logits) + t * a->logits_stride * elem_bytes(a->logits_dtype);
-      const hipError_t e = launch_route(
-          route_args(*a->router, logits, a->logits_dtype, a->logits_stride, m, ids, weights), hs);
-      if (e != hipSuccess) return report(MOE_EP_ERR_HIP, "route launch failed: %s", hipGetErrorString(e));
+      choice = route_args(*a->router, logits, a->logits_dtype, a->logits_stride, m, ids, weights);
+      if (!routed) {
+        const hipError_t e = launch_route(choice, hs);
+        if (e != hipSuccess) return report(MOE_EP_ERR_HIP, "route launch failed: %s", hipGetErrorString(e));
+      }
     }
     r.n = d.n = m;
     r.x = static_cast<const uint16_t*>(a->hidden) + t * a->hidden_stride;
@@ -390,7 +395,15 @@ int moe_ep_layer(const moe_ep_layer_args* a, void* stream) {
     d.out = static_cast<uint8_t*>(a->out) + t * a->out_stride * out_esz;
     d.chunks = (m + kChunkTokens - 1) / kChunkTokens;
     r.wide = s.wide;
-    hipError_t e = launch_gate_up(r, a->dtype, a->gate_up.group_size, hs);
+    hipError_t e;
+    if (routed) {
+      RowsRoutedKArgs rr;
+      static_cast<RowsKArgs&>(rr) = r;
+      rr.route = choice;
+      e = launch_gate_up_routed(rr, a->dtype, a->gate_up.group_size, hs);
+    } else {
+      e = launch_gate_up(r, a->dtype, a->gate_up.group_size, hs);
+    }
     if (e == hipSuccess && s.wide) {
       RowsKArgs y = r;
       y.w = d.w;

@@ -110,6 +110,13 @@ struct RowsKArgs {
   int32_t tiles_per_block;    // (set by the launcher)
 };
 
+// The same for a few tokens that the kernel routes itself.
+struct RowsRoutedKArgs : RowsKArgs {
+  RouteKArgs route;
+};
+// The most such tokens (a wave of a workgroup for each), pairs and experts.
+constexpr int kRoutedTokens = kExpertWaves, kFewPairs = 64, kRoutedExperts = 256;
+
 // The layer's down product, summed over the experts of each token.
 struct DownKArgs {
   WeightK w;
@@ -127,6 +134,7 @@ hipError_t launch_route(const RouteKArgs& a, hipStream_t stream);
 // dtype: MOE_EP_BF16 or MOE_EP_F16; group: 0 for dense weights, else 32, 64 or 128.
 hipError_t launch_expert_linear(const RowsKArgs& a, int dtype, int group, hipStream_t stream);
 hipError_t launch_gate_up(const RowsKArgs& a, int dtype, int group, hipStream_t stream);
+hipError_t launch_gate_up_routed(const RowsRoutedKArgs& a, int dtype, int group, hipStream_t stream);
 hipError_t launch_down(const DownKArgs& a, int dtype, int group, hipStream_t stream);
 // The down product for many tokens to an expert, and the sum over each token's pairs.
 hipError_t launch_wide_down(const RowsKArgs& a, int dtype, int group, hipStream_t stream);

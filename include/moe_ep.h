@@ -440,7 +440,7 @@ typedef struct moe_ep_layer_args {
 
 /* Bytes of device workspace moe_ep_layer needs for these sizes (the sizes,
  * gate_up.group_size and whether a router is set are read; pointers are not
- * followed). */
+ * followed).  What serves a number of tokens serves any smaller one. */
 MOE_EP_API int moe_ep_layer_workspace_bytes(const moe_ep_layer_args* args, size_t* out_bytes);
 
 /* The experts of a mixture-of-experts layer, whole:
@@ -453,7 +453,8 @@ MOE_EP_API int moe_ep_layer_workspace_bytes(const moe_ep_layer_args* args, size_
  * dispatch and combine, and out may be the rank's combine input buffer.
  *
  * Two kernel launches for few tokens, three for many to an expert (per 2048
- * tokens), and one more for the router's choice.  out may be hidden itself
+ * tokens), and one more for the router's choice unless that is for at most 8
+ * tokens, 64 slots and 256 experts.  out may be hidden itself
  * (same address, stride and type) but not overlap it otherwise.  The
  * workspace holds nothing between calls; calls that may overlap in time
  * (other streams, graphs replayed side by side) need one each.

@@ -179,6 +179,19 @@ def test_layer_workspace_bytes():
         assert status(_lib.moe_ep_layer_workspace_bytes, layer_args(**kw)) == INVALID
 
 
+@pytest.mark.parametrize("g", [0, 32])
+@pytest.mark.parametrize("E,k,H,I", [(1, 1, 64, 32), (8, 2, 4096, 1408), (32, 8, 1024, 512), (256, 8, 200, 40),
+                                     (16, 8, 7168, 2048), (1024, 64, 8, 8)])
+def test_layer_workspace_grows_with_the_tokens(E, k, H, I, g):
+    last = 0
+    for n in list(range(0, 130)) + [200, 256, 300, 512, 700, 1024, 1500, 2047, 2048, 2049, 100000]:
+        a = layer_args(num_tokens=n, num_experts=E, top_k=k, hidden_size=H, intermediate_size=I)
+        a.gate_up.group_size = g
+        size = _lib.moe_ep_layer_workspace_bytes(a)
+        assert size >= last, n
+        last = size
+
+
 def formula_tiles(q, s, g):
     """data and scales written from the header's formula, one element at a time."""
     E, N, K = q.shape

@@ -341,6 +341,32 @@ def test_layer_routed_inside(n, score, bias, groups):
     assert torch.equal(a, b) and not a.isnan().any()
 
 
+@pytest.mark.parametrize("n,E,k", [(8, 256, 8), (9, 256, 7), (8, 40, 9), (1, 256, 64), (3, 257, 5), (2, 3, 3)])
+@pytest.mark.parametrize("dtype,g", [(BF16, 0), (F16, 32)])
+def test_layer_routes_a_few_tokens_itself(n, E, k, dtype, g):
+    """Up to 8 tokens, 64 pairs and 256 experts, and one past each; the experts
+    of one rank, logits of each type in strided rows, NaN and ties among them."""
+    H, I, here, offset = 72, 40, max(1, E // 4), E // 2
+    x = rand(1, n, H, dtype=dtype).cuda()
+    _, gu = make_weight(3, here, 2 * I, H, dtype, g)
+    _, dn = make_weight(4, here, H, I, dtype, g)
+    for i, (score, bias, groups, t) in enumerate([("softmax", False, 1, F32), ("softmax", False, 1, BF16),
+                                                  ("sigmoid", True, 4, F16), ("softmax", True, 2, F32)]):
+        if E % groups or k > E // groups:
+            groups = 1
+        logits = rand(E + i, n, E + 3, dtype=t)
+        logits[-1, ::2] = logits[-1, 0]
+        logits[0, E - 1] = math.nan
+        logits[0, 0] = -math.inf
+        logits = logits.cuda()[:, :E]
+        r = Router(k, score, rand(3, E, dtype=F32, std=0.1).cuda() if bias else None, num_groups=groups,
+                   top_groups=max(1, groups // 2), renormalize=i % 2 == 0, scale=2.5)
+        ids, w = route(logits, r)
+        a = moe_layer(x, gu, dn, ids, w, expert_offset=offset)
+        b = moe_layer(x, gu, dn, router_logits=logits, router=r, expert_offset=offset)
+        assert torch.equal(a, b) and not b.isnan().any(), (score, t)
+
+
 def test_layer_in_place_strides_and_workspace():
     n, E, k, H, I = 5, 4, 2, 50, 30
     rg, gu = make_weight(3, E, 2 * I, H, BF16, 0)
