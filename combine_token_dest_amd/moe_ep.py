@@ -21,6 +21,7 @@ import torch
 
 from . import _lib
 from ._lib import MOE_EP_ALL_RANKS, MOE_EP_BF16, MOE_EP_F16, MOE_EP_F32
+from .experts import Weight, moe_layer
 
 _COMBINE_DTYPES = {torch.float32: MOE_EP_F32, torch.bfloat16: MOE_EP_BF16, torch.float16: MOE_EP_F16}
 
@@ -281,6 +282,39 @@ class MoEEp:
         ptr = _lib.moe_ep_get_combine_input_buffer(self._handle, rank, _COMBINE_DTYPES[dtype])
         self._buffer_dtype = dtype
         return self._view(ptr, self._p.ep_size * self._tpr, self._p.hidden_size * dtype.itemsize, dtype)
+
+    def experts(self, received: Sequence[DispatchResult], gate_up: Sequence[Weight], down: Sequence[Weight], *,
+                dtype: Optional[torch.dtype] = None,
+                workspace: Optional[torch.Tensor] = None) -> List[torch.Tensor]:
+        """Every rank's experts on the rows dispatch left it, written into its
+        combine input buffer: the step between dispatch and combine, whose
+        return value combine takes.
+
+        ``gate_up[d]`` and ``down[d]`` hold rank d's num_experts / ep_size
+        experts as ``moe_layer`` takes them; ``received`` is what dispatch
+        returned, with bfloat16 or float16 rows.  The buffers are of the rows'
+        type, or of ``dtype`` float32 where combine_max_elem_bytes allows it.
+        ``workspace`` as for ``moe_layer`` (of ep_size * tokens_per_rank rows
+        and one rank's experts); the ranks follow one another on the current
+        stream and share it."""
+        if self._handle is None:
+            raise RuntimeError("MoEEp has been destroyed")
+        p = self._p
+        ep = p.ep_size
+        if len(received) != ep or len(gate_up) != ep or len(down) != ep:
+            raise ValueError(f"expected {ep} per-rank received rows, gate_up and down")
+        per = p.num_experts // ep
+        for d in range(ep):
+            e = gate_up[d].data.shape[0]       # (a tensor's .data has its shape)
+            if e != per:
+                raise ValueError(f"rank {d} has {per} experts, gate_up[{d}] holds {e}")
+        odt = received[0].hidden.dtype if dtype is None else dtype
+        bufs = [self.get_combine_input_buffer(d, odt) for d in range(ep)]
+        for d in range(ep):
+            r = received[d]
+            moe_layer(r.hidden, gate_up[d], down[d], r.topk_ids, r.topk_weights, expert_offset=d * per,
+                      out=bufs[d], workspace=workspace)
+        return bufs
 
     def combine(self, expert_output: Sequence[Optional[torch.Tensor]], *,
                 output: Optional[Sequence[Optional[torch.Tensor]]] = None,

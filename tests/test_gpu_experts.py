@@ -557,6 +557,78 @@ def test_decode_step_through_dispatch_and_combine(tokens, g):
         moe.destroy()
 
 
+def by_rank(w, ep):
+    """A layer's weights cut into the ranks' experts."""
+    if isinstance(w, torch.Tensor):
+        return list(w.chunk(ep))
+    return [W4Weights(d, s, w.rows, w.cols) for d, s in zip(w.data.chunk(ep), w.scales.chunk(ep))]
+
+
+@pytest.mark.parametrize("dtype,out_dtype,g", [(BF16, BF16, 0), (F16, F32, 32)])
+def test_experts_between_dispatch_and_combine(dtype, out_dtype, g):
+    """MoEEp.experts on a step with ranks of unequal and no tokens: the same
+    bits as moe_layer rank by rank, the layer's definition after combine, and
+    a captured step replayed with other tokens."""
+    ep, E, k, H, I, cap = 4, 8, 3, 64, 40, 12
+    tokens = (5, 0, 12, 1)
+    rg, gu = make_weight(3, E, 2 * I, H, dtype, g)
+    rd, dn = make_weight(4, E, H, I, dtype, g)
+    gus, dns = by_rank(gu, ep), by_rank(dn, ep)
+    r = Router(k, renormalize=False)
+    hidden = [rand(s + 1, t, H, dtype=dtype).cuda() for s, t in enumerate(tokens)]
+    logits = [rand(s + 11, t, E, dtype=F32).cuda() for s, t in enumerate(tokens)]
+    moe = MoEEp(ep, E, k, cap, H, combine_max_elem_bytes=4)
+    try:
+        def step():
+            routed = [route(l, r) for l in logits]
+            res = moe.dispatch(hidden, [i for i, _ in routed], [w for _, w in routed])
+            bufs = moe.experts(res, gus, dns, dtype=out_dtype)
+            return routed, res, bufs, moe.combine(bufs)
+
+        routed, res, bufs, out = step()
+        for s in range(ep):
+            ids, w = (t.cpu() for t in routed[s])
+            want, parts = torch.zeros(2, tokens[s], H, dtype=torch.float64)
+            for d in range(ep):      # each rank's part is rounded to out_dtype, then added in float32
+                mine = torch.where(ids // (E // ep) == d, ids, torch.full_like(ids, -1))
+                y, tol = ref.layer(hidden[s].cpu(), rg, rd, mine, w, 0, dtype, out_dtype)
+                want += y
+                parts += tol + ep * 2.0 ** -24 * y.abs()
+            close(out[s], want, ref.rounded(want, parts, out_dtype), f"rank {s}")
+        res = moe.dispatch(hidden, [i for i, _ in routed], [w for _, w in routed])
+        bufs = [b.clone() for b in moe.experts(res, gus, dns, dtype=out_dtype)]
+        for d in range(ep):
+            alone = moe_layer(res[d].hidden, gus[d], dns[d], res[d].topk_ids, res[d].topk_weights,
+                              expert_offset=d * (E // ep), out_dtype=out_dtype)
+            assert torch.equal(alone, bufs[d])
+        for bad in ((res[:3], gus, dns), (res, gus[:3], dns), (res, [gu] * ep, dns), (res, gus, [dn] * ep)):
+            with pytest.raises(ValueError):
+                moe.experts(*bad)
+        moe.combine(bufs)
+        with pytest.raises(pkg.MoeEpError):      # no dispatch to follow
+            moe.experts(res, gus, dns)
+
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            step()
+        torch.cuda.current_stream().wait_stream(side)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            captured = step()[3]
+        for i in range(4):
+            for s in range(ep):
+                hidden[s].copy_(rand(40 + 10 * i + s, tokens[s], H, dtype=dtype))
+                logits[s].copy_(rand(41 + 20 * i + s, tokens[s], E, dtype=F32))
+            graph.replay()
+            got = [o.clone() for o in captured]
+            torch.cuda.synchronize()
+            for a, b in zip(got, step()[3]):
+                assert torch.equal(a, b)
+    finally:
+        moe.destroy()
+
+
 # -- refusals that need tensors ------------------------------------------------
 
 def test_refusals():
