@@ -162,8 +162,9 @@ int check_experts(int num_experts, int offset) {
 }
 
 // Largest matrix side: row and column indexes (and two rows of tiles past
-// them) are 32-bit in the kernels, offsets 64-bit.
-constexpr int32_t kMaxSide = 1 << 24;
+// them) are 32-bit in the kernels, offsets 64-bit, and a launch has fewer than
+// 2^32 threads in x (down_kernel: 512 for 16 columns and 128 of 2048 tokens).
+constexpr int32_t kMaxSide = 1 << 22;
 // Fewest elements of a row that the kernels read eight at a time.
 constexpr int32_t kMinRow = 8;
 

@@ -3,6 +3,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "moe_experts_internal.h"
 #include "moe_route_device.h"
 
@@ -41,12 +43,23 @@ void start_route(const RouteKArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-hipError_t launch_route(const RouteKArgs& a, hipStream_t stream) {
-  if (a.num_groups > 1) start_route<double, 64, true>(a, stream);
-  else if (a.bias) start_route<double, 64, false>(a, stream);
-  else if (a.n >= 2048 && a.num_experts <= 256 && a.top_k <= 16) start_route<float, 16, false>(a, stream);
-  else start_route<float, 64, false>(a, stream);
-  return hipGetLastError();
+hipError_t launch_route(const RouteKArgs& all, hipStream_t stream) {
+  // A launch has fewer than 2^32 threads in x, and a token up to 64.
+  constexpr int kMost = 1 << 24;
+  RouteKArgs a = all;
+  for (int64_t t = 0; t < all.n; t += kMost) {
+    a.n = (int32_t)std::min<int64_t>(kMost, all.n - t);
+    a.logits = static_cast<const uint8_t*>(all.logits) + t * all.logits_stride * (all.logits_dtype == MOE_EP_F32 ? 4 : 2);
+    a.ids = all.ids + t * all.top_k;
+    a.weights = all.weights + t * all.top_k;
+    if (a.num_groups > 1) start_route<double, 64, true>(a, stream);
+    else if (a.bias) start_route<double, 64, false>(a, stream);
+    else if (a.n >= 2048 && a.num_experts <= 256 && a.top_k <= 16) start_route<float, 16, false>(a, stream);
+    else start_route<float, 64, false>(a, stream);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace moe_ep_detail

@@ -253,6 +253,12 @@ def _logits(logits: torch.Tensor) -> Tuple[int, int, int]:
     return dev, _DTYPES[logits.dtype], logits.stride(0)
 
 
+def _int32(n: int, what: str) -> int:
+    if n > 0x7fffffff or n < 0:
+        raise ValueError(f"{what} {n} is not in [0, 2^31)")
+    return n
+
+
 def _call(entry, dev: int, *args) -> None:
     """entry(*args, stream) on the current stream of GPU ``dev``, with that
     device current.  (The raw accessors: torch.cuda.current_stream() builds a
@@ -274,6 +280,7 @@ def route(logits: torch.Tensor, router: Router, *, topk_ids: Optional[torch.Tens
     ``invalid_expert_id`` and weight 0.  See include/moe_ep.h, moe_ep_route."""
     dev, dtype, stride = _logits(logits)
     n, E = logits.shape
+    _int32(n, "token count")
     r = _router(router, E, dev)
     shape = (n, router.top_k)
     if topk_ids is None:
@@ -314,7 +321,8 @@ def expert_linear(x: torch.Tensor, weight: Weight, expert_ids: Optional[torch.Te
         expert_ids = _ids(expert_ids, (n,), dev, "expert_ids")
         a.expert_ids = expert_ids.data_ptr()
     a.dtype, a.out_dtype = _DTYPES[x.dtype], _DTYPES[out.dtype]
-    a.num_rows, a.num_experts, a.expert_offset = n, E, expert_offset
+    a.num_rows, a.num_experts = _int32(n, "row count"), E
+    a.expert_offset = _int32(expert_offset, "expert_offset")
     a.in_features, a.out_features = K, N
     _call(_lib.moe_ep_expert_linear, dev, a)
     return out
@@ -374,7 +382,8 @@ def moe_layer(hidden: torch.Tensor, gate_up: Weight, down: Weight, topk_ids: Opt
     a.hidden, a.hidden_stride = _rows(hidden, dev, "hidden")
     a.out, a.out_stride = _rows(out, dev, "out")
     a.dtype, a.out_dtype = _DTYPES[dtype], _DTYPES[out.dtype]
-    a.num_tokens, a.top_k, a.num_experts, a.expert_offset = n, top_k, E, expert_offset
+    a.num_tokens, a.top_k, a.num_experts = _int32(n, "token count"), top_k, E
+    a.expert_offset = _int32(expert_offset, "expert_offset")
     a.hidden_size, a.intermediate_size = H, inter
     if workspace is None:
         nbytes = _lib.moe_ep_layer_workspace_bytes(a)

@@ -364,7 +364,7 @@ typedef struct moe_ep_router {
 /* Chooses the experts of num_tokens tokens: logits device [num_tokens,
  * num_experts] of logits_dtype (any moe_ep_dtype), rows logits_stride apart;
  * topk_ids device int32 and topk_weights device float, both [num_tokens,
- * top_k], as moe_ep_dispatch takes them.  One kernel launch. */
+ * top_k], as moe_ep_dispatch takes them.  One kernel launch per 2^24 tokens. */
 MOE_EP_API int moe_ep_route(const moe_ep_router* router, const void* logits, int32_t logits_dtype,
                             int64_t logits_stride, int32_t num_tokens, int32_t* topk_ids,
                             float* topk_weights, void* stream);
@@ -395,7 +395,7 @@ typedef struct moe_ep_linear_args {
   const void* x;                  /* device [num_rows, in_features] of dtype */
   int64_t x_stride;               /* >= 0; 0 repeats one row */
   const int32_t* expert_ids;      /* device [num_rows], or NULL: every row is expert 0's */
-  void* out;                      /* device [num_rows, out_features] of out_dtype; must not overlap x */
+  void* out;                      /* device [num_rows, out_features] of out_dtype */
   int64_t out_stride;             /* >= out_features */
   moe_ep_weight weight;           /* N = out_features, K = in_features */
   int32_t dtype;                  /* MOE_EP_BF16 or MOE_EP_F16 */
@@ -403,14 +403,15 @@ typedef struct moe_ep_linear_args {
   int32_t num_rows;
   int32_t num_experts;            /* 1..MOE_EP_MAX_EXPERTS */
   int32_t expert_offset;          /* expert_ids of the first expert, >= 0 */
-  int32_t in_features;            /* 8..2^24 */
-  int32_t out_features;           /* 1..2^24 */
+  int32_t in_features;            /* 8..2^22 */
+  int32_t out_features;           /* 1..2^22 */
 } moe_ep_linear_args;
 
 /* out[r] = W[expert_ids[r] - expert_offset] x[r].  Rows whose id is outside
  * [expert_offset, expert_offset + num_experts) get zeros.  Made for the few
  * rows of a decode step: the weights of each used expert are read once per
- * 2048 rows.  One kernel launch per 2048 rows. */
+ * 2048 rows.  One kernel launch per 2048 rows.  x and out, each from its
+ * first element to its last, must not overlap. */
 MOE_EP_API int moe_ep_expert_linear(const moe_ep_linear_args* args, void* stream);
 
 typedef struct moe_ep_layer_args {
@@ -434,8 +435,8 @@ typedef struct moe_ep_layer_args {
   int32_t top_k;                  /* 1..MOE_EP_MAX_TOPK; the router's with router */
   int32_t num_experts;            /* experts whose weights are here, 1..MOE_EP_MAX_EXPERTS */
   int32_t expert_offset;          /* id of the first of them, >= 0 */
-  int32_t hidden_size;            /* 8..2^24 */
-  int32_t intermediate_size;      /* 8..2^24 */
+  int32_t hidden_size;            /* 8..2^22 */
+  int32_t intermediate_size;      /* 8..2^22 */
 } moe_ep_layer_args;
 
 /* Bytes of device workspace moe_ep_layer needs for these sizes (the sizes,
@@ -455,7 +456,8 @@ MOE_EP_API int moe_ep_layer_workspace_bytes(const moe_ep_layer_args* args, size_
  * Two kernel launches for few tokens, three for many to an expert (per 2048
  * tokens), and one more for the router's choice unless that is for at most 8
  * tokens, 64 slots and 256 experts.  out may be hidden itself
- * (same address, stride and type) but not overlap it otherwise.  The
+ * (same address, stride and type) but not overlap it otherwise, each taken
+ * from its first element to its last.  The
  * workspace holds nothing between calls; calls that may overlap in time
  * (other streams, graphs replayed side by side) need one each.
  *

@@ -164,6 +164,15 @@ def test_layer_refusals():
         assert layer(**kw) == ALIGN, kw
 
 
+def test_sides_a_launch_can_cover():
+    side = 1 << 22
+    for kw in (dict(hidden_size=side + 1), dict(intermediate_size=side + 1)):
+        assert layer(**dict(kw, num_tokens=0)) == INVALID
+    assert layer(num_tokens=0, hidden_size=side, hidden_stride=side, out_stride=side) == _lib.MOE_EP_OK
+    assert linear(num_rows=0, out_features=side + 1, out_stride=side + 1) == INVALID
+    assert linear(num_rows=0, out_features=side, out_stride=side) == _lib.MOE_EP_OK
+
+
 def test_layer_workspace_bytes():
     def size(**kw):
         return _lib.moe_ep_layer_workspace_bytes(layer_args(**kw))

@@ -101,6 +101,17 @@ def test_route_many_tokens(n):
     check_route(rand(n, n, 96, dtype=F32), Router(6, "sigmoid"))
 
 
+def test_route_more_tokens_than_a_launch_has():
+    n = 2 ** 26 + 5                       # at 64 lanes each, 2^32 threads and more
+    pattern = rand(7, 64, 2, dtype=F16).cuda()
+    logits = pattern[torch.arange(n, device="cuda") % 64]
+    for r in (Router(1), Router(1, bias=torch.zeros(2, device="cuda"))):
+        ids, w = route(logits, r)
+        want_ids, want_w = route(pattern, r)
+        at = torch.arange(n, device="cuda") % 64
+        assert torch.equal(ids, want_ids[at]) and torch.equal(w, want_w[at])
+
+
 def test_route_ties_go_to_the_lowest_index():
     logits = torch.randint(-1, 2, (64, 96), generator=gen(3)).to(BF16)
     check_route(logits, Router(12))
@@ -645,6 +656,11 @@ def test_refusals():
                 lambda: expert_linear(x, w.transpose(1, 2)),
                 lambda: expert_linear(x, W4Weights(w4.data, w4.scales.bfloat16()[:, :, :3], 32, 64))):
         with pytest.raises((ValueError, TypeError)):
+            bad()
+    for bad in (lambda: expert_linear(x, w, ids, expert_offset=2 ** 32), lambda: expert_linear(x, w, expert_offset=-1),
+                lambda: moe_layer(x, w, rand(4, 2, 64, 16).cuda(), ids.view(4, 1), expert_offset=2 ** 32),
+                lambda: route(torch.zeros(1, 4, device="cuda").expand(2 ** 32, 4), Router(1))):
+        with pytest.raises(ValueError, match="not in"):
             bad()
     wide = torch.zeros(4, 96, dtype=BF16, device="cuda")
     with pytest.raises(pkg.MoeEpError, match="overlap"):
