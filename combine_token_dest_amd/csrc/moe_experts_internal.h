@@ -108,6 +108,7 @@ struct RowsKArgs {
   int64_t pair_stride;
   int32_t split;              // waves that share a tile (set by the launcher)
   int32_t tiles_per_block;    // (set by the launcher)
+  int32_t busiest_first;      // wide: blockIdx.y counts the experts by their pairs (set by the launcher)
 };
 
 // The same for a few tokens that the kernel routes itself.

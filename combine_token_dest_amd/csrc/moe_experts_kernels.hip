@@ -1081,6 +1081,36 @@ __device__ __forceinline__ bool whole_rows(const RowsKArgs& a) {
   return ((reinterpret_cast<uintptr_t>(a.out) / (a.out_f32 ? 4 : 2)) | (uintptr_t)a.out_stride) % 4 == 0;
 }
 
+// The expert with the rank-th most pairs among num_experts (at most
+// kWideThreads), the lower one first among equals.  Called by a whole wide
+// workgroup; counts has room for them.
+__device__ __forceinline__ int busiest(const RowsKArgs& a, int rank, int* counts) {
+  __shared__ int found;
+  const int tid = threadIdx.x, pairs = a.n * a.top_k;
+  counts[tid] = 0;
+  __syncthreads();
+  constexpr int kUnroll = 8;
+  for (int base = 0; base < pairs; base += kWideThreads * kUnroll) {
+    int v[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) v[u] = a.ids[min(base + u * kWideThreads + tid, pairs - 1)];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      if (base + u * kWideThreads + tid < pairs && v[u] >= a.offset && (int64_t)v[u] - a.offset < a.num_experts)
+        atomicAdd(&counts[v[u] - a.offset], 1);
+    }
+  }
+  __syncthreads();
+  if (tid < a.num_experts) {
+    const int mine = counts[tid];
+    int ahead = 0;
+    for (int e = 0; e < a.num_experts; ++e) ahead += counts[e] > mine || (counts[e] == mine && e < tid);
+    if (ahead == rank) found = tid;
+  }
+  __syncthreads();
+  return __builtin_amdgcn_readfirstlane(found);
+}
+
 // A workgroup takes one expert (blockIdx.y) and kWideWaves * 2 tiles of 16
 // weight rows (kWideGated: as many gate as up tiles, a pair to a wave), lists
 // the expert's tokens and multiplies them 48 at a time, with as many columns as
@@ -1104,7 +1134,9 @@ __global__ void __launch_bounds__(kWideThreads, OP == kWideDown ? 2 : 3) wide_ke
     for (int i = tid; i < a.n; i += kWideThreads) list[i] = i << 6;
     __syncthreads();
   } else {
-    const int id = a.by_pair ? __builtin_amdgcn_readfirstlane(a.ids[slot]) : a.offset + slot;
+    const int id = a.by_pair         ? __builtin_amdgcn_readfirstlane(a.ids[slot])
+                   : a.busiest_first ? a.offset + busiest(a, slot, reinterpret_cast<int*>(bmem))
+                                     : a.offset + slot;
     const bool inside = id >= a.offset && (int64_t)id - a.offset < a.num_experts;
     expert = inside ? id - a.offset : 0;
     m = 0;
@@ -1247,7 +1279,7 @@ void start_rows(Args a, hipStream_t stream) {
 }
 
 template <class T, int G, WideOp OP>
-void start_wide(const RowsKArgs& a, hipStream_t stream) {
+void start_wide(RowsKArgs a, hipStream_t stream) {
   const int slots = a.ids == nullptr ? 1 : a.by_pair ? a.n * a.top_k : a.num_experts;
   const int tiles = (a.inter + 15) / 16;
   const int per = kWideWaves * (OP == kWideGated ? 1 : 2);
@@ -1262,6 +1294,11 @@ void start_wide(const RowsKArgs& a, hipStream_t stream) {
   const int64_t at_once = experts * kWideTiles * 16;
   const int64_t passes = ((int64_t)a.n * a.top_k + at_once - 1) / at_once;
   const dim3 grid((tiles + per - 1) / per, slots, (unsigned)std::max<int64_t>(1, std::min(passes, 512 / blocks)));
+  // The card holds some 768 workgroups at once: an expert of several passes that
+  // started with the last of them would run on alone.  (32 experts of 4096 x
+  // 7168 and 7168 x 2048, 4 bits, 1 to 130 of 1389 pairs each: layer 483 us in
+  // the experts' order, 401 busiest first; 0 to 107 of 1147: 350 and 345.)
+  a.busiest_first = a.ids != nullptr && !a.by_pair && blocks > 512 && a.num_experts <= kWideThreads;
   if constexpr (OP == kWideGated && G != 0) {
     if (a.inter % 4 != 0) {
       wide_kernel<T, G, OP, true, true><<<grid, kWideThreads, 0, stream>>>(a);

@@ -316,6 +316,25 @@ def test_layer_many_tokens(n, E, k):
     close(moe_layer(x.cuda(), gu, dn, ids.cuda(), w.cuda()), want, tol)
 
 
+@pytest.mark.parametrize("g", [0, 64])
+@pytest.mark.parametrize("H,I", [(64, 1100), (2200, 24)])
+def test_layer_experts_of_unequal_load(H, I, g):
+    """More workgroups than the card holds at once: experts of no, one and
+    many tokens, equals among them, experts of other ranks, repeated ids."""
+    n, k, E, offset = 500, 3, 32, 5
+    x = rand(1, n, H)
+    rg, gu = make_weight(3, E, 2 * I, H, BF16, g)
+    rd, dn = make_weight(4, E, H, I, BF16, g)
+    ids = torch.randint(0, 16, (n, k), generator=gen(2)) * torch.randint(0, 3, (n, k), generator=gen(3)) + offset - 2
+    ids[:, 2] = torch.where(torch.arange(n) % 3 == 0, ids[:, 0], torch.full((n,), E + offset))
+    ids = ids.int()
+    w = rand(4, n, k, dtype=F32).abs()
+    want, tol = ref.layer(x, rg, rd, ids, w, offset, BF16, BF16)
+    close(moe_layer(x.cuda(), gu, dn, ids.cuda(), w.cuda(), expert_offset=offset), want, tol)
+    y, ytol = ref.linear(x, rg, ids[:, 0], offset, BF16)
+    close(expert_linear(x.cuda(), gu, ids[:, 0].cuda().contiguous(), expert_offset=offset), y, ytol, "linear")
+
+
 @pytest.mark.parametrize("g", [0, 32])
 @pytest.mark.parametrize("n,k", [(3, 4), (20, 8), (600, 4)])
 def test_layer_ids_named_by_every_slot(n, k, g):
