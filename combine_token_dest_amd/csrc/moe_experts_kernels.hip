@@ -575,14 +575,15 @@ __device__ __forceinline__ float pair_weight(const RowsKArgs& a, int pair, int e
 // A workgroup takes one expert (blockIdx.y) and a run of tiles of 16 output
 // rows (GATED: 16 gate rows and the 16 up rows beside them), a.split of its
 // waves to a tile.  It lists the tokens that chose the expert and multiplies
-// them 16 at a time.  GATED: silu(gate) * up goes to the workspace in two
+// them 4 (4-bit) or 8 (dense) at a time.  GATED: silu(gate) * up goes to the workspace in two
 // 16-bit parts (the down product then sees it to 16 bits and more, not
 // rounded to the 8 of a bfloat16), and the first workgroup of an expert
 // leaves the plan down_kernel follows.
 // ROUTED (a few tokens, GATED): every workgroup makes the router's choice for
-// itself, a wave for each token. That takes the 7 us that a kernel before this
-// one takes, but saves its launch and the wait between the two (one token of 256
-// experts, 4-bit: 54.1 -> 52.3 us; two tokens of 8 small experts: 20.2 -> 17.6).
+// itself, a wave for each token.  One token of 256 grouped experts takes it 5.5
+// us, little less than a kernel of its own (6.4), but the launch and the wait
+// between the two are saved (that layer, 4-bit: 54.1 -> 52.3 us; two tokens of 8
+// small experts: 20.2 -> 17.6).
 template <class T, int G, bool GATED, bool SHIFT, bool CUT, bool ROUTED>
 __global__ void __launch_bounds__(kThreads, 4)
     rows_kernel(const std::conditional_t<ROUTED, RowsRoutedKArgs, RowsKArgs> a) {
@@ -794,7 +795,7 @@ __global__ void __launch_bounds__(kThreads, 4) down_kernel(const DownKArgs a) {
   int s = uniform((int)(all * wave / kExpertWaves));
   const int end = uniform((int)(all * (wave + 1) / kExpertWaves));
 
-  // One product of the run: an expert's k steps [k0, k1) with 16 of its tokens.
+  // One product of the run: an expert's k steps [k0, k1) with a pass of its tokens.
   struct Item {
     int expert, k0, k1, left;
     PairRec rec;
