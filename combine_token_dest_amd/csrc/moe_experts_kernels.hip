@@ -579,6 +579,9 @@ __device__ __forceinline__ float pair_weight(const RowsKArgs& a, int pair, int e
 // 16-bit parts (the down product then sees it to 16 bits and more, not
 // rounded to the 8 of a bfloat16), and the first workgroup of an expert
 // leaves the plan down_kernel follows.
+// Bound by HBM where an expert has one pass: gate and up of 64 dense experts 1024
+// x 4096, 32 tokens, 195 us, 5.5 TB/s; 32 4-bit matrices 4096 x 7168 for 48 rows
+// 118 us, 3.5 TB/s; one of them 7.3 us, mostly start-up.
 // ROUTED (a few tokens, GATED): every workgroup makes the router's choice for
 // itself, a wave for each token.  One token of 256 grouped experts takes it 5.5
 // us, little less than a kernel of its own (6.4), but the launch and the wait
@@ -744,6 +747,8 @@ __global__ void __launch_bounds__(kThreads, 4)
 // weight * product into its own copy of the chunk's output tile in LDS (each
 // token at most once per expert, so lanes never meet), and the copies are
 // added in wave order at the end.
+// Bound by HBM: 64 dense experts 4096 x 1024, 32 tokens, 99 us, 5.4 TB/s; one
+// token's 8 4-bit experts 7168 x 2048 21 us, 2.8 TB/s, a fifth of it start-up.
 template <class T, int G, bool CUT>
 __global__ void __launch_bounds__(kThreads, 4) down_kernel(const DownKArgs a) {
   constexpr bool W4 = G != 0;
@@ -1090,15 +1095,28 @@ __device__ __forceinline__ int busiest(const RowsKArgs& a, int rank, int* counts
   const int tid = threadIdx.x, pairs = a.n * a.top_k;
   counts[tid] = 0;
   __syncthreads();
-  constexpr int kUnroll = 8;
-  for (int base = 0; base < pairs; base += kWideThreads * kUnroll) {
-    int v[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) v[u] = a.ids[min(base + u * kWideThreads + tid, pairs - 1)];
+  constexpr int kUnroll = 4;
+  for (int base = 0; base < pairs; base += kWideThreads * 4 * kUnroll) {
+    i32x4 v[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      if (base + u * kWideThreads + tid < pairs && v[u] >= a.offset && (int64_t)v[u] - a.offset < a.num_experts)
-        atomicAdd(&counts[v[u] - a.offset], 1);
+      const int i = base + (u * kWideThreads + tid) * 4;
+      v[u] = i32x4{-1, -1, -1, -1};       // (offset >= 0)
+      if (i + 4 <= pairs) {
+        v[u] = reinterpret_cast<const Ints4*>(a.ids + i)->v;
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (i + c < pairs) v[u][c] = a.ids[i + c];
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (v[u][c] >= a.offset && (int64_t)v[u][c] - a.offset < a.num_experts) atomicAdd(&counts[v[u][c] - a.offset], 1);
+      }
     }
   }
   __syncthreads();
@@ -1116,8 +1134,14 @@ __device__ __forceinline__ int busiest(const RowsKArgs& a, int rank, int* counts
 // weight rows (kWideGated: as many gate as up tiles, a pair to a wave), lists
 // the expert's tokens and multiplies them 48 at a time, with as many columns as
 // are left in the last pass.
+// kWideGated leaves its lists in the plan for kWideDown, whose workgroups are
+// spared the going through all ids.
 // kWideDown reads the activations of kWideGated and writes each pair's
 // weighted product, in float32, for sum_kernel.
+// Bound by issue: decoding, matrix and LDS instructions of a step hardly overlap
+// between the waves of a workgroup, which the barrier keeps together.  32 4-bit
+// experts of 4096 x 7168 and 7168 x 2048, some 1200 pairs: 196 and 143 us (1.6 to
+// 2.4 TB/s of weights, an expert of 130 tokens three times), sum_kernel 16.
 template <class T, int G, WideOp OP, bool SHIFT, bool CUT>
 __global__ void __launch_bounds__(kWideThreads, OP == kWideDown ? 2 : 3) wide_kernel(const RowsKArgs a) {
   constexpr bool W4 = G != 0;
@@ -1131,7 +1155,14 @@ __global__ void __launch_bounds__(kWideThreads, OP == kWideDown ? 2 : 3) wide_ke
   const int tiles = (a.inter + 15) >> 4;
 
   int m = a.n, expert = 0;
-  if (a.ids == nullptr) {
+  const PlanK& p = a.plan;
+  PairRec* rec = reinterpret_cast<PairRec*>(p.pair) + (int64_t)slot * a.n;
+  if (OP == kWideDown) {
+    m = p.head[slot];
+    expert = __builtin_amdgcn_readfirstlane(p.head[p.slots + slot]);
+    for (int i = tid; i < m; i += kWideThreads) list[i] = rec[i].pair;
+    __syncthreads();
+  } else if (a.ids == nullptr) {
     for (int i = tid; i < a.n; i += kWideThreads) list[i] = i << 6;
     __syncthreads();
   } else {
@@ -1145,6 +1176,13 @@ __global__ void __launch_bounds__(kWideThreads, OP == kWideDown ? 2 : 3) wide_ke
       m = lister.run(a.ids, a.n * k, k, id, list);
       if (a.by_pair && (list[0] >> 6) * k + (list[0] & 63) != slot) m = 0;
     }
+  }
+  if (OP == kWideGated && blockIdx.x == 0 && blockIdx.z == 0) {
+    if (tid == 0) {
+      p.head[slot] = m;
+      p.head[p.slots + slot] = expert;
+    }
+    for (int i = tid; i < m; i += kWideThreads) rec[i] = PairRec{list[i], pair_weight(a, list[i], expert, lister.repeated)};
   }
   if (OP == kWideLinear && a.ids != nullptr && slot == 0) {
     const int c0 = blockIdx.x * kWideWaves * TL * 16;
@@ -1199,7 +1237,7 @@ __global__ void __launch_bounds__(kWideThreads, OP == kWideDown ? 2 : 3) wide_ke
             u32x2{lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16};
       } else {
         float weight = 1.0f;
-        if constexpr (OP == kWideDown) weight = pair_weight(a, at, expert, lister.repeated);
+        if constexpr (OP == kWideDown) weight = rec[i].weight;
 #pragma unroll
         for (int t = 0; t < TL; ++t) {
           const int n = tile[t] * 16 + (lane >> 4) * 4;
@@ -1299,7 +1337,10 @@ void start_wide(RowsKArgs a, hipStream_t stream) {
   // started with the last of them would run on alone.  (32 experts of 4096 x
   // 7168 and 7168 x 2048, 4 bits, 1 to 130 of 1389 pairs each: layer 483 us in
   // the experts' order, 401 busiest first; 0 to 107 of 1147: 350 and 345.)
-  a.busiest_first = a.ids != nullptr && !a.by_pair && blocks > 512 && a.num_experts <= kWideThreads;
+  // (kWideDown follows kWideGated's order, whose w.cols are its rows.)
+  const int64_t then = OP == kWideGated ? ((int64_t)a.w.cols + kWideWaves * 32 - 1) / (kWideWaves * 32) * slots : 0;
+  a.busiest_first = OP != kWideDown && a.ids != nullptr && !a.by_pair && std::max(blocks, then) > 512 &&
+                    a.num_experts <= kWideThreads;
   if constexpr (OP == kWideGated && G != 0) {
     if (a.inter % 4 != 0) {
       wide_kernel<T, G, OP, true, true><<<grid, kWideThreads, 0, stream>>>(a);

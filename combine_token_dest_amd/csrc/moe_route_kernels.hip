@@ -13,6 +13,9 @@ namespace {
 
 constexpr int kRouteThreads = 256;
 
+// One token of 256 experts in groups 6.4 us, 1024
+// tokens of 256 experts 5.3, 8192 of 128 (16 lanes to a token) 6.6; with a wave to
+// a token the last takes 11.7.
 template <typename V, int LPT, int VPL, bool GROUPS>
 __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteKArgs a) {
   constexpr int kTokens = 64 / LPT;

@@ -541,6 +541,40 @@ def test_graph_replays():
             assert torch.equal(a, b), i
 
 
+def test_graph_replays_of_many_tokens():
+    """A captured layer and linear product of many tokens to an expert, replayed
+    with other ids (experts that had tokens have none, and back), against
+    eager calls on another stream at the same time."""
+    n, E, k, H, I = 300, 8, 4, 64, 1100
+    _, gu = make_weight(3, E, 2 * I, H, BF16, 64)
+    _, dn = make_weight(4, E, H, I, BF16, 64)
+    x, ids, w = rand(1, n, H).cuda(), make_ids(2, n, E, k).cuda(), rand(3, n, k, dtype=F32).cuda()
+    first = ids[:, 0].contiguous()
+
+    def step():
+        return moe_layer(x, gu, dn, ids, w), expert_linear(x, gu, first)
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        captured = step()
+    for i in range(4):
+        x.copy_(rand(10 + i, n, H))
+        ids.copy_(make_ids(20 + i, n, E, k) if i % 2 else torch.full((n, k), i + 1, dtype=torch.int32))
+        first.copy_(ids[:, 0])
+        side.wait_stream(torch.cuda.current_stream())
+        graph.replay()
+        with torch.cuda.stream(side):
+            eager = step()
+        torch.cuda.current_stream().wait_stream(side)
+        for a, b in zip(captured, eager):
+            assert torch.equal(a, b) and not b.isnan().any()
+        for b in eager:
+            b.record_stream(torch.cuda.current_stream())
+
+
 # -- the operators as a decode step uses them ----------------------------------
 
 @pytest.mark.parametrize("tokens,g", [((3, 0, 5, 1), 0), ((16, 16, 16, 16), 64)])
