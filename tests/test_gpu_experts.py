@@ -541,6 +541,39 @@ def test_graph_replays():
             assert torch.equal(a, b), i
 
 
+@pytest.mark.parametrize("dtype,g", [(BF16, 0), (F16, 128)])
+def test_many_tokens_in_place_strides_and_neighbours(dtype, g):
+    """More than 2048 tokens, many to an expert: out is hidden, a row repeated
+    by stride 0, a workspace of exactly its size; what lies between and behind
+    the rows stays as it was."""
+    n, E, k, H, I, offset = 2100, 6, 3, 70, 600, 2
+    rg, gu = make_weight(3, E, 2 * I, H, dtype, g)
+    rd, dn = make_weight(4, E, H, I, dtype, g)
+    ids = make_ids(2, n, E, k, offset, 4)
+    w = rand(4, n, k, dtype=F32).abs()
+    x = rand(1, n, H, dtype=dtype)
+    want, tol = ref.layer(x, rg, rd, ids, w, offset, dtype, dtype)
+    nbytes = pkg.moe_layer_workspace_bytes(n, k, E, H, I, group_size=g)
+    ws = torch.full((nbytes + 256,), 173, dtype=torch.uint8, device="cuda")
+    wide = torch.full((n + 2, H + 9), 7.0, dtype=dtype, device="cuda")
+    rows = wide[:n, 3:3 + H]
+    rows.copy_(x)
+    y = moe_layer(rows, gu, dn, ids.cuda(), w.cuda(), expert_offset=offset, out=rows, workspace=ws[:nbytes])
+    close(y, want, tol, "in place")
+    wide[:n, 3:3 + H] = 7.0
+    assert (wide == 7.0).all() and (ws[nbytes:] == 173).all()
+    one = x[:1].cuda().expand(n, H)
+    want, tol = ref.layer(x[:1].expand(n, H), rg, rd, ids, w, offset, dtype, F32)
+    got = moe_layer(one, gu, dn, ids.cuda(), w.cuda(), expert_offset=offset, out_dtype=F32)
+    close(got, want, tol, "repeated row")
+    first = ids[:, 0].contiguous()
+    out = torch.full((n + 1, 2 * I + 5), 7.0, dtype=dtype, device="cuda")
+    y, ytol = ref.linear(x, rg, first, offset, dtype)
+    close(expert_linear(x.cuda(), gu, first.cuda(), expert_offset=offset, out=out[:n, 1:1 + 2 * I]), y, ytol, "linear")
+    out[:n, 1:1 + 2 * I] = 7.0
+    assert (out == 7.0).all()
+
+
 def test_graph_replays_of_many_tokens():
     """A captured layer and linear product of many tokens to an expert, replayed
     with other ids (experts that had tokens have none, and back), against
