@@ -453,13 +453,13 @@ MOE_EP_API int moe_ep_layer_workspace_bytes(const moe_ep_layer_args* args, size_
  * rows dispatch left that rank it is the expert computation between
  * dispatch and combine, and out may be the rank's combine input buffer.
  *
- * Two kernel launches for few tokens, three for many to an expert (per 2048
- * tokens), and one more for the router's choice unless that is for at most 8
- * tokens, 64 slots and 256 experts.  out may be hidden itself
+ * Per 2048 tokens two kernel launches, or three for many tokens to an expert;
+ * one more for the router's choice, which the first of the two makes itself
+ * for at most 8 tokens, 64 slots and 256 experts.  out may be hidden itself
  * (same address, stride and type) but not overlap it otherwise, each taken
- * from its first element to its last.  The
- * workspace holds nothing between calls; calls that may overlap in time
- * (other streams, graphs replayed side by side) need one each.
+ * from its first element to its last.  The workspace holds nothing between
+ * calls; calls that may overlap in time (other streams, graphs replayed side
+ * by side) need one each.
  *
  * Between the products an activation keeps 16 significant bits (bfloat16)
  * or 22 (float16, where it saturates at 131008). */
