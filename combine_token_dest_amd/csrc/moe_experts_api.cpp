@@ -222,9 +222,9 @@ int make_space(const moe_ep_layer_args* a, LayerSpace* s) {
   s->weights = take(a->router ? pairs * 4 : 0);
   s->head = take((int64_t)s->slots * kMaxChunks * 4);
   s->pair = take((int64_t)s->slots * s->n * 8);
-  s->act = take(2 * pairs * s->act_stride * 2);
   s->wide = is_wide(s->n, a->top_k, a->num_experts, a->intermediate_size, kWideWaves * 16,
                     a->hidden_size, a->gate_up.group_size);
+  s->act = take(kParts * pairs * s->act_stride * 2);      // float32 ones are smaller
   s->pair_stride = up(a->hidden_size, 16);
   s->pair_out = take(s->wide ? pairs * s->pair_stride * 4 : 0);
   s->total = std::max<int64_t>(off, 256);
@@ -356,7 +356,7 @@ int moe_ep_layer(const moe_ep_layer_args* a, void* stream) {
   PlanK p;
   p.head = reinterpret_cast<int32_t*>(ws + s.head);
   p.pair = ws + s.pair;
-  p.act = reinterpret_cast<uint16_t*>(ws + s.act);
+  p.act = ws + s.act;
   p.act_stride = s.act_stride;
   r.x_stride = a->hidden_stride;
   r.top_k = d.top_k = a->top_k;
@@ -391,7 +391,7 @@ int moe_ep_layer(const moe_ep_layer_args* a, void* stream) {
     r.topk_weights = a->router ? weights : a->topk_weights ? a->topk_weights + t * a->top_k : nullptr;
     r.by_pair = pairs <= a->num_experts;
     p.slots = (int32_t)std::min<int64_t>(pairs, a->num_experts);
-    p.act_plane = pairs * p.act_stride;
+    p.act_plane = s.wide || a->down.group_size ? pairs * p.act_stride : 0;
     r.plan = d.plan = p;
     d.out = static_cast<uint8_t*>(a->out) + t * a->out_stride * out_esz;
     d.chunks = (m + kChunkTokens - 1) / kChunkTokens;

@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "moe_experts_internal.h"
+
 namespace moe_ep_detail {
 namespace {
 
@@ -28,12 +30,6 @@ struct BF16 {
   static __device__ __forceinline__ uint16_t from_float(float f) {
     return __builtin_bit_cast(uint16_t, static_cast<__bf16>(f));
   }
-  // v as high + low: 16 significant bits.  Infinities and NaN stay in the high part.
-  static __device__ __forceinline__ void split(float v, uint16_t* hi, uint16_t* lo) {
-    *hi = from_float(v);
-    const float h = to_float(*hi);
-    *lo = __builtin_isfinite(h) ? from_float(v - h) : (uint16_t)0;
-  }
 };
 
 struct F16 {
@@ -52,18 +48,54 @@ struct F16 {
   static __device__ __forceinline__ uint16_t from_float(float f) {
     return __builtin_bit_cast(uint16_t, static_cast<_Float16>(f));
   }
-  // 22 significant bits up to 65504; a finite value beyond that keeps the
-  // rest in the low part, and saturates at 131008.
-  static __device__ __forceinline__ void split(float v, uint16_t* hi, uint16_t* lo) {
-    if (!__builtin_isfinite(v)) {
-      *hi = from_float(v);
-      *lo = 0;
-      return;
-    }
-    *hi = from_float(__builtin_fminf(__builtin_fmaxf(v, -65504.0f), 65504.0f));
-    *lo = from_float(__builtin_fminf(__builtin_fmaxf(v - to_float(*hi), -65504.0f), 65504.0f));
-  }
 };
+
+// v as the sum of kParts bfloat16 (moe_experts_internal.h): 8 significant bits
+// cut off after another, so that nothing is rounded: the three hold float32's
+// 24 bits in float32's range (below 2^-110 the last ones end at bfloat16's
+// smallest value).  An infinity or NaN stays in the first.
+__device__ __forceinline__ void split_parts(float v, uint16_t (&part)[kParts]) {
+  const bool finite = __builtin_isfinite(v);
+  const uint32_t u0 = __float_as_uint(v);
+  const float r1 = v - __uint_as_float(u0 & 0xFFFF0000u);
+  const uint32_t u1 = __float_as_uint(r1);
+  const uint32_t u2 = __float_as_uint(r1 - __uint_as_float(u1 & 0xFFFF0000u));
+  part[0] = finite ? (uint16_t)(u0 >> 16) : BF16::from_float(v);
+  part[1] = finite ? (uint16_t)(u1 >> 16) : (uint16_t)0;
+  part[2] = finite ? (uint16_t)(u2 >> 16) : (uint16_t)0;
+}
+
+// Eight floats as their parts.
+__device__ __forceinline__ void split_floats(const u32x4 (&v)[2], u32x4 (&part)[kParts]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t u[2][kParts];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const float x = __uint_as_float(v[i >> 1][(i & 1) * 2 + c]);
+      u[c][0] = __float_as_uint(x);
+      float r = x - __uint_as_float(u[c][0] & 0xFFFF0000u);
+      r = r == r ? r : 0.0f;              // of an infinity
+      u[c][1] = __float_as_uint(r);
+      u[c][2] = __float_as_uint(r - __uint_as_float(u[c][1] & 0xFFFF0000u));
+    }
+#pragma unroll
+    for (int pl = 0; pl < kParts; ++pl) part[pl][i] = u[0][pl] >> 16 | (u[1][pl] & 0xFFFF0000u);
+  }
+}
+
+// Eight float16 as the sums of two bfloat16 each: 8 bits, then the other 3.
+// Exact for finite values.
+__device__ __forceinline__ void split_f16(const u32x4& v, u32x4* hi, u32x4* lo) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = F16::to_float((uint16_t)v[i]), b = F16::to_float((uint16_t)(v[i] >> 16));
+    const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b) & 0xFFFF0000u;
+    const float ra = a - __uint_as_float(ua & 0xFFFF0000u), rb = b - __uint_as_float(ub);
+    (*hi)[i] = ua >> 16 | ub;
+    (*lo)[i] = __float_as_uint(ra) >> 16 | (__float_as_uint(rb) & 0xFFFF0000u);
+  }
+}
 
 }  // namespace
 }  // namespace moe_ep_detail

@@ -25,6 +25,13 @@ constexpr int kMaxChunks = kPassTokens / kChunkTokens;
 // Waves of a workgroup of the expert kernels; they share the sum over k.
 constexpr int kExpertWaves = 8;
 
+// The activations between the layer's products are float32 values, whole:
+// bfloat16 parts of 8 bits each are what the down product's matrix
+// instructions take.  (Two parts of the activations' own type would halve
+// these instructions' cost, but keep 16 bits for bfloat16, and float16 keeps
+// nothing of small values and ends at 131008.)
+constexpr int kParts = 3;
+
 // Waves of a workgroup of the kernels for many tokens to an expert.
 constexpr int kWideWaves = 4;
 
@@ -64,8 +71,10 @@ struct WeightK {
 struct PlanK {
   int32_t* head;              // [chunks, slots]: pack_head() of the slot's tokens in the chunk
   void* pair;                 // [slots, n] of {token << 6 | top-k slot, weight}, tokens ascending
-  uint16_t* act;              // [2, n * top_k, act_stride]: activations, high and low part
-  int64_t act_plane;          // elements from a high part to its low part
+  // The activations: their parts, bfloat16 [kParts, n * top_k, act_stride]; for
+  // down_kernel with dense weights float32 [n * top_k, act_stride].
+  void* act;
+  int64_t act_plane;          // elements from a part to the next; 0: float32
   int32_t act_stride;
   int32_t slots;
 };

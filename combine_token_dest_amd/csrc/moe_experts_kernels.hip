@@ -136,9 +136,29 @@ __device__ __forceinline__ u32x4 decode(uint32_t w) {
                T::template nibbles<true>(hi)};
 }
 
+// The type of the matrix instruction's operands: the activations' parts are
+// bfloat16 whatever the weights are (4-bit integers are exact in it too, and
+// float16 weights go in as two bfloat16 each).
+template <class T, int P>
+using Operand = std::conditional_t<P == kParts, BF16, T>;
+// Dense weights that go in as two operands.
+template <class T, int G, int P>
+constexpr bool kTwoPartA = G == 0 && P == kParts && std::is_same<T, F16>::value;
+
+// acc += a (and a2) times the P parts of b.
+template <class T, int G, int P>
+__device__ __forceinline__ f32x4 dense_mfma(const u32x4& a, const u32x4& a2, const u32x4 (&b)[P], f32x4 acc) {
+#pragma unroll
+  for (int pl = 0; pl < P; ++pl) {
+    acc = Operand<T, P>::mfma(a, b[pl], acc);
+    if (kTwoPartA<T, G, P>) acc = Operand<T, P>::mfma(a2, b[pl], acc);
+  }
+  return acc;
+}
+
 // One wave's products of TL tiles of 16 weight rows with up to kCols columns
 // of B, one item after another.  An item is count steps s0, s0 + ds, ...; P
-// planes of B (high, low part) are `plane` elements apart.
+// planes of B (an activation's parts) are `plane` elements apart.
 //
 // aim() points the loads at an item, prime() sends out its first kDepth
 // steps' loads, run() goes through the steps, each step's loads kDepth steps
@@ -166,13 +186,20 @@ struct Mac {
   static constexpr int kCols = 64 / kUnits;               // columns of a pass: 4 (4-bit) or 8 (dense)
   static constexpr int kPitch = P * kUnits * 16 + 16;     // bytes from column to column in LDS
   static constexpr int kLds = kCols * kPitch;             // a wave's piece
-  static constexpr int kStageRegs = (W4 ? TL * (4 + 2 * kG) : TL * 8) + P * 4;
+  // Dense weights leave the time to cut float32 columns into their parts on the
+  // way to LDS, which are fewer bytes and registers than the parts (64 experts
+  // of 4096 x 1024, 32 tokens: layer 284 us, and 302 with parts from memory);
+  // 4-bit ones do not (one token's 8 experts of 7168 x 2048: 60 and 54.5 us).
+  static constexpr bool kFloats = P > 1 && !W4;
+  static constexpr int kB = kFloats ? 2 : P;              // 16-byte loads of a step
+  typedef std::conditional_t<kFloats, float, uint16_t> Elem;
+  static constexpr int kStageRegs = (W4 ? TL * (4 + 2 * kG) : TL * 8) + kB * 4;
   static constexpr int kDepth = TL == 2 ? (W4 ? 2 : 3) : (CUT ? 48 : 64) / kStageRegs;   // within 128 registers
 
   struct Stage {
     u32x4 a[TL][W4 ? 1 : 2];
     u32x2 sc[W4 ? TL : 1][kG];
-    u32x4 b[P];
+    u32x4 b[kB];
   };
   struct Item {
     int s0, ds, count;
@@ -182,7 +209,7 @@ struct Mac {
   const uint16_t* scbase[TL];
   uint32_t aoff[TL], scoff[TL], scoff2[TL];
   int shift[TL];
-  const uint16_t* bp;         // B's row of column load_col()
+  const Elem* bp;             // B's row of column load_col()
   int64_t plane;
   char* lds_write;
   const char* lds_read;
@@ -214,7 +241,10 @@ struct Mac {
     // compute() cuts them.
     const int k = CUT ? min(s * kStep + unit8, bend - 8) : s * kStep + unit8;
 #pragma unroll
-    for (int pl = 0; pl < P; ++pl) x.b[pl] = load8(bp + pl * plane + k);
+    for (int i = 0; i < kB; ++i) {
+      if constexpr (kFloats) x.b[i] = gload<u32x4>(bp + k + 4 * i);
+      else x.b[i] = load8(bp + i * plane + k);
+    }
 #pragma unroll
     for (int t = 0; t < TL; ++t) {
       if constexpr (W4) {
@@ -239,7 +269,7 @@ struct Mac {
     }
   }
 
-  __device__ __forceinline__ void aim(const RowPtr<W4> (&ap)[TL], const uint16_t* row) {
+  __device__ __forceinline__ void aim(const RowPtr<W4> (&ap)[TL], const Elem* row) {
     bp = row;
 #pragma unroll
     for (int t = 0; t < TL; ++t) {
@@ -284,38 +314,67 @@ struct Mac {
   }
 
   __device__ __forceinline__ void compute(f32x4 (&acc)[TL], const Stage& x, int s) {
-    const u32x4 minus8 = {T::kMinus8, T::kMinus8, T::kMinus8, T::kMinus8};
-    if (!CUT || s < full) {
-      store_b(x.b);
+    typedef Operand<T, P> O;
+    const u32x4 minus8 = {O::kMinus8, O::kMinus8, O::kMinus8, O::kMinus8};
+    u32x4 b[P];
+    if constexpr (kFloats) {
+      split_floats(x.b, b);
     } else {
-      u32x4 b[P];
 #pragma unroll
-      for (int pl = 0; pl < P; ++pl) b[pl] = cut8(x.b[pl], bend - s * kStep - unit8);
-      store_b(b);
+      for (int pl = 0; pl < P; ++pl) b[pl] = x.b[pl];
     }
+    if (CUT && s >= full) {
+#pragma unroll
+      for (int pl = 0; pl < P; ++pl) b[pl] = cut8(b[pl], bend - s * kStep - unit8);
+    }
+    store_b(b);
     if constexpr (W4) {
 #pragma unroll
       for (int g = 0; g < kG; ++g) {
-        // -8 times the columns' sums, then the nibbles on top of it
         f32x4 corr = {0, 0, 0, 0}, part[TL];
-        u32x4 b[GJ][P];
+        if constexpr (GJ * P <= 4) {
+          // -8 times the columns' sums, then the nibbles on top of it
+          u32x4 b[GJ][P];
 #pragma unroll
-        for (int i = 0; i < GJ; ++i) {
+          for (int i = 0; i < GJ; ++i) {
 #pragma unroll
-          for (int pl = 0; pl < P; ++pl) {
-            b[i][pl] = operand_b(pl, g * GJ + i);
-            corr = T::mfma(minus8, b[i][pl], corr);
+            for (int pl = 0; pl < P; ++pl) {
+              b[i][pl] = operand_b(pl, g * GJ + i);
+              corr = O::mfma(minus8, b[i][pl], corr);
+            }
           }
-        }
 #pragma unroll
-        for (int t = 0; t < TL; ++t) part[t] = corr;
+          for (int t = 0; t < TL; ++t) part[t] = corr;
 #pragma unroll
-        for (int i = 0; i < GJ; ++i) {
+          for (int i = 0; i < GJ; ++i) {
+#pragma unroll
+            for (int t = 0; t < TL; ++t) {
+              const u32x4 f = decode<O>(x.a[t][0][g * GJ + i]);
+#pragma unroll
+              for (int pl = 0; pl < P; ++pl) part[t] = O::mfma(f, b[i][pl], part[t]);
+            }
+          }
+        } else {
+          // side by side: there are no registers for all of a group's parts
+#pragma unroll
+          for (int t = 0; t < TL; ++t) part[t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+          for (int i = 0; i < GJ; ++i) {
+            u32x4 f[TL];
+#pragma unroll
+            for (int t = 0; t < TL; ++t) f[t] = decode<O>(x.a[t][0][g * GJ + i]);
+#pragma unroll
+            for (int pl = 0; pl < P; ++pl) {
+              const u32x4 b = operand_b(pl, g * GJ + i);
+              corr = O::mfma(minus8, b, corr);
+#pragma unroll
+              for (int t = 0; t < TL; ++t) part[t] = O::mfma(f[t], b, part[t]);
+            }
+          }
 #pragma unroll
           for (int t = 0; t < TL; ++t) {
-            const u32x4 f = decode<T>(x.a[t][0][g * GJ + i]);
 #pragma unroll
-            for (int pl = 0; pl < P; ++pl) part[t] = T::mfma(f, b[i][pl], part[t]);
+            for (int r = 0; r < 4; ++r) part[t][r] += corr[r];
           }
         }
 #pragma unroll
@@ -329,18 +388,16 @@ struct Mac {
       }
     } else {
 #pragma unroll
-      for (int pl = 0; pl < P; ++pl) {
+      for (int h = 0; h < 2; ++h) {
+        u32x4 b[P];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const u32x4 b = operand_b(pl, h);
-          if (!CUT || s < full) {
+        for (int pl = 0; pl < P; ++pl) b[pl] = operand_b(pl, h);
 #pragma unroll
-            for (int t = 0; t < TL; ++t) acc[t] = T::mfma(x.a[t][h], b, acc[t]);
-          } else {
-#pragma unroll
-            for (int t = 0; t < TL; ++t)
-              acc[t] = T::mfma(cut8(x.a[t][h], kend - s * kStep - 32 * h - q8), b, acc[t]);
-          }
+        for (int t = 0; t < TL; ++t) {
+          u32x4 a = x.a[t][h], a2 = a;
+          if (CUT && s >= full) a = cut8(a, kend - s * kStep - 32 * h - q8);
+          if constexpr (kTwoPartA<T, G, P>) split_f16(a, &a, &a2);
+          acc[t] = dense_mfma<T, G, P>(a, a2, b, acc[t]);
         }
       }
     }
@@ -575,9 +632,8 @@ __device__ __forceinline__ float pair_weight(const RowsKArgs& a, int pair, int e
 // A workgroup takes one expert (blockIdx.y) and a run of tiles of 16 output
 // rows (GATED: 16 gate rows and the 16 up rows beside them), a.split of its
 // waves to a tile.  It lists the tokens that chose the expert and multiplies
-// them 4 (4-bit) or 8 (dense) at a time.  GATED: silu(gate) * up goes to the workspace in two
-// 16-bit parts (the down product then sees it to 16 bits and more, not
-// rounded to the 8 of a bfloat16), and the first workgroup of an expert
+// them 4 (4-bit) or 8 (dense) at a time.  GATED: silu(gate) * up goes to the
+// workspace whole, in kParts parts, and the first workgroup of an expert
 // leaves the plan down_kernel follows.
 // Bound by HBM where an expert has one pass: gate and up of 64 dense experts 1024
 // x 4096, 32 tokens, 195 us, 5.5 TB/s; 32 4-bit matrices 4096 x 7168 for 48 rows
@@ -728,10 +784,14 @@ __global__ void __launch_bounds__(kThreads, 4)
         // rows past the intermediate size are zeros: the down product reads whole 16-row tiles
         const float act = n < a.inter ? v[0] / (1.0f + expf(-v[0])) * v[TL - 1] : 0.0f;
         const int64_t o = ((int64_t)token * k + (at & 63)) * a.plan.act_stride + n;
-        uint16_t hi, lo;
-        T::split(act, &hi, &lo);
-        a.plan.act[o] = hi;
-        a.plan.act[a.plan.act_plane + o] = lo;
+        if (a.plan.act_plane == 0) {
+          static_cast<float*>(a.plan.act)[o] = act;
+        } else {
+          uint16_t v16[kParts];
+          split_parts(act, v16);
+#pragma unroll
+          for (int pl = 0; pl < kParts; ++pl) static_cast<uint16_t*>(a.plan.act)[pl * a.plan.act_plane + o] = v16[pl];
+        }
       } else if (n < a.inter) {
         store_out<T>(a.out, (int64_t)token * a.out_stride + n, v[0], a.out_f32);
       }
@@ -752,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, 4)
 template <class T, int G, bool CUT>
 __global__ void __launch_bounds__(kThreads, 4) down_kernel(const DownKArgs a) {
   constexpr bool W4 = G != 0;
-  typedef Mac<T, G, false, CUT, 1, 2> M;
+  typedef Mac<T, G, false, CUT, 1, kParts> M;
   __shared__ __attribute__((aligned(16))) char bmem[kExpertWaves][M::kLds];
   __shared__ int heads[MOE_EP_MAX_EXPERTS];
   __shared__ short slots[MOE_EP_MAX_EXPERTS];
@@ -831,7 +891,7 @@ __global__ void __launch_bounds__(kThreads, 4) down_kernel(const DownKArgs a) {
     const RowPtr<W4> ap[1] = {row_ptr<W4>(a.w, it.expert, tile * 16)};
     // lane c < kCols has column c's record; the lanes that load the column need it
     const int pair = __shfl(it.rec.pair, M::load_col());
-    mac.aim(ap, p.act + ((int64_t)(pair >> 6) * a.top_k + (pair & 63)) * p.act_stride);
+    mac.aim(ap, static_cast<const typename M::Elem*>(p.act) + ((int64_t)(pair >> 6) * a.top_k + (pair & 63)) * p.act_stride);
     return mac.item(it.k0, it.k1, 1);
   };
   Item cur;
@@ -963,6 +1023,7 @@ struct WideMac {
       }
     };
     auto compute = [&](const Stage& x, int s) {
+      typedef Operand<T, P> O;
       const int buffer = (s & 1) * kBuffer;
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
@@ -981,7 +1042,7 @@ struct WideMac {
         return *reinterpret_cast<const u32x4*>(read + buffer + ct * 16 * kPitch + pl * kUnits * 16 + j * 64);
       };
       if constexpr (W4) {
-        const u32x4 minus8 = {T::kMinus8, T::kMinus8, T::kMinus8, T::kMinus8};
+        const u32x4 minus8 = {O::kMinus8, O::kMinus8, O::kMinus8, O::kMinus8};
 #pragma unroll
         for (int g = 0; g < kG; ++g) {
           u32x4 f[TL][GJ];
@@ -990,28 +1051,42 @@ struct WideMac {
           for (int t = 0; t < TL; ++t) {
             sc[t] = scale_floats<T>(x.sc[t][g]);
 #pragma unroll
-            for (int i = 0; i < GJ; ++i) f[t][i] = decode<T>(x.a[t][0][g * GJ + i]);
+            for (int i = 0; i < GJ; ++i) f[t][i] = decode<O>(x.a[t][0][g * GJ + i]);
           }
 #pragma unroll
           for (int ct = 0; ct < CT; ++ct) {
             f32x4 corr = {0, 0, 0, 0}, part[TL];
-            u32x4 b[GJ][P];
+            if constexpr (P == 1) {
+              u32x4 b[GJ];
 #pragma unroll
-            for (int i = 0; i < GJ; ++i) {
-#pragma unroll
-              for (int pl = 0; pl < P; ++pl) {
-                b[i][pl] = operand_b(ct, pl, g * GJ + i);
-                corr = T::mfma(minus8, b[i][pl], corr);
+              for (int i = 0; i < GJ; ++i) {
+                b[i] = operand_b(ct, 0, g * GJ + i);
+                corr = O::mfma(minus8, b[i], corr);
               }
-            }
 #pragma unroll
-            for (int t = 0; t < TL; ++t) part[t] = corr;
+              for (int t = 0; t < TL; ++t) part[t] = corr;
 #pragma unroll
-            for (int i = 0; i < GJ; ++i) {
+              for (int i = 0; i < GJ; ++i) {
 #pragma unroll
-              for (int pl = 0; pl < P; ++pl) {
+                for (int t = 0; t < TL; ++t) part[t] = O::mfma(f[t][i], b[i], part[t]);
+              }
+            } else {
 #pragma unroll
-                for (int t = 0; t < TL; ++t) part[t] = T::mfma(f[t][i], b[i][pl], part[t]);
+              for (int t = 0; t < TL; ++t) part[t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+              for (int i = 0; i < GJ; ++i) {
+#pragma unroll
+                for (int pl = 0; pl < P; ++pl) {
+                  const u32x4 b = operand_b(ct, pl, g * GJ + i);
+                  corr = O::mfma(minus8, b, corr);
+#pragma unroll
+                  for (int t = 0; t < TL; ++t) part[t] = O::mfma(f[t][i], b, part[t]);
+                }
+              }
+#pragma unroll
+              for (int t = 0; t < TL; ++t) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) part[t][r] += corr[r];
               }
             }
 #pragma unroll
@@ -1023,25 +1098,26 @@ struct WideMac {
           __builtin_amdgcn_sched_barrier(0);
         }
       } else {
-        u32x4 f[TL][2];
+        u32x4 f[TL][2], f2[TL][2];
 #pragma unroll
         for (int t = 0; t < TL; ++t) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             f[t][h] = x.a[t][h];
             if (CUT && s >= full) f[t][h] = cut8(f[t][h], kend - s * kStep - 32 * h - q8);
+            if constexpr (kTwoPartA<T, G, P>) split_f16(f[t][h], &f[t][h], &f2[t][h]);
+            else f2[t][h] = f[t][h];
           }
         }
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
 #pragma unroll
-          for (int pl = 0; pl < P; ++pl) {
+          for (int h = 0; h < 2; ++h) {
+            u32x4 b[P];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const u32x4 b = operand_b(ct, pl, h);
+            for (int pl = 0; pl < P; ++pl) b[pl] = operand_b(ct, pl, h);
 #pragma unroll
-              for (int t = 0; t < TL; ++t) acc[t][ct] = T::mfma(f[t][h], b, acc[t][ct]);
-            }
+            for (int t = 0; t < TL; ++t) acc[t][ct] = dense_mfma<T, G, P>(f[t][h], f2[t][h], b, acc[t][ct]);
           }
         }
       }
@@ -1145,8 +1221,10 @@ __device__ __forceinline__ int busiest(const RowsKArgs& a, int rank, int* counts
 template <class T, int G, WideOp OP, bool SHIFT, bool CUT>
 __global__ void __launch_bounds__(kWideThreads, OP == kWideDown ? 2 : 3) wide_kernel(const RowsKArgs a) {
   constexpr bool W4 = G != 0;
-  constexpr int TL = 2, P = OP == kWideDown ? 2 : 1, kMost = kWideTiles;
-  __shared__ int list[kPassTokens];
+  constexpr int TL = 2, P = OP == kWideDown ? kParts : 1, kMost = kWideTiles;
+  // kWideDown's list stays in the plan: beside the activations' parts it would
+  // leave room for one workgroup on a compute unit instead of two.
+  __shared__ int list[OP == kWideDown ? 1 : kPassTokens];
   __shared__ Lister<kWideWaves> lister;
   __shared__ __attribute__((aligned(16))) char bmem[2 * WideMac<T, G, SHIFT, CUT, P, kMost>::kBuffer];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -1160,8 +1238,6 @@ __global__ void __launch_bounds__(kWideThreads, OP == kWideDown ? 2 : 3) wide_ke
   if (OP == kWideDown) {
     m = p.head[slot];
     expert = __builtin_amdgcn_readfirstlane(p.head[p.slots + slot]);
-    for (int i = tid; i < m; i += kWideThreads) list[i] = rec[i].pair;
-    __syncthreads();
   } else if (a.ids == nullptr) {
     for (int i = tid; i < a.n; i += kWideThreads) list[i] = i << 6;
     __syncthreads();
@@ -1191,6 +1267,7 @@ __global__ void __launch_bounds__(kWideThreads, OP == kWideDown ? 2 : 3) wide_ke
   m = __builtin_amdgcn_readfirstlane(m);
   if (m == 0) return;
 
+  auto pair_at = [&](int i) { return OP == kWideDown ? gload<int>(&rec[i].pair) : list[i]; };
   const bool whole = whole_rows(a);
   RowPtr<W4> ap[TL];
   int tile[TL];           // of the output; past the last one: not stored
@@ -1209,8 +1286,8 @@ __global__ void __launch_bounds__(kWideThreads, OP == kWideDown ? 2 : 3) wide_ke
       for (int ct = 0; ct < CT; ++ct) acc[t][ct] = f32x4{0, 0, 0, 0};
     }
     auto col_row = [&](int c) -> const uint16_t* {      // columns past the list repeat its last token
-      const int at = list[min(c0 + c, m - 1)];
-      if constexpr (OP == kWideDown) return a.plan.act + ((int64_t)(at >> 6) * k + (at & 63)) * a.plan.act_stride;
+      const int at = pair_at(min(c0 + c, m - 1));
+      if constexpr (OP == kWideDown) return static_cast<const uint16_t*>(a.plan.act) + ((int64_t)(at >> 6) * k + (at & 63)) * a.plan.act_stride;
       else return a.x + (int64_t)(at >> 6) * a.x_stride;
     };
     WideMac<T, G, SHIFT, CUT, P, CT>::run(acc, a.w, ap, col_row, a.plan.act_plane,
@@ -1219,22 +1296,24 @@ __global__ void __launch_bounds__(kWideThreads, OP == kWideDown ? 2 : 3) wide_ke
     for (int ct = 0; ct < CT; ++ct) {
       const int i = c0 + ct * 16 + (lane & 15);
       if (i >= m) continue;
-      const int at = list[i];
+      const int at = pair_at(i);
       const int64_t pair = (int64_t)(at >> 6) * k + (at & 63);
       if constexpr (OP == kWideGated) {
         if (tile[0] >= tiles) continue;
         const int n = tile[0] * 16 + (lane >> 4) * 4;
-        uint16_t hi[4], lo[4];
+        uint16_t v16[4][kParts];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const float g = acc[0][ct][r], u = acc[1][ct][r];
           // rows past the intermediate size are zeros: the down product reads whole 16-row tiles
-          T::split(n + r < a.inter ? g / (1.0f + expf(-g)) * u : 0.0f, &hi[r], &lo[r]);
+          split_parts(n + r < a.inter ? g / (1.0f + expf(-g)) * u : 0.0f, v16[r]);
         }
-        uint16_t* o = a.plan.act + pair * a.plan.act_stride + n;      // a multiple of four elements
-        *reinterpret_cast<u32x2*>(o) = u32x2{hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16};
-        *reinterpret_cast<u32x2*>(o + a.plan.act_plane) =
-            u32x2{lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16};
+        uint16_t* o = static_cast<uint16_t*>(a.plan.act) + pair * a.plan.act_stride + n;      // a multiple of four elements
+#pragma unroll
+        for (int pl = 0; pl < kParts; ++pl) {
+          *reinterpret_cast<u32x2*>(o + pl * a.plan.act_plane) =
+              u32x2{v16[0][pl] | (uint32_t)v16[1][pl] << 16, v16[2][pl] | (uint32_t)v16[3][pl] << 16};
+        }
       } else {
         float weight = 1.0f;
         if constexpr (OP == kWideDown) weight = rec[i].weight;

@@ -384,7 +384,8 @@ MOE_EP_API int moe_ep_route(const moe_ep_router* router, const void* logits, int
  * 4 bytes at (16 i + r) * 16 + 4 j: byte e of them holds column e < 4 in its
  * low half and column e + 4 in its high half.  Rows past N and columns past
  * K are padding of any value.  A token whose activations hold an infinity
- * gets NaN from 4-bit weights. */
+ * gets NaN from 4-bit weights, and so may one whose activations' sums times
+ * 15 are beyond float32 (q x and 8 x are summed apart). */
 typedef struct moe_ep_weight {
   const void* data;
   const void* scales;
@@ -461,8 +462,9 @@ MOE_EP_API int moe_ep_layer_workspace_bytes(const moe_ep_layer_args* args, size_
  * calls; calls that may overlap in time (other streams, graphs replayed side
  * by side) need one each.
  *
- * Between the products an activation keeps 16 significant bits (bfloat16)
- * or 22 (float16, where it saturates at 131008). */
+ * Between the products an activation is a float32 value, whole: what is
+ * small or large beside float16's own range keeps its 24 bits.  An infinite
+ * weight in down may give NaN where the formula has an infinity. */
 MOE_EP_API int moe_ep_layer(const moe_ep_layer_args* args, void* stream);
 
 /* Static text for a status code. */
