@@ -261,10 +261,10 @@ __device__ __forceinline__ void route_token(const RouteKArgs& a, int64_t t, doub
   }
 
   if (!scores && a.score == MOE_EP_SCORE_SOFTMAX && !a.renormalize) {
-    float s = 0.0f;
+    double s = 0.0;
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) s += l[v] == -INFINITY ? 0.0f : expf(l[v] - top);
-    total = (double)reduce_sum<LPT>(s);
+    for (int v = 0; v < VPL; ++v) s += l[v] == -INFINITY ? 0.0 : score64(MOE_EP_SCORE_SOFTMAX, l[v], top);
+    total = reduce_sum<LPT>(s);
   }
   const bool open = mine != INT_MAX && sub < a.top_k;
   const double s = open ? score64(a.score, mine_l, top) : 0.0;

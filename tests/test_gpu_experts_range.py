@@ -12,7 +12,7 @@ import pytest
 import torch
 
 import combine_token_dest_amd as pkg
-from combine_token_dest_amd import W4Weights, moe_layer
+from combine_token_dest_amd import Router, W4Weights, moe_layer, route
 from tests import experts_ref as ref
 
 pytestmark = pytest.mark.gpu
@@ -111,3 +111,21 @@ def test_layer_keeps_every_activation_whole(dtype, g, size, many):
     tol = 30 * HALF * w.double() * mag[e, :, at] * v.abs().unsqueeze(1) + 2.0 ** -149
     close(moe_layer(x.cuda(), take_gu, take_dn, ids.cuda(), w.cuda(), out_dtype=F32), want, tol,
           f"activations {v.abs().min():.1e} to {v.abs().max():.1e}")
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("n,E,k", [(1, 1024, 8), (37, 60, 4), (300, 256, 8), (2050, 128, 8), (2100, 256, 16)])
+def test_route_weights_are_rounded_once(n, E, k, score, renorm):
+    """Each weight is its float64 value rounded to float32: half a step (2^-24),
+    and 2^-40 for a float64 sum of up to 1024 exponentials and the quotients.
+    Logits of float32 with all their bits, -8 to 8 and a few beyond."""
+    print(f"[route weights] n={n} E={E} k={k} {score} renorm={renorm}", flush=True)
+    logits = torch.randn(n, E, generator=gen(n + E)) * 3
+    logits[:, ::7] *= 2
+    r = Router(k, score, renormalize=renorm, scale=2.5)
+    ids, w = route(logits.cuda(), r)
+    want_ids, want_w = ref.route(logits, k, score, renormalize=renorm, scale=2.5)
+    assert ids.tolist() == want_ids
+    want = torch.tensor(want_w, dtype=torch.float64)
+    close(w, want, want * (HALF + 2.0 ** -40) + 2.0 ** -149, "weights")
