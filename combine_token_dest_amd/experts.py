@@ -213,10 +213,16 @@ def _output(out, shape, dtype, out_dtype, x) -> torch.Tensor:
     return out
 
 
+def int32_ids(t: torch.Tensor) -> torch.Tensor:
+    """int64 expert ids as the library's int32.  What int32 does not hold
+    becomes its first or last value, which names no expert either (wrapped, it
+    could)."""
+    return t.clamp(-0x80000000, 0x7fffffff).to(torch.int32)
+
+
 def _ids(t: torch.Tensor, shape, dev: int, what: str) -> torch.Tensor:
     if t.dtype == torch.int64:
-        # The library takes int32 ids; expert ids must fit in int32.
-        t = t.to(torch.int32)
+        t = int32_ids(t)
     if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape):
         raise ValueError(f"{what} must be int32 (or int64, converted) {list(shape)}")
     if t.get_device() != dev:

@@ -21,7 +21,7 @@ import torch
 
 from . import _lib
 from ._lib import MOE_EP_ALL_RANKS, MOE_EP_BF16, MOE_EP_F16, MOE_EP_F32
-from .experts import Weight, moe_layer
+from .experts import Weight, int32_ids, moe_layer
 
 _COMBINE_DTYPES = {torch.float32: MOE_EP_F32, torch.bfloat16: MOE_EP_BF16, torch.float16: MOE_EP_F16}
 
@@ -190,8 +190,7 @@ class MoEEp:
         for s in range(ep):
             h, ids = hidden_states[s], topk_ids[s]
             if ids.dtype == torch.int64:
-                # The library takes int32 ids; expert ids must fit in int32.
-                ids = ids.to(torch.int32)
+                ids = int32_ids(ids)
                 keep.append(ids)
             if ids.dtype != torch.int32:
                 raise TypeError("topk_ids must be int32 (or int64, converted)")

@@ -12,7 +12,7 @@ import pytest
 import torch
 
 import combine_token_dest_amd as pkg
-from combine_token_dest_amd import Router, W4Weights, moe_layer, route
+from combine_token_dest_amd import MoEEp, Router, W4Weights, expert_linear, moe_layer, route
 from tests import experts_ref as ref
 
 pytestmark = pytest.mark.gpu
@@ -129,3 +129,28 @@ def test_route_weights_are_rounded_once(n, E, k, score, renorm):
     assert ids.tolist() == want_ids
     want = torch.tensor(want_w, dtype=torch.float64)
     close(w, want, want * (HALF + 2.0 ** -40) + 2.0 ** -149, "weights")
+
+
+def test_int64_ids_past_32_bits_name_no_expert():
+    """Ids that an int32 would wrap into the experts' range: zeros, as for any
+    other id outside, and no copy of the row in dispatch."""
+    E, H, I = 8, 64, 32
+    far = [2 ** 32 + 3, -2 ** 32 + 1, 2 ** 40 + 2, -2 ** 63, 2 ** 63 - 1, 2 ** 31, 5, -1]
+    n = len(far)
+    x = torch.randn(n, H, generator=gen(1)).to(BF16).cuda()
+    gu = torch.randn(E, 2 * I, H, generator=gen(2)).to(BF16).cuda()
+    dn = torch.randn(E, H, I, generator=gen(3)).to(BF16).cuda()
+    ids = torch.tensor(far, device="cuda")
+    near = torch.tensor([v if abs(v) < 2 ** 31 else -1 for v in far], dtype=torch.int32, device="cuda")
+    assert torch.equal(expert_linear(x, gu, ids), expert_linear(x, gu, near))
+    got = moe_layer(x, gu, dn, ids.view(n, 1))
+    assert torch.equal(got, moe_layer(x, gu, dn, near.view(n, 1)))
+    assert (got[:6] == 0).all() and (got[6] != 0).any()
+    moe = MoEEp(1, E, 1, n, H)
+    try:
+        res = moe.dispatch([x], [ids.view(n, 1)], [torch.ones(n, 1, device="cuda")])
+        took = (res[0].topk_ids >= 0) & (res[0].topk_ids < E)
+        assert took.flatten().tolist() == [v == 5 for v in far]
+        moe.combine([res[0].hidden])
+    finally:
+        moe.destroy()
