@@ -9,7 +9,8 @@ Every step runs in the library's gfx950 kernels (include/moe_ep.h); torch is
 used for device memory and the current stream.  Work is enqueued on the
 current stream of the tensors' device; what a call needs beyond its inputs
 comes from torch's allocator for that stream, so calls may be captured into
-graphs and run on several streams at once.
+graphs and run on several streams at once.  There is no backward pass: tensors
+that require gradients are refused outside ``torch.no_grad()``.
 """
 
 from __future__ import annotations
@@ -150,6 +151,17 @@ class W4Weights:
 Weight = Union[torch.Tensor, W4Weights]
 
 
+def _forward_only(what: str, *tensors) -> None:
+    """Refuses what autograd would have to record (the result has no graph)."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if isinstance(t, W4Weights):
+                t = t.scales
+            if t is not None and t.requires_grad:
+                raise RuntimeError(f"{what} has no backward pass, but a tensor requires gradients: "
+                                   f"call it under torch.no_grad() or with detached tensors")
+
+
 def _on(t: torch.Tensor, dev: int, what: str) -> int:
     if t.get_device() != dev:
         raise ValueError(f"{what} is on {t.device}, expected cuda:{dev}")
@@ -284,6 +296,7 @@ def route(logits: torch.Tensor, router: Router, *, topk_ids: Optional[torch.Tens
     take.  Ties go to the lowest id; an expert whose logit or bias is -inf or
     NaN is never chosen, and a slot left without one gets
     ``invalid_expert_id`` and weight 0.  See include/moe_ep.h, moe_ep_route."""
+    _forward_only("route", logits, router.bias, topk_weights)
     dev, dtype, stride = _logits(logits)
     n, E = logits.shape
     _int32(n, "token count")
@@ -314,6 +327,7 @@ def expert_linear(x: torch.Tensor, weight: Weight, expert_ids: Optional[torch.Te
     ``expert_ids`` every row is multiplied with the first expert's matrix.
     The result is of x's type or float32 (``out_dtype``).  Made for the few
     rows of a decode step; see include/moe_ep.h, moe_ep_expert_linear."""
+    _forward_only("expert_linear", x, weight, out)
     dev = _activations(x, "x")
     a = _lib.moe_ep_linear_args()
     E, N, K = _weight(weight, dev, x.dtype, "weight", a.weight)
@@ -353,6 +367,8 @@ def moe_layer(hidden: torch.Tensor, gate_up: Weight, down: Weight, topk_ids: Opt
     ``workspace`` (uint8, ``moe_layer_workspace_bytes`` of it) is taken from
     torch's allocator when not passed; one that is passed must not be used by
     two calls that may overlap in time.  See include/moe_ep.h, moe_ep_layer."""
+    _forward_only("moe_layer", hidden, gate_up, down, topk_weights, router_logits,
+                  None if router is None else router.bias, out)
     dev = _activations(hidden, "hidden")
     a = _lib.moe_ep_layer_args()
     dtype = hidden.dtype
