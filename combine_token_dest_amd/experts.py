@@ -88,6 +88,9 @@ class W4Weights:
         g = next((g for g in (32, 64, 128) if -(-K // g) == scales.shape[2]), None)
         if g is None:
             raise ValueError(f"{scales.shape[2]} scale groups do not cover {K} columns by 32, 64 or 128")
+        whole = q == q.round() if q.is_floating_point() else True
+        if not bool(((q >= 0) & (q <= 15) & whole).all()):
+            raise ValueError("q must be integers in 0..15")
         nt, kb = -(-N // _TILE_ROWS), -(-K // _TILE_COLS)
         full = torch.full((E, nt * _TILE_ROWS, kb * _TILE_COLS), 8, dtype=torch.uint8, device=q.device)
         full[:, :N, :K] = q.to(torch.uint8)
@@ -96,7 +99,7 @@ class W4Weights:
         data = (v[..., 0, :] | (v[..., 1, :] << 4)).permute(0, 1, 3, 5, 2, 4, 6)
         sc = torch.zeros((E, nt * _TILE_ROWS, kb * _TILE_COLS // g), dtype=scales.dtype, device=scales.device)
         sc[:, :N, :scales.shape[2]] = scales
-        sc = sc.view(E, nt, _TILE_ROWS, -1).transpose(2, 3)
+        sc = sc.view(E, nt, _TILE_ROWS, kb * _TILE_COLS // g).transpose(2, 3)
         return cls(data.reshape(E, nt, kb, _TILE_BYTES).contiguous(), sc.contiguous(), N, K)
 
     @classmethod

@@ -56,3 +56,23 @@ def test_route_refuses_tensors_that_require_gradients(which):
         route(logits, r, topk_weights=w)
     with torch.no_grad(), pytest.raises(ValueError, match="GPU"):
         route(logits, r, topk_weights=w)
+
+
+@pytest.mark.parametrize("q", [16, -1, 255, 2.5, float("nan")])
+def test_pack_refuses_what_four_bits_do_not_hold(q):
+    """One such value would change its neighbour in the byte."""
+    t = torch.full((1, 16, 128), 8.0)
+    t[0, 3, 5] = q
+    t = t if isinstance(q, float) else t.to(torch.int32)
+    with pytest.raises(ValueError, match="0..15"):
+        W4Weights.pack(t, torch.ones(1, 16, 1).half())
+
+
+def test_pack_takes_integers_of_any_type():
+    q = torch.randint(0, 16, (2, 16, 128), generator=torch.Generator().manual_seed(1), dtype=torch.uint8)
+    s = torch.ones(2, 16, 4).half()
+    want = W4Weights.pack(q, s).data
+    for t in (q.to(torch.int8), q.long(), q.float()):
+        assert torch.equal(W4Weights.pack(t, s).data, want)
+    empty = W4Weights.pack(q[:0], s[:0])
+    assert empty.num_experts == 0
