@@ -106,7 +106,8 @@ class W4Weights:
     def quantize(cls, w: torch.Tensor, group_size: int = 128) -> "W4Weights":
         """Nearest 4-bit weights of dense ``w`` [experts, rows, cols] or
         [rows, cols] (bfloat16 or float16): a group's scale is its largest
-        magnitude / 7, rounded to w's type."""
+        magnitude / 7, rounded to w's type.  A group with an infinity or NaN
+        becomes NaN as a whole."""
         if w.dtype not in (torch.bfloat16, torch.float16):
             raise TypeError("weights must be bfloat16 or float16")
         if group_size not in (32, 64, 128):
@@ -119,7 +120,7 @@ class W4Weights:
         x = x.view(E, N, groups, group_size)
         scales = (x.abs().amax(3) / 7).to(w.dtype)
         s = scales.float().unsqueeze(3)
-        q = torch.where(s > 0, x / s, torch.zeros_like(x)).round().clamp(-8, 7) + 8
+        q = torch.where((s > 0) & (s < math.inf), x / s, torch.zeros_like(x)).round().clamp(-8, 7) + 8
         q = q.view(E, N, groups * group_size)[:, :, :K]
         # spelled out, since several group sizes can give this number of groups
         return cls._pack_groups(q, scales, group_size)

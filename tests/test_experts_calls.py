@@ -76,3 +76,17 @@ def test_pack_takes_integers_of_any_type():
         assert torch.equal(W4Weights.pack(t, s).data, want)
     empty = W4Weights.pack(q[:0], s[:0])
     assert empty.num_experts == 0
+
+
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_quantize_marks_a_group_it_cannot_scale(dtype, bad):
+    """A group with an infinity or NaN becomes NaN as a whole, not finite
+    values or an infinity of the other sign; its neighbours stay."""
+    w = torch.randn(1, 16, 128, generator=torch.Generator().manual_seed(2)).to(dtype)
+    clean = W4Weights.quantize(w, 32).dequantize()
+    w[0, 3, 40] = bad
+    got = W4Weights.quantize(w, 32).dequantize()
+    assert got[0, 3, 32:64].isnan().all()
+    got[0, 3, 32:64] = clean[0, 3, 32:64]
+    assert torch.equal(got, clean)
