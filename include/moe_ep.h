@@ -410,9 +410,11 @@ typedef struct moe_ep_linear_args {
 
 /* out[r] = W[expert_ids[r] - expert_offset] x[r].  Rows whose id is outside
  * [expert_offset, expert_offset + num_experts) get zeros.  Made for the few
- * rows of a decode step: the weights of each used expert are read once per
- * 2048 rows.  One kernel launch per 2048 rows.  x and out, each from its
- * first element to its last, must not overlap. */
+ * rows of a decode step: a used expert's weights are gone through once for
+ * every 4 (4-bit) or 8 (dense) of its rows, or for every 48 where it has many,
+ * after the first time from a cache where they fit.  One kernel launch per
+ * 2048 rows.  x and out, each from its first element to its last, must not
+ * overlap. */
 MOE_EP_API int moe_ep_expert_linear(const moe_ep_linear_args* args, void* stream);
 
 typedef struct moe_ep_layer_args {
@@ -442,7 +444,11 @@ typedef struct moe_ep_layer_args {
 
 /* Bytes of device workspace moe_ep_layer needs for these sizes (the sizes,
  * gate_up.group_size and whether a router is set are read; pointers are not
- * followed).  What serves a number of tokens serves any smaller one. */
+ * followed).  What serves a number of tokens serves any smaller one.  It is
+ * for a pass of up to 2048 tokens and counts every (token, slot) pair, its
+ * expert here or not: 6 bytes for each column of intermediate_size, and with
+ * many tokens to an expert 4 for each of hidden_size (1024 rows, top_k 8,
+ * hidden 7168, intermediate 2048: 320 MiB). */
 MOE_EP_API int moe_ep_layer_workspace_bytes(const moe_ep_layer_args* args, size_t* out_bytes);
 
 /* The experts of a mixture-of-experts layer, whole:
