@@ -175,8 +175,8 @@ constexpr int32_t kMinRow = 8;
 // over k between waves; the wide ones read the weights once per 48 tokens, but
 // a workgroup covers `tile_rows` of the weights' rows and goes through all of
 // k alone.  Measured, narrow / wide in us:
-//   layer, 64 experts, top-8, 4096 x 1024, 4 bits: 8 tokens 78 / 82, 16: 90 / 90, 32: 138 / 104, 128: 379 / 134
-//   the same dense:                                32 tokens 284 / 315, 64: 382 / 325, 128: 628 / 339
+//   layer, 64 experts, top-8, 4096 x 1024, 4 bits: 8 tokens 79 / 79, 16: 113 / 102, 32: 153 / 111, 128: 413 / 132
+//   the same dense:                                32 tokens 284 / 302, 64: 390 / 308, 128: 625 / 318
 //   one 4-bit matrix 4096 x 4096: 24 rows 15 / 20, 48: 27 / 27, 96: 50 / 27;  4096 x 1024: 12 rows 7.3 / 6.0
 //   one dense matrix 4096 x 4096: 48 rows 33 / 35, 96: 63 / 35;  4096 x 1024: 12 rows 7.6 / 11, 48: 17 / 11
 // (The experts' tokens are counted as if all of them were chosen here.)

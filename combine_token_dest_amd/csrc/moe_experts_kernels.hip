@@ -641,8 +641,8 @@ __device__ __forceinline__ float pair_weight(const RowsKArgs& a, int pair, int e
 // ROUTED (a few tokens, GATED): every workgroup makes the router's choice for
 // itself, a wave for each token.  One token of 256 grouped experts takes it 5.5
 // us, little less than a kernel of its own (6.4), but the launch and the wait
-// between the two are saved (that layer, 4-bit: 54.1 -> 52.3 us; two tokens of 8
-// small experts: 20.2 -> 17.6).
+// between the two are saved (2 us of that layer with 4-bit weights, 53; two tokens
+// of 8 small experts: 20.2 -> 17.6).
 template <class T, int G, bool GATED, bool SHIFT, bool CUT, bool ROUTED>
 __global__ void __launch_bounds__(kThreads, 4)
     rows_kernel(const std::conditional_t<ROUTED, RowsRoutedKArgs, RowsKArgs> a) {
@@ -807,8 +807,10 @@ __global__ void __launch_bounds__(kThreads, 4)
 // weight * product into its own copy of the chunk's output tile in LDS (each
 // token at most once per expert, so lanes never meet), and the copies are
 // added in wave order at the end.
-// Bound by HBM: 64 dense experts 4096 x 1024, 32 tokens, 99 us, 5.4 TB/s; one
-// token's 8 4-bit experts 7168 x 2048 21 us, 2.8 TB/s, a fifth of it start-up.
+// Bound by HBM: 64 dense experts 4096 x 1024, 32 tokens, 104 us, 5.1 TB/s; one
+// token's 8 4-bit experts 7168 x 2048 24 us, 2.5 TB/s, a fifth of it start-up and
+// three steps of loads ahead, not four, for the activations' parts (21.4 us with two
+// parts).
 template <class T, int G, bool CUT>
 __global__ void __launch_bounds__(kThreads, 4) down_kernel(const DownKArgs a) {
   constexpr bool W4 = G != 0;
@@ -933,12 +935,12 @@ __global__ void __launch_bounds__(kThreads, 4) down_kernel(const DownKArgs a) {
 
 constexpr int kWideThreads = kWideWaves * 64;
 
-// What a wide workgroup computes.
 // Most tiles of 16 columns in a pass: 48 columns leave registers for three
 // workgroups on a compute unit, 64 for two (gate and up of 32 experts, 4096 x
 // 7168, 4 bits, 32 tokens each: 208 and 212 us).
 constexpr int kWideTiles = 3;
 
+// What a wide workgroup computes.
 enum WideOp { kWideLinear, kWideGated, kWideDown };
 
 // One pass of a workgroup: kWideWaves * TL tiles of 16 weight rows, TL to a
@@ -1216,8 +1218,9 @@ __device__ __forceinline__ int busiest(const RowsKArgs& a, int rank, int* counts
 // weighted product, in float32, for sum_kernel.
 // Bound by issue: decoding, matrix and LDS instructions of a step hardly overlap
 // between the waves of a workgroup, which the barrier keeps together.  32 4-bit
-// experts of 4096 x 7168 and 7168 x 2048, some 1200 pairs: 196 and 143 us (1.6 to
-// 2.4 TB/s of weights, an expert of 130 tokens three times), sum_kernel 16.
+// experts of 4096 x 7168 and 7168 x 2048, some 1200 pairs: 197 and 190 us (1.3 to
+// 2.4 TB/s of weights, an expert of 130 tokens three times), sum_kernel 15; with
+// activations in two parts kWideDown would take 143.
 template <class T, int G, WideOp OP, bool SHIFT, bool CUT>
 __global__ void __launch_bounds__(kWideThreads, OP == kWideDown ? 2 : 3) wide_kernel(const RowsKArgs a) {
   constexpr bool W4 = G != 0;
@@ -1403,7 +1406,7 @@ void start_wide(RowsKArgs a, hipStream_t stream) {
   const int per = kWideWaves * (OP == kWideGated ? 1 : 2);
   // The passes over an expert's tokens go to workgroups of their own while
   // these fill the card (they meet in L2; layer, 695 tokens of 4 of 8 experts,
-  // 1784 x 200, 4 bits: 98 us, and 258 with one workgroup for all passes), as
+  // 1784 x 200, 4 bits: 73 us, and 266 with one workgroup for all passes), as
   // many as all experts' tokens evenly spread would take.  Once the card is
   // full they would only come too late to find the weights in L2 (32 dense
   // matrices 2048 x 2048, 96 rows each: 139 us, and 103 in one workgroup).
@@ -1414,8 +1417,8 @@ void start_wide(RowsKArgs a, hipStream_t stream) {
   const dim3 grid((tiles + per - 1) / per, slots, (unsigned)std::max<int64_t>(1, std::min(passes, 512 / blocks)));
   // The card holds some 768 workgroups at once: an expert of several passes that
   // started with the last of them would run on alone.  (32 experts of 4096 x
-  // 7168 and 7168 x 2048, 4 bits, 1 to 130 of 1389 pairs each: layer 483 us in
-  // the experts' order, 401 busiest first; 0 to 107 of 1147: 350 and 345.)
+  // 7168 and 7168 x 2048, 4 bits, 1 to 130 of 1389 pairs each: layer 525 us in
+  // the experts' order, 413 busiest first; 0 to 107 of 1147: 352 and 341.)
   // (kWideDown follows kWideGated's order, whose w.cols are its rows.)
   const int64_t then = OP == kWideGated ? ((int64_t)a.w.cols + kWideWaves * 32 - 1) / (kWideWaves * 32) * slots : 0;
   a.busiest_first = OP != kWideDown && a.ids != nullptr && !a.by_pair && std::max(blocks, then) > 512 &&
