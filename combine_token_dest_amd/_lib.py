@@ -27,6 +27,7 @@ MOE_EP_ERR_UNSUPPORTED = -7
 MOE_EP_F32 = 0
 MOE_EP_BF16 = 1
 MOE_EP_F16 = 2
+MOE_EP_E4M3 = 8
 
 MOE_EP_ORDER_AUTO = 0
 MOE_EP_ORDER_SOURCE_ROW = 1
@@ -40,7 +41,9 @@ EXPORTS = [
     "moe_ep_get_combine_input_buffer", "moe_ep_combine", "moe_ep_destroy",
     "moe_ep_create_vmm", "moe_ep_workspace", "moe_ep_checkpoint_prepare", "moe_ep_checkpoint_restore",
     "moe_ep_dispatch_noalloc", "moe_ep_active_rank_mask", "moe_ep_route", "moe_ep_expert_linear",
-    "moe_ep_layer_workspace_bytes", "moe_ep_layer", "moe_ep_status_string", "moe_ep_last_error",
+    "moe_ep_layer_workspace_bytes", "moe_ep_layer", "moe_ep_rms_norm", "moe_ep_gated",
+    "moe_ep_gated_grad_workspace_bytes", "moe_ep_gated_grad", "moe_ep_adapter_workspace_bytes",
+    "moe_ep_adapter_linear", "moe_ep_status_string", "moe_ep_last_error",
 ]
 
 MOE_EP_NOALLOC_MAX_ROWS = 65536
@@ -48,6 +51,7 @@ MOE_EP_NOALLOC_MAX_ROWS = 65536
 MOE_EP_MAX_EXPERTS = 1024
 MOE_EP_MAX_TOPK = 64
 MOE_EP_MAX_GROUPS = 64
+MOE_EP_MAX_RANK = 1024
 
 MOE_EP_SCORE_SOFTMAX = 0
 MOE_EP_SCORE_SIGMOID = 1
@@ -124,6 +128,44 @@ class moe_ep_layer_args(Structure):
     ]
 
 
+class moe_ep_norm_args(Structure):
+    _fields_ = [
+        ("x", c_void_p), ("x_stride", c_int64), ("residual", c_void_p), ("residual_stride", c_int64),
+        ("weight", c_void_p), ("out", c_void_p), ("out_stride", c_int64), ("scales", c_void_p),
+        ("scales_stride", c_int64), ("residual_out", c_void_p), ("residual_out_stride", c_int64),
+        ("dtype", c_int32), ("weight_dtype", c_int32), ("out_dtype", c_int32), ("group_size", c_int32),
+        ("num_rows", c_int32), ("hidden_size", c_int32), ("eps", c_float),
+    ]
+
+
+class moe_ep_gated_args(Structure):
+    _fields_ = [
+        ("x", c_void_p), ("x_stride", c_int64), ("gate_up", c_void_p), ("gate_up_stride", c_int64),
+        ("out", c_void_p), ("out_stride", c_int64), ("pre", c_void_p), ("dtype", c_int32), ("out_dtype", c_int32),
+        ("num_rows", c_int32), ("hidden_size", c_int32), ("intermediate_size", c_int32),
+    ]
+
+
+class moe_ep_gated_grad_args(Structure):
+    _fields_ = [
+        ("dout", c_void_p), ("dout_stride", c_int64), ("x", c_void_p), ("x_stride", c_int64),
+        ("gate_up", c_void_p), ("gate_up_stride", c_int64), ("pre", c_void_p), ("dx", c_void_p),
+        ("dx_stride", c_int64), ("dgate_up", c_void_p), ("dgate_up_stride", c_int64), ("workspace", c_void_p),
+        ("workspace_bytes", c_size_t), ("dtype", c_int32), ("dout_dtype", c_int32), ("num_rows", c_int32),
+        ("hidden_size", c_int32), ("intermediate_size", c_int32),
+    ]
+
+
+class moe_ep_adapter_args(Structure):
+    _fields_ = [
+        ("x", c_void_p), ("x_stride", c_int64), ("weight", c_void_p), ("weight_stride", c_int64),
+        ("lora_a", c_void_p), ("lora_b", c_void_p), ("adapter_ids", c_void_p), ("scales", c_void_p),
+        ("out", c_void_p), ("out_stride", c_int64), ("workspace", c_void_p), ("workspace_bytes", c_size_t),
+        ("dtype", c_int32), ("out_dtype", c_int32), ("num_rows", c_int32), ("in_features", c_int32),
+        ("out_features", c_int32), ("num_adapters", c_int32), ("rank", c_int32),
+    ]
+
+
 class MoeEpError(RuntimeError):
     """A non-zero status from the library."""
 
@@ -182,6 +224,18 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.moe_ep_layer_workspace_bytes.restype = c_int
     lib.moe_ep_layer.argtypes = [POINTER(moe_ep_layer_args), c_void_p]
     lib.moe_ep_layer.restype = c_int
+    lib.moe_ep_rms_norm.argtypes = [POINTER(moe_ep_norm_args), c_void_p]
+    lib.moe_ep_rms_norm.restype = c_int
+    lib.moe_ep_gated.argtypes = [POINTER(moe_ep_gated_args), c_void_p]
+    lib.moe_ep_gated.restype = c_int
+    lib.moe_ep_gated_grad_workspace_bytes.argtypes = [POINTER(moe_ep_gated_grad_args), POINTER(c_size_t)]
+    lib.moe_ep_gated_grad_workspace_bytes.restype = c_int
+    lib.moe_ep_gated_grad.argtypes = [POINTER(moe_ep_gated_grad_args), c_void_p]
+    lib.moe_ep_gated_grad.restype = c_int
+    lib.moe_ep_adapter_workspace_bytes.argtypes = [POINTER(moe_ep_adapter_args), POINTER(c_size_t)]
+    lib.moe_ep_adapter_workspace_bytes.restype = c_int
+    lib.moe_ep_adapter_linear.argtypes = [POINTER(moe_ep_adapter_args), c_void_p]
+    lib.moe_ep_adapter_linear.restype = c_int
     lib.moe_ep_status_string.argtypes = [c_int]
     lib.moe_ep_status_string.restype = c_char_p
     lib.moe_ep_last_error.argtypes = []
@@ -304,3 +358,39 @@ def moe_ep_layer(args: moe_ep_layer_args, stream: int) -> None:
     st = (_lib or load()).moe_ep_layer(byref(args), stream)
     if st:
         _check(st, "moe_ep_layer")
+
+
+def moe_ep_rms_norm(args: moe_ep_norm_args, stream: int) -> None:
+    st = (_lib or load()).moe_ep_rms_norm(byref(args), stream)
+    if st:
+        _check(st, "moe_ep_rms_norm")
+
+
+def moe_ep_gated(args: moe_ep_gated_args, stream: int) -> None:
+    st = (_lib or load()).moe_ep_gated(byref(args), stream)
+    if st:
+        _check(st, "moe_ep_gated")
+
+
+def moe_ep_gated_grad_workspace_bytes(args: moe_ep_gated_grad_args) -> int:
+    out = c_size_t(0)
+    _check(load().moe_ep_gated_grad_workspace_bytes(byref(args), byref(out)), "moe_ep_gated_grad_workspace_bytes")
+    return out.value
+
+
+def moe_ep_gated_grad(args: moe_ep_gated_grad_args, stream: int) -> None:
+    st = (_lib or load()).moe_ep_gated_grad(byref(args), stream)
+    if st:
+        _check(st, "moe_ep_gated_grad")
+
+
+def moe_ep_adapter_workspace_bytes(args: moe_ep_adapter_args) -> int:
+    out = c_size_t(0)
+    _check(load().moe_ep_adapter_workspace_bytes(byref(args), byref(out)), "moe_ep_adapter_workspace_bytes")
+    return out.value
+
+
+def moe_ep_adapter_linear(args: moe_ep_adapter_args, stream: int) -> None:
+    st = (_lib or load()).moe_ep_adapter_linear(byref(args), stream)
+    if st:
+        _check(st, "moe_ep_adapter_linear")

@@ -32,6 +32,11 @@ DEVICE_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall",
           f"-I{INCLUDE}", f"-I{CSRC}"]
 
+# the largest first
+DEVICE_SOURCES = ["moe_experts_kernels.hip", "moe_gated_kernels.hip", "moe_adapter_kernels.hip",
+                  "moe_route_kernels.hip", "moe_ep_kernels.hip", "moe_norm_kernels.hip"]
+HOST_SOURCES = ["moe_ep_api.cpp", "moe_ep_plan.cpp", "moe_experts_api.cpp", "moe_dense_api.cpp"]
+
 
 def _run(cmd):
     proc = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
@@ -44,27 +49,17 @@ def _run(cmd):
 def build(verbose: bool = False) -> str:
     """Compile the kernels for gfx950 and the host API, link LIB_PATH."""
     with tempfile.TemporaryDirectory(prefix="moe_ep_build_") as tmp:
-        k_obj = os.path.join(tmp, "moe_ep_kernels.o")
-        a_obj = os.path.join(tmp, "moe_ep_api.o")
-        p_obj = os.path.join(tmp, "moe_ep_plan.o")
-        xk_obj = os.path.join(tmp, "moe_experts_kernels.o")
-        xr_obj = os.path.join(tmp, "moe_route_kernels.o")
-        xa_obj = os.path.join(tmp, "moe_experts_api.o")
+        device = [HIPCC, f"--offload-arch={ARCH}", *COMMON, *DEVICE_FLAGS, "-x", "hip", "-c"]
+        host = [HIPCC, *COMMON, "-c"]
+        objs, compile_steps = [], []
+        for name in DEVICE_SOURCES + HOST_SOURCES:
+            objs.append(os.path.join(tmp, os.path.splitext(name)[0] + ".o"))
+            compile_steps.append([*(device if name in DEVICE_SOURCES else host), os.path.join(CSRC, name),
+                                  "-o", objs[-1]])
         lib_tmp = os.path.join(tmp, LIB_NAME)
-        compile_steps = [
-            [HIPCC, f"--offload-arch={ARCH}", *COMMON, *DEVICE_FLAGS, "-x", "hip", "-c",
-             os.path.join(CSRC, "moe_experts_kernels.hip"), "-o", xk_obj],
-            [HIPCC, f"--offload-arch={ARCH}", *COMMON, *DEVICE_FLAGS, "-x", "hip", "-c",
-             os.path.join(CSRC, "moe_route_kernels.hip"), "-o", xr_obj],
-            [HIPCC, f"--offload-arch={ARCH}", *COMMON, *DEVICE_FLAGS, "-x", "hip", "-c",
-             os.path.join(CSRC, "moe_ep_kernels.hip"), "-o", k_obj],
-            [HIPCC, *COMMON, "-c", os.path.join(CSRC, "moe_ep_api.cpp"), "-o", a_obj],
-            [HIPCC, *COMMON, "-c", os.path.join(CSRC, "moe_ep_plan.cpp"), "-o", p_obj],
-            [HIPCC, *COMMON, "-c", os.path.join(CSRC, "moe_experts_api.cpp"), "-o", xa_obj],
-        ]
-        link = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", k_obj, a_obj, p_obj, xk_obj, xr_obj, xa_obj,
-                "-o", lib_tmp]
-        with ThreadPoolExecutor(max_workers=len(compile_steps)) as pool:
+        link = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", lib_tmp]
+        # at most 16 compilers at once
+        with ThreadPoolExecutor(max_workers=min(16, len(compile_steps))) as pool:
             outs = list(pool.map(_run, compile_steps))
         outs.append(_run(link))
         for out in outs:

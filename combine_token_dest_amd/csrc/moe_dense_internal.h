@@ -1,0 +1,97 @@
+// Internal interface between the host code of the dense operators
+// (moe_dense_api.cpp) and their gfx950 kernels (moe_norm_kernels.hip,
+// moe_gated_kernels.hip, moe_adapter_kernels.hip).  Not
+// installed, not part of the ABI.
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+#include <stdint.h>
+
+#include "moe_ep.h"
+
+namespace moe_ep_detail {
+
+struct NormKArgs {
+  const uint16_t* x;
+  const uint16_t* residual;   // or NULL
+  const void* weight;
+  void* out;
+  float* scales;              // 8-bit rows only
+  uint16_t* residual_out;     // or NULL
+  int64_t x_stride, residual_stride, out_stride, scales_stride, residual_out_stride;
+  int32_t n;
+  int32_t hidden;
+  int32_t group;              // 8-bit rows: columns of a scale; 0: a whole row
+  float eps;
+};
+
+// One operand of a matrix product: element (row, k) is p[row * stride + k], or
+// p[k * stride + row] where the rows lie side by side.
+struct MatK {
+  const uint16_t* p;
+  int64_t stride;
+  int32_t rows;               // of a gated weight: of each half
+  // Whether tiles may be loaded in whole 16-byte units: base, stride and the
+  // side by side extent are multiples of them, and the stride is at most 2^22
+  // (offsets inside a tile have 32 bits).
+  bool whole;
+};
+
+struct GatedKArgs {
+  MatK w, x;
+  int32_t hidden;
+  int32_t inter;
+  void* out;                  // [n, inter]
+  float* pre;                 // [n, 2 * inter] gate and up, or NULL
+  int64_t out_stride;
+  int32_t out_f32;
+  int32_t ptiles, qtiles;     // (set by the launcher)
+};
+
+// out[q][p] = *factor * sum over k
+struct ProductKArgs {
+  MatK p, q;
+  int32_t k;
+  int32_t q_rows;             // rows of out (q may have more, of no account)
+  uint16_t* out;
+  int64_t out_stride;
+  const float* factor;        // or NULL: 1
+  int32_t ptiles, qtiles;     // (set by the launcher)
+};
+
+// d = [dgate, dup] of a gated product, times a power of two for float16.
+struct GatedGradKArgs {
+  const void* dout;           // [n, inter]
+  const float* pre;           // [n, 2 * inter]
+  uint16_t* d;                // [n, d_stride], columns from 2 * inter on are not written
+  int64_t dout_stride, d_stride;
+  int32_t dout_f32;
+  int32_t n, inter;
+  uint32_t* tops;             // float16: [kTops] largest magnitudes
+  float* factor;              // float16: what the products are multiplied with
+};
+constexpr int kTops = 1024;
+
+struct AdapterKArgs {
+  MatK w, x;
+  int32_t k;
+  void* out;                  // [n, out_features]
+  int64_t out_stride;
+  int32_t out_f32;
+  const float* low;           // [n, rank]: A of the row's adapter times x
+  const uint16_t* b;          // [adapters, out_features, rank]
+  const int32_t* ids;         // [n]
+  const float* scales;        // [adapters] or NULL
+  int32_t adapters, rank;
+  int32_t ptiles, qtiles;     // (set by the launcher)
+};
+
+// dtype: MOE_EP_BF16 or MOE_EP_F16.
+hipError_t launch_gated(const GatedKArgs& a, int dtype, hipStream_t stream);
+hipError_t launch_gated_grad(const GatedGradKArgs& a, int dtype, hipStream_t stream);
+// p lies with its rows side by side; q with its rows side by side, or with k (q_kc).
+hipError_t launch_product(const ProductKArgs& a, int dtype, bool q_kc, hipStream_t stream);
+hipError_t launch_adapter(const AdapterKArgs& a, int dtype, hipStream_t stream);
+hipError_t launch_rms_norm(const NormKArgs& a, int dtype, bool weight_f32, bool eight, hipStream_t stream);
+
+}  // namespace moe_ep_detail

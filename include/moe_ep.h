@@ -473,6 +473,163 @@ MOE_EP_API int moe_ep_layer_workspace_bytes(const moe_ep_layer_args* args, size_
  * weight in down may give NaN where the formula has an infinity. */
 MOE_EP_API int moe_ep_layer(const moe_ep_layer_args* args, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Dense operators: what a block computes on all of its tokens beside the
+ * routed experts.  The residual's addition and the norm that make the rows
+ * dispatch takes, in 16 bits or in 8 bits with scales (moe_ep_rms_norm); the
+ * first half of a shared expert's gated feed-forward and its gradients
+ * (moe_ep_gated, moe_ep_gated_grad); a projection that the requests of a
+ * batch share, with a low-rank adapter of each one's own
+ * (moe_ep_adapter_linear).  They need no handle; streams, devices, strides
+ * and alignment are as for the expert-side operators.  Sums are float32 or
+ * wider, and results do not depend on timing.
+ * ------------------------------------------------------------------------ */
+
+/* out_dtype of moe_ep_rms_norm for 8-bit rows: OCP e4m3 (largest value 448). */
+#define MOE_EP_E4M3 8
+
+typedef struct moe_ep_norm_args {
+  const void* x;                  /* device [num_rows, hidden_size] of dtype */
+  int64_t x_stride;               /* >= 0; 0 repeats one row */
+  const void* residual;           /* device [num_rows, hidden_size] of dtype, or NULL */
+  int64_t residual_stride;        /* >= 0; 0 repeats one row */
+  const void* weight;             /* device [hidden_size] of weight_dtype */
+  void* out;                      /* device [num_rows, hidden_size] of out_dtype */
+  int64_t out_stride;             /* >= hidden_size */
+  float* scales;                  /* device [num_rows, groups], MOE_EP_E4M3 only */
+  int64_t scales_stride;          /* >= groups */
+  void* residual_out;             /* device [num_rows, hidden_size] of dtype, with residual only */
+  int64_t residual_out_stride;    /* >= hidden_size */
+  int32_t dtype;                  /* MOE_EP_BF16 or MOE_EP_F16 */
+  int32_t weight_dtype;           /* dtype, or MOE_EP_F32 */
+  int32_t out_dtype;              /* dtype, or MOE_EP_E4M3 */
+  int32_t group_size;             /* MOE_EP_E4M3: columns of a scale, 32, 64 or 128; 0: a whole row */
+  int32_t num_rows;
+  int32_t hidden_size;            /* 8..2^22 */
+  float eps;                      /* >= 0, finite */
+} moe_ep_norm_args;
+
+/* With s = x + residual (float32; x without a residual) and m = mean(s^2)
+ * over a row:
+ *   residual_out = s, rounded to dtype
+ *   y            = s / sqrt(m + eps) * weight
+ *   out          = y, rounded to dtype; or, in 8 bits,
+ *   scales       = max|y| / 448 over a group of columns (the last may be short)
+ *   out          = y / scale, rounded to e4m3, ties to even
+ * y is made from the float32 sum, not from its rounding, and m is summed in
+ * float64, so no square overflows.  A group whose scale is 0 holds zeros.  An
+ * infinity or NaN in a row makes NaN of the row's y that it reaches by the
+ * formula, and a group with NaN has the scale NaN and NaN throughout.
+ *
+ * groups is ceil(hidden_size / group_size), or 1: with group_size 128 the
+ * rows and scales are what dispatch forwards as hidden and scale rows.  out
+ * and residual_out may each be x or residual itself (same address, stride
+ * and element size); otherwise no output may overlap an input or another
+ * output, each taken from its first element to its last.  One kernel launch. */
+MOE_EP_API int moe_ep_rms_norm(const moe_ep_norm_args* args, void* stream);
+
+typedef struct moe_ep_gated_args {
+  const void* x;                  /* device [num_rows, hidden_size] of dtype */
+  int64_t x_stride;               /* >= 0; 0 repeats one row */
+  const void* gate_up;            /* device [2 * intermediate_size, hidden_size] of dtype: gate rows, then up rows */
+  int64_t gate_up_stride;         /* >= hidden_size */
+  void* out;                      /* device [num_rows, intermediate_size] of out_dtype */
+  int64_t out_stride;             /* >= intermediate_size */
+  float* pre;                     /* device [num_rows, 2 * intermediate_size], or NULL; see below */
+  int32_t dtype;                  /* MOE_EP_BF16 or MOE_EP_F16 */
+  int32_t out_dtype;              /* dtype, or MOE_EP_F32 */
+  int32_t num_rows;
+  int32_t hidden_size;            /* 8..2^22 */
+  int32_t intermediate_size;      /* 8..2^22 */
+} moe_ep_gated_args;
+
+/* The first half of a gated feed-forward, whose weights lie as moe_ep_layer's
+ * gate_up of one expert:
+ *   g = gate_up[:I] x, u = gate_up[I:] x, out = silu(g) * u = g / (1 + exp(-g)) * u
+ * in one kernel launch; g and u stay float32 until out is rounded.  With pre
+ * they are kept for moe_ep_gated_grad as they are, g in the first I columns
+ * and u in the others.  Outputs must not overlap inputs or one another, each
+ * taken from its first element to its last. */
+MOE_EP_API int moe_ep_gated(const moe_ep_gated_args* args, void* stream);
+
+typedef struct moe_ep_gated_grad_args {
+  const void* dout;               /* device [num_rows, intermediate_size] of dout_dtype */
+  int64_t dout_stride;            /* >= 0; 0 repeats one row */
+  const void* x;                  /* as moe_ep_gated's */
+  int64_t x_stride;
+  const void* gate_up;
+  int64_t gate_up_stride;
+  const float* pre;               /* what moe_ep_gated kept */
+  void* dx;                       /* device [num_rows, hidden_size] of dtype, or NULL */
+  int64_t dx_stride;              /* >= hidden_size */
+  void* dgate_up;                 /* device [2 * intermediate_size, hidden_size] of dtype, or NULL */
+  int64_t dgate_up_stride;        /* >= hidden_size */
+  void* workspace;                /* device, moe_ep_gated_grad_workspace_bytes() bytes, 256-byte aligned */
+  size_t workspace_bytes;
+  int32_t dtype;                  /* MOE_EP_BF16 or MOE_EP_F16 */
+  int32_t dout_dtype;             /* dtype, or MOE_EP_F32 */
+  int32_t num_rows;
+  int32_t hidden_size;            /* 8..2^22 */
+  int32_t intermediate_size;      /* 8..2^22 */
+} moe_ep_gated_grad_args;
+
+/* Bytes of device workspace moe_ep_gated_grad needs for these sizes (the
+ * sizes and dtype are read; pointers are not followed): 4 for each element
+ * of dout. */
+MOE_EP_API int moe_ep_gated_grad_workspace_bytes(const moe_ep_gated_grad_args* args, size_t* out_bytes);
+
+/* The gradients of moe_ep_gated's inputs:
+ *   dg = dout * u * s * (1 + g * (1 - s)), s = 1 / (1 + exp(-g));  du = dout * g * s
+ *   dx = dg gate_up[:I] + du gate_up[I:],  dgate_up = [dg^T x; du^T x]
+ * each written whole, not added to (without rows dgate_up is zeros).  dg and
+ * du are rounded once to dtype, float16 ones after a multiplication with a
+ * power of two that brings the largest finite one to 2^14..2^15, so that none
+ * overflows.  x is read for dgate_up only and gate_up for dx only; the other
+ * may be NULL.  One kernel launch (float16: two) and one for each gradient.
+ * Outputs must not overlap inputs or one another.  The workspace holds
+ * nothing between calls; calls that may overlap in time need one each. */
+MOE_EP_API int moe_ep_gated_grad(const moe_ep_gated_grad_args* args, void* stream);
+
+typedef struct moe_ep_adapter_args {
+  const void* x;                  /* device [num_rows, in_features] of dtype */
+  int64_t x_stride;               /* >= 0; 0 repeats one row */
+  const void* weight;             /* device [out_features, in_features] of dtype */
+  int64_t weight_stride;          /* >= in_features */
+  const void* lora_a;             /* device [num_adapters, rank, in_features] of dtype */
+  const void* lora_b;             /* device [num_adapters, out_features, rank] of dtype */
+  const int32_t* adapter_ids;     /* device [num_rows] */
+  const float* scales;            /* device [num_adapters], or NULL: all 1 */
+  void* out;                      /* device [num_rows, out_features] of out_dtype */
+  int64_t out_stride;             /* >= out_features */
+  void* workspace;                /* device, moe_ep_adapter_workspace_bytes() bytes, 256-byte aligned */
+  size_t workspace_bytes;
+  int32_t dtype;                  /* MOE_EP_BF16 or MOE_EP_F16 */
+  int32_t out_dtype;              /* dtype, or MOE_EP_F32 */
+  int32_t num_rows;
+  int32_t in_features;            /* 8..2^22 */
+  int32_t out_features;           /* 1..2^22 */
+  int32_t num_adapters;           /* 1..MOE_EP_MAX_EXPERTS */
+  int32_t rank;                   /* 1..MOE_EP_MAX_RANK; smaller adapters are padded with zeros */
+} moe_ep_adapter_args;
+
+/* Largest rank of an adapter. */
+#define MOE_EP_MAX_RANK 1024
+
+/* Bytes of device workspace moe_ep_adapter_linear needs for these sizes (the
+ * sizes are read; pointers are not followed): 4 for each row and rank. */
+MOE_EP_API int moe_ep_adapter_workspace_bytes(const moe_ep_adapter_args* args, size_t* out_bytes);
+
+/* A projection that all rows share, with a low-rank adapter of each row's own:
+ *   out[r] = weight x[r] + scales[a] * lora_b[a] (lora_a[a] x[r]), a = adapter_ids[r];
+ * rows whose id is outside [0, num_adapters) have no adapter.  lora_a[a] x is
+ * kept as float32, whole, and the sum of both products is rounded once.  What
+ * is in an adapter that a row does not name does not reach the row.  out must
+ * not overlap an input, each taken from its first element to its last.  The
+ * workspace holds nothing between calls; calls that may overlap in time need
+ * one each.  Two kernel launches, and one more for each 2048 rows after the
+ * first. */
+MOE_EP_API int moe_ep_adapter_linear(const moe_ep_adapter_args* args, void* stream);
+
 /* Static text for a status code. */
 MOE_EP_API const char* moe_ep_status_string(int status);
 
