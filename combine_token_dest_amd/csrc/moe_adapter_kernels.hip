@@ -36,24 +36,24 @@ __device__ __forceinline__ void low_parts(const float* row, int k, int rank, flo
   split_floats(v, part);
 }
 
-template <class T, int TP, int TQ, int WP, int WQ, bool DIRECT>
-__global__ void __launch_bounds__(WP* WQ * 64, 2) adapter_kernel(AdapterKArgs a) {
-  typedef Gemm<T, true, true, false, TP, TQ, WP, WQ, DIRECT> G;
-  __shared__ __attribute__((aligned(1024))) char lds[2 * G::kBuffer];
+template <class G>
+__global__ void __launch_bounds__(G::kThreads, G::kThreads / 256) adapter_kernel(AdapterKArgs a) {
+  typedef typename G::T T;
+  __shared__ __attribute__((aligned(1024))) char lds[G::kLds];
   int pt, qt;
   tile_of(a.ptiles, a.qtiles, &pt, &qt);
   typename G::SideP sp;
   typename G::SideQ sq;
-  sp.aim(a.w, pt * TP);
-  sq.aim(a.x, qt * TQ);
+  sp.aim(a.w, pt * G::TP);
+  sq.aim(a.x, qt * G::TQ);
   typename G::Acc acc;
-  G::run((MOE_EP_LDS char*)lds, sp, sq, a.k, acc);
+  if (!G::run((MOE_EP_LDS char*)lds, sp, sq, a.k, acc)) return;
 
-  const int lane = threadIdx.x & 63, half = lane >> 5;
+  const int lane = threadIdx.x & 63, quarter = lane >> 4;
   const int N = a.w.rows, R = a.rank;
 #pragma unroll
   for (int j = 0; j < G::FQ; ++j) {
-    const int q = qt * TQ + G::wave_q() + j * 32 + (lane & 31);
+    const int q = qt * G::TQ + G::wave_q() + j * 16 + (lane & 15);
     const bool here = q < a.x.rows;
     int id = here ? a.ids[q] : -1;
     if (id < 0 || id >= a.adapters) id = -1;
@@ -65,56 +65,58 @@ __global__ void __launch_bounds__(WP* WQ * 64, 2) adapter_kernel(AdapterKArgs a)
       const float* low = a.low + (int64_t)(here ? q : 0) * R;
 #pragma unroll
       for (int i = 0; i < G::FP; ++i) {
-        const int p = min(pt * TP + G::wave_p() + i * 32 + (lane & 31), N - 1);
+        const int p = min(pt * G::TP + G::wave_p() + i * 16 + (lane & 15), N - 1);
         const uint16_t* b = a.b + ((int64_t)ad * N + p) * R;
-        f32x16 sum = {};
-        for (int k = 0; k < R; k += 16) {
+        f32x4 sum = {0, 0, 0, 0};
+        for (int k = 0; k < R; k += 32) {
           u32x4 part[kParts];
-          low_parts(low, k + half * 8, R, scale, part);
-          u32x4 v[2] = {b_elements(b, k + half * 8, R), {}};
+          low_parts(low, k + quarter * 8, R, scale, part);
+          u32x4 v[2] = {b_elements(b, k + quarter * 8, R), {}};
           if constexpr (std::is_same<T, F16>::value) {
             const u32x4 w = v[0];
             split_f16(w, &v[0], &v[1]);
           }
 #pragma unroll
           for (int pl = 0; pl < kParts; ++pl) {
-            sum = mfma32<BF16>(v[0], part[pl], sum);
-            if constexpr (std::is_same<T, F16>::value) sum = mfma32<BF16>(v[1], part[pl], sum);
+            sum = BF16::mfma(v[0], part[pl], sum);
+            if constexpr (std::is_same<T, F16>::value) sum = BF16::mfma(v[1], part[pl], sum);
           }
         }
 #pragma unroll
-        for (int e = 0; e < 16; ++e) acc[i][j][e] = id == ad ? acc[i][j][e] + sum[e] : acc[i][j][e];
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = id == ad ? acc[i][j][e] + sum[e] : acc[i][j][e];
       }
     }
     if (!here) continue;
 #pragma unroll
     for (int i = 0; i < G::FP; ++i) {
+      const int c = pt * G::TP + G::wave_p() + i * 16 + quarter * 4;
+      float v[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int c = pt * TP + G::wave_p() + i * 32 + r * 8 + half * 4;
-        float v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = acc[i][j][r * 4 + e];
-        store4<T>(a.out, q * a.out_stride + c, a.out_f32, N - c, v);
-      }
+      for (int e = 0; e < 4; ++e) v[e] = acc[i][j][e];
+      store4<T>(a.out, q * a.out_stride + c, a.out_f32, N - c, v);
     }
   }
 }
 
-constexpr int tiles(int64_t rows, int tile) { return (int)((rows + tile - 1) / tile); }
-
-template <class T, int TP, int TQ, int WP, int WQ, bool DIRECT>
-hipError_t adapter(AdapterKArgs a, hipStream_t stream) {
-  a.ptiles = tiles(a.w.rows, TP);
-  a.qtiles = tiles(a.x.rows, TQ);
-  adapter_kernel<T, TP, TQ, WP, WQ, DIRECT><<<dim3(a.ptiles * a.qtiles), dim3(WP * WQ * 64), 0, stream>>>(a);
+template <class G>
+hipError_t adapter_tiles(AdapterKArgs a, hipStream_t stream) {
+  a.ptiles = tiles(a.w.rows, G::TP);
+  a.qtiles = tiles(a.x.rows, G::TQ);
+  adapter_kernel<G><<<dim3(a.ptiles * a.qtiles), dim3(G::kThreads), 0, stream>>>(a);
   return hipGetLastError();
 }
 template <class T>
 hipError_t adapter(const AdapterKArgs& a, hipStream_t stream) {
-  if (!a.w.whole || !a.x.whole) return adapter<T, 128, 128, 2, 2, false>(a, stream);
-  if ((int64_t)tiles(a.w.rows, 256) * tiles(a.x.rows, 256) >= 256) return adapter<T, 256, 256, 2, 4, true>(a, stream);
-  return adapter<T, 128, 128, 2, 2, true>(a, stream);
+  const bool direct = a.w.whole && a.x.whole;
+  switch (tile_size(a.w.rows, a.x.rows, direct)) {
+    case 256: return adapter_tiles<Gemm<T, true, true, false, 256, 256, 2, 4, 1, true>>(a, stream);
+    case 128:
+      return direct ? adapter_tiles<Gemm<T, true, true, false, 128, 128, 2, 2, 2, true>>(a, stream)
+                    : adapter_tiles<Gemm<T, true, true, false, 128, 128, 2, 2, 2, false>>(a, stream);
+    default:
+      return direct ? adapter_tiles<Gemm<T, true, true, false, 64, 64, 2, 2, 4, true>>(a, stream)
+                    : adapter_tiles<Gemm<T, true, true, false, 64, 64, 2, 2, 4, false>>(a, stream);
+  }
 }
 
 }  // namespace

@@ -29,74 +29,67 @@ namespace {
 
 __device__ __forceinline__ float sigmoid(float v) { return 1.0f / (1.0f + __expf(-v)); }
 
-template <class T, int TP, int TQ, int WP, int WQ, bool DIRECT>
-__global__ void __launch_bounds__(WP* WQ * 64, 2) gated_kernel(GatedKArgs a) {
-  typedef Gemm<T, true, true, true, TP, TQ, WP, WQ, DIRECT> G;
-  __shared__ __attribute__((aligned(1024))) char lds[2 * G::kBuffer];
+template <class G>
+__global__ void __launch_bounds__(G::kThreads, G::kThreads / 256) gated_kernel(GatedKArgs a) {
+  typedef typename G::T T;
+  __shared__ __attribute__((aligned(1024))) char lds[G::kLds];
   int pt, qt;
   tile_of(a.ptiles, a.qtiles, &pt, &qt);
   typename G::SideP sp;
   typename G::SideQ sq;
-  sp.aim(a.w, pt * (TP / 2));
-  sq.aim(a.x, qt * TQ);
+  sp.aim(a.w, pt * (G::TP / 2));
+  sq.aim(a.x, qt * G::TQ);
   typename G::Acc acc;
-  G::run((MOE_EP_LDS char*)lds, sp, sq, a.hidden, acc);
+  if (!G::run((MOE_EP_LDS char*)lds, sp, sq, a.hidden, acc)) return;
   const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int j = 0; j < G::FQ; ++j) {
-    const int q = qt * TQ + G::wave_q() + j * 32 + (lane & 31);
+    const int q = qt * G::TQ + G::wave_q() + j * 16 + (lane & 15);
     if (q >= a.x.rows) continue;
 #pragma unroll
     for (int i = 0; i < G::FP; i += 2) {
+      const int c = pt * (G::TP / 2) + (G::wave_p() + i * 16) / 2 + (lane >> 4) * 4;
+      float g[4], u[4], h[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int c = pt * (TP / 2) + (G::wave_p() + i * 32) / 2 + r * 8 + (lane >> 5) * 4;
-        const int have = a.inter - c;
-        float g[4], u[4], h[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          g[e] = acc[i][j][r * 4 + e];
-          u[e] = acc[i + 1][j][r * 4 + e];
-          h[e] = g[e] * sigmoid(g[e]) * u[e];
-        }
-        store4<T>(a.out, q * a.out_stride + c, a.out_f32, have, h);
-        if (a.pre) {
-          store4<T>(a.pre, (int64_t)q * 2 * a.inter + c, true, have, g);
-          store4<T>(a.pre, ((int64_t)q * 2 + 1) * a.inter + c, true, have, u);
-        }
+      for (int e = 0; e < 4; ++e) {
+        g[e] = acc[i][j][e];
+        u[e] = acc[i + 1][j][e];
+        h[e] = g[e] * sigmoid(g[e]) * u[e];
+      }
+      store4<T>(a.out, q * a.out_stride + c, a.out_f32, a.inter - c, h);
+      if (a.pre) {
+        store4<T>(a.pre, (int64_t)q * 2 * a.inter + c, true, a.inter - c, g);
+        store4<T>(a.pre, ((int64_t)q * 2 + 1) * a.inter + c, true, a.inter - c, u);
       }
     }
   }
 }
 
-template <class T, bool QKC, int TP, int TQ, int WP, int WQ, bool DIRECT>
-__global__ void __launch_bounds__(WP* WQ * 64, 2) product_kernel(ProductKArgs a) {
-  typedef Gemm<T, false, QKC, false, TP, TQ, WP, WQ, DIRECT> G;
-  __shared__ __attribute__((aligned(1024))) char lds[2 * G::kBuffer];
+template <class G>
+__global__ void __launch_bounds__(G::kThreads, G::kThreads / 256) product_kernel(ProductKArgs a) {
+  typedef typename G::T T;
+  __shared__ __attribute__((aligned(1024))) char lds[G::kLds];
   int pt, qt;
   tile_of(a.ptiles, a.qtiles, &pt, &qt);
   typename G::SideP sp;
   typename G::SideQ sq;
-  sp.aim(a.p, pt * TP);
-  sq.aim(a.q, qt * TQ);
+  sp.aim(a.p, pt * G::TP);
+  sq.aim(a.q, qt * G::TQ);
   typename G::Acc acc;
-  G::run((MOE_EP_LDS char*)lds, sp, sq, a.k, acc);
+  if (!G::run((MOE_EP_LDS char*)lds, sp, sq, a.k, acc)) return;
   const float factor = a.factor ? *a.factor : 1.0f;
   const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int j = 0; j < G::FQ; ++j) {
-    const int q = qt * TQ + G::wave_q() + j * 32 + (lane & 31);
+    const int q = qt * G::TQ + G::wave_q() + j * 16 + (lane & 15);
     if (q >= a.q_rows) continue;
 #pragma unroll
     for (int i = 0; i < G::FP; ++i) {
+      const int c = pt * G::TP + G::wave_p() + i * 16 + (lane >> 4) * 4;
+      float v[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int c = pt * TP + G::wave_p() + i * 32 + r * 8 + (lane >> 5) * 4;
-        float v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = acc[i][j][r * 4 + e] * factor;
-        store4<T>(a.out, q * a.out_stride + c, false, a.p.rows - c, v);
-      }
+      for (int e = 0; e < 4; ++e) v[e] = acc[i][j][e] * factor;
+      store4<T>(a.out, q * a.out_stride + c, false, a.p.rows - c, v);
     }
   }
 }
@@ -232,35 +225,46 @@ __global__ void __launch_bounds__(256) gated_grad_kernel(GatedGradKArgs a, int t
   }
 }
 
-constexpr int tiles(int64_t rows, int tile) { return (int)((rows + tile - 1) / tile); }
-
-template <class T, int TP, int TQ, int WP, int WQ, bool DIRECT>
-hipError_t gated(GatedKArgs a, hipStream_t stream) {
-  a.ptiles = tiles(a.inter, TP / 2);
-  a.qtiles = tiles(a.x.rows, TQ);
-  gated_kernel<T, TP, TQ, WP, WQ, DIRECT><<<dim3(a.ptiles * a.qtiles), dim3(WP * WQ * 64), 0, stream>>>(a);
+template <class G>
+hipError_t gated_tiles(GatedKArgs a, hipStream_t stream) {
+  a.ptiles = tiles(a.inter, G::TP / 2);
+  a.qtiles = tiles(a.x.rows, G::TQ);
+  gated_kernel<G><<<dim3(a.ptiles * a.qtiles), dim3(G::kThreads), 0, stream>>>(a);
   return hipGetLastError();
 }
 template <class T>
 hipError_t gated(const GatedKArgs& a, hipStream_t stream) {
-  if (!a.w.whole || !a.x.whole) return gated<T, 128, 128, 2, 2, false>(a, stream);
-  if ((int64_t)tiles(a.inter, 128) * tiles(a.x.rows, 256) >= 256) return gated<T, 256, 256, 2, 4, true>(a, stream);
-  return gated<T, 128, 128, 2, 2, true>(a, stream);
+  const bool direct = a.w.whole && a.x.whole;
+  switch (tile_size(2 * (int64_t)a.inter, a.x.rows, direct)) {
+    case 256: return gated_tiles<Gemm<T, true, true, true, 256, 256, 2, 4, 1, true>>(a, stream);
+    case 128:
+      return direct ? gated_tiles<Gemm<T, true, true, true, 128, 128, 2, 2, 2, true>>(a, stream)
+                    : gated_tiles<Gemm<T, true, true, true, 128, 128, 2, 2, 2, false>>(a, stream);
+    default:
+      return direct ? gated_tiles<Gemm<T, true, true, true, 64, 64, 2, 2, 4, true>>(a, stream)
+                    : gated_tiles<Gemm<T, true, true, true, 64, 64, 2, 2, 4, false>>(a, stream);
+  }
 }
 
-template <class T, bool QKC, int TP, int TQ, int WP, int WQ, bool DIRECT>
-hipError_t product(ProductKArgs a, hipStream_t stream) {
-  a.ptiles = tiles(a.p.rows, TP);
-  a.qtiles = tiles(a.q_rows, TQ);
-  product_kernel<T, QKC, TP, TQ, WP, WQ, DIRECT><<<dim3(a.ptiles * a.qtiles), dim3(WP * WQ * 64), 0, stream>>>(a);
+template <class G>
+hipError_t product_tiles(ProductKArgs a, hipStream_t stream) {
+  a.ptiles = tiles(a.p.rows, G::TP);
+  a.qtiles = tiles(a.q_rows, G::TQ);
+  product_kernel<G><<<dim3(a.ptiles * a.qtiles), dim3(G::kThreads), 0, stream>>>(a);
   return hipGetLastError();
 }
 template <class T, bool QKC>
 hipError_t product(const ProductKArgs& a, hipStream_t stream) {
-  if (!a.p.whole || !a.q.whole) return product<T, QKC, 128, 128, 2, 2, false>(a, stream);
-  if ((int64_t)tiles(a.p.rows, 256) * tiles(a.q_rows, 256) >= 256)
-    return product<T, QKC, 256, 256, 2, 4, true>(a, stream);
-  return product<T, QKC, 128, 128, 2, 2, true>(a, stream);
+  const bool direct = a.p.whole && a.q.whole;
+  switch (tile_size(a.p.rows, a.q_rows, direct)) {
+    case 256: return product_tiles<Gemm<T, false, QKC, false, 256, 256, 2, 4, 1, true>>(a, stream);
+    case 128:
+      return direct ? product_tiles<Gemm<T, false, QKC, false, 128, 128, 2, 2, 2, true>>(a, stream)
+                    : product_tiles<Gemm<T, false, QKC, false, 128, 128, 2, 2, 2, false>>(a, stream);
+    default:
+      return direct ? product_tiles<Gemm<T, false, QKC, false, 64, 64, 2, 2, 4, true>>(a, stream)
+                    : product_tiles<Gemm<T, false, QKC, false, 64, 64, 2, 2, 4, false>>(a, stream);
+  }
 }
 
 template <class T>
