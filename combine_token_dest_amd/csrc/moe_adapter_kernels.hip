@@ -1,18 +1,28 @@
-// gfx950 kernel of a shared projection with low-rank adapters:
-//   y[r] = W x[r] + s_a B_a (A_a x[r]), a = ids[r],
-// where low[r] = A_a x[r] (float32) has been made by expert_linear's kernels.
+// gfx950 kernels of a shared projection with low-rank adapters:
+//   y[r] = W x[r] + s_a B_a (A_a x[r]), a = ids[r].
+//
+// low_kernel makes the scaled low-rank values s_a A_a x: 1 or 16 rows of x to
+// a workgroup, and the rows of A of each adapter that they name, one adapter
+// after another.  Up to kLowFew rows share k between workgroups, whose float32
+// sums the second kernel adds in turn.
 //
 // The shared product is that of moe_gemm_device.h.  Behind it, while the sums
 // are still in registers, a wave goes through the adapters that its rows name,
 // one after another: B_a's rows times the low-rank values by matrix
 // instructions, added to the rows that have this adapter and to no others (a
 // row's result never meets another adapter's B, whatever is in it).  The low
-// values go in as three bfloat16 each, float32's 24 bits.
+// values go in as three bfloat16 each, float32's 24 bits.  Few rows take the
+// kernel that streams the weights (moe_few_device.h), where each result adds
+// its own adapter's sum over the rank in float32, made while the first weights
+// are on their way.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "moe_dense_internal.h"
+#include "moe_few_device.h"
 #include "moe_gemm_device.h"
 
 namespace moe_ep_detail {
@@ -28,12 +38,137 @@ __device__ __forceinline__ u32x4 b_elements(const uint16_t* row, int k, int rank
   return v;
 }
 
-// Eight low values times the scale, in parts.
-__device__ __forceinline__ void low_parts(const float* row, int k, int rank, float scale, u32x4 (&part)[kParts]) {
-  u32x4 v[2];
+constexpr int kLowWaves = 8;
+// Calls of up to this many rows, which may be one request's each, take them
+// one by one; more are prompts, whose rows share adapters.
+constexpr int kLowSingle = 512;
+
+// The low values of BLOCK rows of x and 16 RT of the rank.
+template <class T, int BLOCK, int RT, bool FEW>
+__global__ void __launch_bounds__(kLowWaves * 64) low_kernel(AdapterKArgs a) {
+  __shared__ f32x4 sums[kLowWaves][RT][16][4];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, i = lane & 15;
+  const int r0 = blockIdx.x * BLOCK, k0 = blockIdx.y * (16 * RT), split = blockIdx.z;
+  const int R = a.rank, n = a.x.rows;
+  const int row = min(r0 + min(i, BLOCK - 1), n - 1);
+  // lanes of the same row name the same adapter; rows past the last none
+  int id = r0 + min(i, BLOCK - 1) < n ? a.ids[row] : -1;
+  if (id < 0 || id >= a.adapters) id = -1;
+  const uint16_t* rb[1] = {a.x.p + (int64_t)row * a.x.stride};
+  // this part's steps of 64 k
+  constexpr int splits = FEW ? kLowSplits : 1;
+  const int steps = a.k / 64, left = a.k % 64;
+  const int first = (int)((int64_t)steps * split / splits), last = (int)((int64_t)steps * (split + 1) / splits);
+  uint64_t pending = __ballot(id >= 0);
+  while (pending) {
+    const int ad = __builtin_amdgcn_readlane(id, __builtin_ctzll(pending));
+    pending &= ~__ballot(id == ad);
+    const uint16_t* ra[RT];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) v[e >> 2][e & 3] = k + e < rank ? __float_as_uint(row[k + e] * scale) : 0u;
-  split_floats(v, part);
+    for (int m = 0; m < RT; ++m) ra[m] = a.a + ((int64_t)ad * R + min(k0 + m * 16 + i, R - 1)) * a.k;
+    Few<T, RT, 1, kLowWaves> few;
+    few.aim(ra, rb, first, last - first, blockIdx.x);
+    few.prime(wave, kLowWaves);
+    f32x4 acc[RT][1] = {};
+    few.run(wave, kLowWaves, acc);
+    if (left && split == splits - 1 && wave == kLowWaves - 1) few.tail(left, acc);
+#pragma unroll
+    for (int m = 0; m < RT; ++m) sums[wave][m][i][lane >> 4] = acc[m][0];
+    __syncthreads();
+    const float* sum = reinterpret_cast<const float*>(sums);
+    const float scale = a.scales ? a.scales[ad] : 1.0f;
+    // a rank up to 16 is followed by zeros up to 32 where the stride has them
+    constexpr int kWide = RT == 1 && !FEW ? 32 : 16 * RT;
+    for (int o = threadIdx.x; o < BLOCK * kWide; o += kLowWaves * 64) {
+      const int r = o / kWide, c = o % kWide, k = k0 + c;
+      float v = 0;
+      if (c < 16 * RT) {
+#pragma unroll
+        for (int w = 0; w < kLowWaves; ++w) v += sum[((w * RT + c / 16) * 16 + r) * 16 + c % 16];
+      }
+      v = k < R ? v * scale : 0.0f;
+      if (__shfl(id, r) != ad || k >= a.low_stride) continue;
+      const int64_t at = (int64_t)(r0 + r) * a.low_stride + k, plane = (int64_t)n * a.low_stride;
+      if constexpr (FEW) {
+        static_cast<float*>(a.low)[split * plane + at] = v;
+      } else {
+        uint16_t part[kParts];
+        split_parts(v, part);
+#pragma unroll
+        for (int pl = 0; pl < kParts; ++pl) static_cast<uint16_t*>(a.low)[pl * plane + at] = part[pl];
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// Up to 16 NT rows: 16 columns of the result to a workgroup.
+template <class T, int NT, int WAVES>
+__global__ void __launch_bounds__(WAVES * 64) adapter_few_kernel(AdapterKArgs a) {
+  __shared__ f32x4 sums[WAVES][NT][16][4];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, i = lane & 15;
+  const int c0 = blockIdx.x * 16, N = a.w.rows, R = a.rank;
+  const uint16_t* ra[1] = {a.w.p + (int64_t)min(c0 + i, N - 1) * a.w.stride};
+  const uint16_t* rb[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) rb[t] = a.x.p + (int64_t)min(t * 16 + i, a.x.rows - 1) * a.x.stride;
+  Few<T, 1, NT, WAVES> few;
+  const int steps = a.k / 64, left = a.k % 64;
+  few.aim(ra, rb, 0, steps, blockIdx.x);
+  few.prime(wave, WAVES);
+  // The adapters' sums of this thread's results, while the first weights are on their way.
+  constexpr int kMine = (NT * 256 + WAVES * 64 - 1) / (WAVES * 64);
+  constexpr int kUnroll = WAVES > 8 ? 1 : 2;
+  float own[kMine];
+#pragma unroll
+  for (int m = 0; m < kMine; ++m) {
+    const int o = m * WAVES * 64 + threadIdx.x, r = o >> 4, c = c0 + (o & 15);
+    own[m] = 0;
+    if (r < a.x.rows && c < N) {
+      const int id = a.ids[r];
+      if (id >= 0 && id < a.adapters) {
+        const uint16_t* b = a.b + ((int64_t)id * N + c) * R;
+        const float* low = static_cast<const float*>(a.low) + (int64_t)r * a.low_stride;
+        const int64_t plane = (int64_t)a.x.rows * a.low_stride;
+#pragma unroll kUnroll
+        for (int k = 0; k < R; k += 8) {
+          const u32x4 w = b_elements(b, k, R);
+          f32x4 v[kLowSplits][2];
+#pragma unroll
+          for (int s = 0; s < kLowSplits; ++s)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) v[s][h] = *reinterpret_cast<const f32x4*>(low + s * plane + k + h * 4);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            float l = 0;
+#pragma unroll
+            for (int s = 0; s < kLowSplits; ++s) l += v[s][e >> 2][e & 3];
+            // (what is past the rank is 0 in both)
+            own[m] += l * T::to_float((uint16_t)(w[e >> 1] >> (e & 1) * 16));
+          }
+        }
+      }
+    }
+  }
+  f32x4 acc[1][NT] = {};
+  few.run(wave, WAVES, acc);
+  if (left && steps % WAVES == wave) few.tail(left, acc);
+#pragma unroll
+  for (int t = 0; t < NT; ++t) sums[wave][t][i][lane >> 4] = acc[0][t];
+  __syncthreads();
+  const float* sum = reinterpret_cast<const float*>(sums);
+#pragma unroll
+  for (int m = 0; m < kMine; ++m) {
+    const int o = m * WAVES * 64 + threadIdx.x, r = o >> 4, c = c0 + (o & 15);
+    if (r >= a.x.rows || c >= N) continue;
+    float v = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) v += sum[(w * NT * 16 + r) * 16 + (o & 15)];
+    v += own[m];
+    const int64_t at = r * a.out_stride + c;
+    if (a.out_f32) static_cast<float*>(a.out)[at] = v;
+    else static_cast<uint16_t*>(a.out)[at] = T::from_float(v);
+  }
 }
 
 template <class G>
@@ -61,29 +196,31 @@ __global__ void __launch_bounds__(G::kThreads, G::kThreads / 256) adapter_kernel
     while (pending) {
       const int ad = __builtin_amdgcn_readlane(id, __builtin_ctzll(pending));
       pending &= ~__ballot(id == ad);
-      const float scale = a.scales ? a.scales[ad] : 1.0f;
-      const float* low = a.low + (int64_t)(here ? q : 0) * R;
+      const uint16_t* low = static_cast<const uint16_t*>(a.low) + (int64_t)(here ? q : 0) * a.low_stride + quarter * 8;
+      const int64_t plane = (int64_t)a.x.rows * a.low_stride;
+      for (int k = 0; k < R; k += 32) {
+        u32x4 part[kParts];
 #pragma unroll
-      for (int i = 0; i < G::FP; ++i) {
-        const int p = min(pt * G::TP + G::wave_p() + i * 16 + (lane & 15), N - 1);
-        const uint16_t* b = a.b + ((int64_t)ad * N + p) * R;
-        f32x4 sum = {0, 0, 0, 0};
-        for (int k = 0; k < R; k += 32) {
-          u32x4 part[kParts];
-          low_parts(low, k + quarter * 8, R, scale, part);
-          u32x4 v[2] = {b_elements(b, k + quarter * 8, R), {}};
-          if constexpr (std::is_same<T, F16>::value) {
-            const u32x4 w = v[0];
-            split_f16(w, &v[0], &v[1]);
-          }
+        for (int pl = 0; pl < kParts; ++pl) part[pl] = *reinterpret_cast<const u32x4*>(low + pl * plane + k);
+        u32x4 b[G::FP];
+#pragma unroll
+        for (int i = 0; i < G::FP; ++i) {
+          const int p = min(pt * G::TP + G::wave_p() + i * 16 + (lane & 15), N - 1);
+          b[i] = b_elements(a.b + ((int64_t)ad * N + p) * R, k + quarter * 8, R);
+        }
+#pragma unroll
+        for (int i = 0; i < G::FP; ++i) {
+          f32x4 sum = {0, 0, 0, 0};
+          u32x4 v[2] = {b[i], {}};
+          if constexpr (std::is_same<T, F16>::value) split_f16(b[i], &v[0], &v[1]);
 #pragma unroll
           for (int pl = 0; pl < kParts; ++pl) {
             sum = BF16::mfma(v[0], part[pl], sum);
             if constexpr (std::is_same<T, F16>::value) sum = BF16::mfma(v[1], part[pl], sum);
           }
-        }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = id == ad ? acc[i][j][e] + sum[e] : acc[i][j][e];
+          for (int e = 0; e < 4; ++e) acc[i][j][e] = id == ad ? acc[i][j][e] + sum[e] : acc[i][j][e];
+        }
       }
     }
     if (!here) continue;
@@ -105,12 +242,37 @@ hipError_t adapter_tiles(AdapterKArgs a, hipStream_t stream) {
   adapter_kernel<G><<<dim3(a.ptiles * a.qtiles), dim3(G::kThreads), 0, stream>>>(a);
   return hipGetLastError();
 }
+template <class T, int NT>
+hipError_t adapter_few(const AdapterKArgs& a, hipStream_t stream) {
+  const int blocks = tiles(a.w.rows, 16);
+  if (NT > 2 || blocks >= 256) adapter_few_kernel<T, NT, 8><<<dim3(blocks), dim3(512), 0, stream>>>(a);
+  else adapter_few_kernel<T, NT < 4 ? NT : 2, 16><<<dim3(blocks), dim3(1024), 0, stream>>>(a);
+  return hipGetLastError();
+}
+template <class T, int BLOCK, bool FEW>
+hipError_t low(const AdapterKArgs& a, hipStream_t stream) {
+  const dim3 grid(tiles(a.x.rows, BLOCK), a.rank <= 16 ? 1 : tiles(a.rank, 64), FEW ? kLowSplits : 1);
+  const dim3 block(kLowWaves * 64);
+  if (a.rank <= 16) low_kernel<T, BLOCK, 1, FEW><<<grid, block, 0, stream>>>(a);
+  else low_kernel<T, BLOCK, 4, FEW><<<grid, block, 0, stream>>>(a);
+  return hipGetLastError();
+}
 template <class T>
 hipError_t adapter(const AdapterKArgs& a, hipStream_t stream) {
+  static_assert(kLowFew == 64, "the few kernels' rows");
+  const int n = a.x.rows;
+  const hipError_t e = n <= kLowFew      ? low<T, 1, true>(a, stream)
+                       : n <= kLowSingle ? low<T, 1, false>(a, stream)
+                                         : low<T, 16, false>(a, stream);
+  if (e != hipSuccess) return e;
+  if (n <= 16) return adapter_few<T, 1>(a, stream);
+  if (n <= 32) return adapter_few<T, 2>(a, stream);
+  if (n <= 64) return adapter_few<T, 4>(a, stream);
   const bool direct = a.w.whole && a.x.whole;
   switch (tile_size(a.w.rows, a.x.rows, direct)) {
-    case 256: return adapter_tiles<Gemm<T, true, true, false, 256, 256, 2, 4, 1, true>>(a, stream);
-    case 128:
+    case k256x256: return adapter_tiles<Gemm<T, true, true, false, 256, 256, 2, 4, 1, true>>(a, stream);
+    case k256x128: return adapter_tiles<Gemm<T, true, true, false, 256, 128, 2, 4, 1, true>>(a, stream);
+    case k128x128:
       return direct ? adapter_tiles<Gemm<T, true, true, false, 128, 128, 2, 2, 2, true>>(a, stream)
                     : adapter_tiles<Gemm<T, true, true, false, 128, 128, 2, 2, 2, false>>(a, stream);
     default:

@@ -111,7 +111,7 @@ int check_adapter_sizes(const moe_ep_adapter_args* a) {
 }
 
 size_t adapter_workspace(const moe_ep_adapter_args* a) {
-  return std::max<size_t>((size_t)up((int64_t)a->num_rows * a->rank * 4, 256), 256);
+  return std::max<size_t>((size_t)up(LowSpace(a->num_rows, a->rank).bytes, 256), 256);
 }
 
 }  // namespace
@@ -353,22 +353,6 @@ int moe_ep_adapter_linear(const moe_ep_adapter_args* a, void* stream) {
   if (st == MOE_EP_OK) st = check_stream(stream);
   if (st != MOE_EP_OK) return st;
 
-  moe_ep_linear_args low = {};
-  low.x = a->x;
-  low.x_stride = a->x_stride;
-  low.expert_ids = a->adapter_ids;
-  low.out = a->workspace;
-  low.out_stride = R;
-  low.weight.data = a->lora_a;
-  low.dtype = a->dtype;
-  low.out_dtype = MOE_EP_F32;
-  low.num_rows = n;
-  low.num_experts = a->num_adapters;
-  low.in_features = K;
-  low.out_features = a->rank;
-  st = moe_ep_expert_linear(&low, stream);
-  if (st != MOE_EP_OK) return st;
-
   AdapterKArgs k = {};
   k.w = operand(a->weight, a->weight_stride, N, K);
   k.x = operand(a->x, a->x_stride, n, K);
@@ -376,7 +360,9 @@ int moe_ep_adapter_linear(const moe_ep_adapter_args* a, void* stream) {
   k.out = a->out;
   k.out_stride = a->out_stride;
   k.out_f32 = a->out_dtype == MOE_EP_F32;
-  k.low = static_cast<const float*>(a->workspace);
+  k.a = static_cast<const uint16_t*>(a->lora_a);
+  k.low = a->workspace;
+  k.low_stride = LowSpace(n, a->rank).stride;
   k.b = static_cast<const uint16_t*>(a->lora_b);
   k.ids = a->adapter_ids;
   k.scales = a->scales;

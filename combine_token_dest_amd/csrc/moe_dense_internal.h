@@ -78,7 +78,9 @@ struct AdapterKArgs {
   void* out;                  // [n, out_features]
   int64_t out_stride;
   int32_t out_f32;
-  const float* low;           // [n, rank]: A of the row's adapter times x
+  const uint16_t* a;          // [adapters, rank, in_features]
+  void* low;                  // scale * A x of each row with its adapter: LowSpace
+  int32_t low_stride;
   const uint16_t* b;          // [adapters, out_features, rank]
   const int32_t* ids;         // [n]
   const float* scales;        // [adapters] or NULL
@@ -91,6 +93,19 @@ hipError_t launch_gated(const GatedKArgs& a, int dtype, hipStream_t stream);
 hipError_t launch_gated_grad(const GatedGradKArgs& a, int dtype, hipStream_t stream);
 // p lies with its rows side by side; q with its rows side by side, or with k (q_kc).
 hipError_t launch_product(const ProductKArgs& a, int dtype, bool q_kc, hipStream_t stream);
+// The low-rank values between the two kernels, zeros from the rank to the
+// stride.  Few rows: float32 [kLowSplits, rows, stride], sums over parts of k.
+// Else their bfloat16 parts [kParts, rows, stride].
+constexpr int kLowFew = 64, kLowSplits = 4;
+struct LowSpace {
+  int32_t stride;
+  int64_t bytes;
+  LowSpace(int64_t rows, int32_t rank) {
+    const bool few = rows <= kLowFew;
+    stride = few ? (rank + 7) / 8 * 8 : (rank + 31) / 32 * 32;
+    bytes = rows * stride * (few ? 4 * kLowSplits : 2 * 3);
+  }
+};
 hipError_t launch_adapter(const AdapterKArgs& a, int dtype, hipStream_t stream);
 hipError_t launch_rms_norm(const NormKArgs& a, int dtype, bool weight_f32, bool eight, hipStream_t stream);
 

@@ -22,6 +22,7 @@
 #include <algorithm>
 
 #include "moe_dense_internal.h"
+#include "moe_few_device.h"
 #include "moe_gemm_device.h"
 
 namespace moe_ep_detail {
@@ -61,6 +62,48 @@ __global__ void __launch_bounds__(G::kThreads, G::kThreads / 256) gated_kernel(G
         store4<T>(a.pre, (int64_t)q * 2 * a.inter + c, true, a.inter - c, g);
         store4<T>(a.pre, ((int64_t)q * 2 + 1) * a.inter + c, true, a.inter - c, u);
       }
+    }
+  }
+}
+
+// The same for up to 16 NT rows (moe_few_device.h): eight gate rows and the
+// same eight up rows to a workgroup.
+template <class T, int NT, int WAVES>
+__global__ void __launch_bounds__(WAVES * 64) gated_few_kernel(GatedKArgs a) {
+  __shared__ f32x4 sums[WAVES][NT][16][4];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, i = lane & 15;
+  const int c0 = blockIdx.x * 8;
+  const uint16_t* ra[1] = {a.w.p + ((int64_t)min(c0 + (i & 7), a.inter - 1) + (i & 8 ? a.inter : 0)) * a.w.stride};
+  const uint16_t* rb[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) rb[t] = a.x.p + (int64_t)min(t * 16 + i, a.x.rows - 1) * a.x.stride;
+  Few<T, 1, NT, WAVES> few;
+  const int steps = a.hidden / 64, left = a.hidden % 64;
+  few.aim(ra, rb, 0, steps, blockIdx.x);
+  few.prime(wave, WAVES);
+  f32x4 acc[1][NT] = {};
+  few.run(wave, WAVES, acc);
+  if (left && steps % WAVES == wave) few.tail(left, acc);
+#pragma unroll
+  for (int t = 0; t < NT; ++t) sums[wave][t][i][lane >> 4] = acc[0][t];
+  __syncthreads();
+  const float* sum = reinterpret_cast<const float*>(sums);
+  for (int o = threadIdx.x; o < a.x.rows * 8; o += WAVES * 64) {
+    const int r = o >> 3, c = o & 7;
+    if (c0 + c >= a.inter) continue;
+    float g = 0, u = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+      g += sum[(w * NT * 16 + r) * 16 + c];
+      u += sum[(w * NT * 16 + r) * 16 + 8 + c];
+    }
+    const float h = g * sigmoid(g) * u;
+    const int64_t at = r * a.out_stride + c0 + c;
+    if (a.out_f32) static_cast<float*>(a.out)[at] = h;
+    else static_cast<uint16_t*>(a.out)[at] = T::from_float(h);
+    if (a.pre) {
+      a.pre[(int64_t)r * 2 * a.inter + c0 + c] = g;
+      a.pre[((int64_t)r * 2 + 1) * a.inter + c0 + c] = u;
     }
   }
 }
@@ -232,12 +275,22 @@ hipError_t gated_tiles(GatedKArgs a, hipStream_t stream) {
   gated_kernel<G><<<dim3(a.ptiles * a.qtiles), dim3(G::kThreads), 0, stream>>>(a);
   return hipGetLastError();
 }
+template <class T, int NT>
+hipError_t gated_few(const GatedKArgs& a, hipStream_t stream) {
+  const int blocks = tiles(a.inter, 8);
+  if (blocks >= 256) gated_few_kernel<T, NT, 8><<<dim3(blocks), dim3(512), 0, stream>>>(a);
+  else gated_few_kernel<T, NT, 16><<<dim3(blocks), dim3(1024), 0, stream>>>(a);
+  return hipGetLastError();
+}
 template <class T>
 hipError_t gated(const GatedKArgs& a, hipStream_t stream) {
+  if (a.x.rows <= 16) return gated_few<T, 1>(a, stream);
+  if (a.x.rows <= 32) return gated_few<T, 2>(a, stream);
   const bool direct = a.w.whole && a.x.whole;
   switch (tile_size(2 * (int64_t)a.inter, a.x.rows, direct)) {
-    case 256: return gated_tiles<Gemm<T, true, true, true, 256, 256, 2, 4, 1, true>>(a, stream);
-    case 128:
+    case k256x256: return gated_tiles<Gemm<T, true, true, true, 256, 256, 2, 4, 1, true>>(a, stream);
+    case k256x128: return gated_tiles<Gemm<T, true, true, true, 256, 128, 2, 4, 1, true>>(a, stream);
+    case k128x128:
       return direct ? gated_tiles<Gemm<T, true, true, true, 128, 128, 2, 2, 2, true>>(a, stream)
                     : gated_tiles<Gemm<T, true, true, true, 128, 128, 2, 2, 2, false>>(a, stream);
     default:
@@ -257,8 +310,9 @@ template <class T, bool QKC>
 hipError_t product(const ProductKArgs& a, hipStream_t stream) {
   const bool direct = a.p.whole && a.q.whole;
   switch (tile_size(a.p.rows, a.q_rows, direct)) {
-    case 256: return product_tiles<Gemm<T, false, QKC, false, 256, 256, 2, 4, 1, true>>(a, stream);
-    case 128:
+    case k256x256: return product_tiles<Gemm<T, false, QKC, false, 256, 256, 2, 4, 1, true>>(a, stream);
+    case k256x128: return product_tiles<Gemm<T, false, QKC, false, 256, 128, 2, 4, 1, true>>(a, stream);
+    case k128x128:
       return direct ? product_tiles<Gemm<T, false, QKC, false, 128, 128, 2, 2, 2, true>>(a, stream)
                     : product_tiles<Gemm<T, false, QKC, false, 128, 128, 2, 2, 2, false>>(a, stream);
     default:

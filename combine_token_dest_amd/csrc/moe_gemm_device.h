@@ -395,11 +395,13 @@ __device__ __forceinline__ void store4(void* out, int64_t at, bool f32, int have
 
 constexpr int tiles(int64_t rows, int tile) { return (int)((rows + tile - 1) / tile); }
 
-// The side of the tiles for P x Q results: the largest of which there are
-// enough for the card's CUs.
-inline int tile_size(int64_t P, int64_t Q, bool direct) {
-  if (direct && (int64_t)tiles(P, 256) * tiles(Q, 256) >= 192) return 256;
-  return (int64_t)tiles(P, 128) * tiles(Q, 128) >= 160 ? 128 : 64;
+// The tiles for P x Q results: the largest of which there are enough for the
+// card's 256 CUs.
+enum TileSize { k256x256, k256x128, k128x128, k64x64 };
+inline TileSize tile_size(int64_t P, int64_t Q, bool direct) {
+  if (direct && (int64_t)tiles(P, 256) * tiles(Q, 256) >= 192) return k256x256;
+  if (direct && (int64_t)tiles(P, 256) * tiles(Q, 128) >= 192) return k256x128;
+  return (int64_t)tiles(P, 128) * tiles(Q, 128) >= 160 ? k128x128 : k64x64;
 }
 
 }  // namespace

@@ -252,5 +252,5 @@ def adapter_linear(x: torch.Tensor, weight: torch.Tensor, lora_a: torch.Tensor, 
 
 def adapter_linear_workspace_bytes(rows: int, rank: int) -> int:
     """Bytes of workspace ``adapter_linear`` takes for these sizes."""
-    a = _lib.moe_ep_adapter_args(num_rows=rows, rank=rank, num_adapters=1, in_features=8, out_features=8)
+    a = _lib.moe_ep_adapter_args(num_rows=rows, rank=rank, num_adapters=1, in_features=8, out_features=1)
     return _lib.moe_ep_adapter_workspace_bytes(a)

@@ -616,7 +616,8 @@ typedef struct moe_ep_adapter_args {
 #define MOE_EP_MAX_RANK 1024
 
 /* Bytes of device workspace moe_ep_adapter_linear needs for these sizes (the
- * sizes are read; pointers are not followed): 4 for each row and rank. */
+ * sizes are read; pointers are not followed): 6 for each row and rank (rounded
+ * up to 32), 16 (rounded up to 8) up to 64 rows. */
 MOE_EP_API int moe_ep_adapter_workspace_bytes(const moe_ep_adapter_args* args, size_t* out_bytes);
 
 /* A projection that all rows share, with a low-rank adapter of each row's own:
@@ -626,8 +627,7 @@ MOE_EP_API int moe_ep_adapter_workspace_bytes(const moe_ep_adapter_args* args, s
  * is in an adapter that a row does not name does not reach the row.  out must
  * not overlap an input, each taken from its first element to its last.  The
  * workspace holds nothing between calls; calls that may overlap in time need
- * one each.  Two kernel launches, and one more for each 2048 rows after the
- * first. */
+ * one each.  Two kernel launches. */
 MOE_EP_API int moe_ep_adapter_linear(const moe_ep_adapter_args* args, void* stream);
 
 /* Static text for a status code. */

@@ -131,8 +131,7 @@ def test_no_rows():
     assert run(x[:0], w, a, b, ids[:0], scales).shape == (0, 16)
 
 
-def test_more_rows_than_one_pass():
-    """The low-rank product takes 2048 rows at a time."""
+def test_many_rows():
     x, w, a, b, _, scales = make(2100, 40, 64, 3, 8, BF16)
     ids = (torch.arange(2100) // 100 % 4 - 1).to(torch.int32)
     check(run(x, w, a, b, ids, scales), x, w, a, b, ids, scales)
