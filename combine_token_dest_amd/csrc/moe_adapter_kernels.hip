@@ -1,17 +1,19 @@
 // gfx950 kernels of a shared projection with low-rank adapters:
 //   y[r] = W x[r] + s_a B_a (A_a x[r]), a = ids[r].
 //
-// low_kernel makes the scaled low-rank values s_a A_a x: 1 or 16 rows of x to
+// low_kernel makes the scaled low-rank values s_a A_a x: 1 or 8 rows of x to
 // a workgroup, and the rows of A of each adapter that they name, one adapter
 // after another.  Up to kLowFew rows share k between workgroups, whose float32
 // sums the second kernel adds in turn.
 //
-// The shared product is that of moe_gemm_device.h.  Behind it, while the sums
-// are still in registers, a wave goes through the adapters that its rows name,
-// one after another: B_a's rows times the low-rank values by matrix
-// instructions, added to the rows that have this adapter and to no others (a
-// row's result never meets another adapter's B, whatever is in it).  The low
-// values go in as three bfloat16 each, float32's 24 bits.  Few rows take the
+// The shared product is that of moe_gemm_device.h.  Its sums begin with the
+// adapters', made while the first tiles are on their way (behind the product
+// the same took 22 us of 136, most of it waiting for ids, low values and B, for
+// 2048 rows, 4096 x 7168 and one adapter): a wave goes through the adapters
+// that its rows name, one after another, B_a's rows times the low values by
+// matrix instructions, added to the rows that have this adapter and to no
+// others (a row's result never meets another adapter's B, whatever is in it).
+// The low values go in as three bfloat16 each, float32's 24 bits.  Few rows take the
 // kernel that streams the weights (moe_few_device.h), where each result adds
 // its own adapter's sum over the rank in float32, made while the first weights
 // are on their way.
@@ -28,25 +30,52 @@
 namespace moe_ep_detail {
 namespace {
 
-// Eight elements of a row of `rank` from k on; zeros past it.
-__device__ __forceinline__ u32x4 b_elements(const uint16_t* row, int k, int rank) {
-  if (k + 8 <= rank) return load_any8(row + k);
-  u32x4 v = {0, 0, 0, 0};
+// Eight elements from k on of COUNT rows of `rank`; zeros past it.  All loads
+// go out at once: with a branch for each row's end every load would wait for
+// the one before (prompts of 2048 rows, 4096 x 7168: 143 us, and 123 so).
+template <int COUNT>
+__device__ __forceinline__ void b_elements(const uint16_t* const (&row)[COUNT], int k, int rank, u32x4 (&v)[COUNT]) {
+  if (rank >= 8) {
+    // the last eight of the row where fewer are left, moved to the front
+    const int have = rank - k, at = min(k, rank - 8), gone = 16 * (8 - max(min(have, 8), 0));
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (k + e < rank) v[e >> 1] |= (uint32_t)row[k + e] << (e & 1) * 16;
-  return v;
+    for (int i = 0; i < COUNT; ++i) v[i] = load_any8(row[i] + at);
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) {
+      typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
+      const u64x2 w = __builtin_bit_cast(u64x2, v[i]);
+      u64x2 r;
+      r[0] = gone == 0 ? w[0] : gone < 64 ? w[0] >> gone | w[1] << (64 - gone) : gone < 128 ? w[1] >> (gone - 64) : 0;
+      r[1] = gone < 64 ? w[1] >> gone : 0;
+      v[i] = __builtin_bit_cast(u32x4, r);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) {
+      uint32_t e[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) e[j] = row[i][min(k + j, rank - 1)];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) e[j] = k + j < rank ? e[j] : 0u;
+      v[i] = u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
+    }
+  }
 }
 
-constexpr int kLowWaves = 8;
+// Waves of a workgroup of low_kernel: more where registers allow it.
+constexpr int low_waves(int rt) { return rt == 1 ? 16 : 8; }
 // Calls of up to this many rows, which may be one request's each, take them
 // one by one; more are prompts, whose rows share adapters.
 constexpr int kLowSingle = 512;
 
 // The low values of BLOCK rows of x and 16 RT of the rank.
 template <class T, int BLOCK, int RT, bool FEW>
-__global__ void __launch_bounds__(kLowWaves * 64) low_kernel(AdapterKArgs a) {
-  __shared__ f32x4 sums[kLowWaves][RT][16][4];
+__global__ void __launch_bounds__(low_waves(RT) * 64) low_kernel(AdapterKArgs a) {
+  constexpr int kLowWaves = low_waves(RT);
+  typedef Few<T, RT, 1, kLowWaves> F;
+  static_assert(F::kLds >= RT * 1024, "the sums fit a wave's piece");
+  __shared__ __attribute__((aligned(1024))) char lds[kLowWaves * F::kLds];
+  f32x4 (*sums)[RT][16][4] = reinterpret_cast<f32x4 (*)[RT][16][4]>(lds);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, i = lane & 15;
   const int r0 = blockIdx.x * BLOCK, k0 = blockIdx.y * (16 * RT), split = blockIdx.z;
   const int R = a.rank, n = a.x.rows;
@@ -54,7 +83,6 @@ __global__ void __launch_bounds__(kLowWaves * 64) low_kernel(AdapterKArgs a) {
   // lanes of the same row name the same adapter; rows past the last none
   int id = r0 + min(i, BLOCK - 1) < n ? a.ids[row] : -1;
   if (id < 0 || id >= a.adapters) id = -1;
-  const uint16_t* rb[1] = {a.x.p + (int64_t)row * a.x.stride};
   // this part's steps of 64 k
   constexpr int splits = FEW ? kLowSplits : 1;
   const int steps = a.k / 64, left = a.k % 64;
@@ -63,19 +91,19 @@ __global__ void __launch_bounds__(kLowWaves * 64) low_kernel(AdapterKArgs a) {
   while (pending) {
     const int ad = __builtin_amdgcn_readlane(id, __builtin_ctzll(pending));
     pending &= ~__ballot(id == ad);
-    const uint16_t* ra[RT];
-#pragma unroll
-    for (int m = 0; m < RT; ++m) ra[m] = a.a + ((int64_t)ad * R + min(k0 + m * 16 + i, R - 1)) * a.k;
-    Few<T, RT, 1, kLowWaves> few;
-    few.aim(ra, rb, first, last - first, blockIdx.x);
+    F few;
+    few.aim([&](int m, int r) { return a.a + ((int64_t)ad * R + min(k0 + m * 16 + r, R - 1)) * a.k; },
+            [&](int, int r) { return a.x.p + (int64_t)min(r0 + min(r, BLOCK - 1), n - 1) * a.x.stride; }, first,
+            last - first, blockIdx.x, lds + wave * F::kLds);
     few.prime(wave, kLowWaves);
     f32x4 acc[RT][1] = {};
     few.run(wave, kLowWaves, acc);
     if (left && split == splits - 1 && wave == kLowWaves - 1) few.tail(left, acc);
+    __syncthreads();                                      // the waves' pieces of lds become the sums
 #pragma unroll
     for (int m = 0; m < RT; ++m) sums[wave][m][i][lane >> 4] = acc[m][0];
     __syncthreads();
-    const float* sum = reinterpret_cast<const float*>(sums);
+    const float* sum = reinterpret_cast<const float*>(lds);
     const float scale = a.scales ? a.scales[ad] : 1.0f;
     // a rank up to 16 is followed by zeros up to 32 where the stride has them
     constexpr int kWide = RT == 1 && !FEW ? 32 : 16 * RT;
@@ -105,16 +133,17 @@ __global__ void __launch_bounds__(kLowWaves * 64) low_kernel(AdapterKArgs a) {
 // Up to 16 NT rows: 16 columns of the result to a workgroup.
 template <class T, int NT, int WAVES>
 __global__ void __launch_bounds__(WAVES * 64) adapter_few_kernel(AdapterKArgs a) {
-  __shared__ f32x4 sums[WAVES][NT][16][4];
+  typedef Few<T, 1, NT, WAVES> F;
+  constexpr int kSums = WAVES * NT * 1024;
+  __shared__ __attribute__((aligned(1024))) char lds[kSums > WAVES * F::kLds ? kSums : WAVES * F::kLds];
+  f32x4 (*sums)[NT][16][4] = reinterpret_cast<f32x4 (*)[NT][16][4]>(lds);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, i = lane & 15;
   const int c0 = blockIdx.x * 16, N = a.w.rows, R = a.rank;
-  const uint16_t* ra[1] = {a.w.p + (int64_t)min(c0 + i, N - 1) * a.w.stride};
-  const uint16_t* rb[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) rb[t] = a.x.p + (int64_t)min(t * 16 + i, a.x.rows - 1) * a.x.stride;
-  Few<T, 1, NT, WAVES> few;
+  F few;
   const int steps = a.k / 64, left = a.k % 64;
-  few.aim(ra, rb, 0, steps, blockIdx.x);
+  few.aim([&](int, int r) { return a.w.p + (int64_t)min(c0 + r, N - 1) * a.w.stride; },
+          [&](int t, int r) { return a.x.p + (int64_t)min(t * 16 + r, a.x.rows - 1) * a.x.stride; }, 0, steps,
+          blockIdx.x, lds + wave * F::kLds);
   few.prime(wave, WAVES);
   // The adapters' sums of this thread's results, while the first weights are on their way.
   constexpr int kMine = (NT * 256 + WAVES * 64 - 1) / (WAVES * 64);
@@ -132,7 +161,10 @@ __global__ void __launch_bounds__(WAVES * 64) adapter_few_kernel(AdapterKArgs a)
         const int64_t plane = (int64_t)a.x.rows * a.low_stride;
 #pragma unroll kUnroll
         for (int k = 0; k < R; k += 8) {
-          const u32x4 w = b_elements(b, k, R);
+          u32x4 bv[1];
+          const uint16_t* const rows[1] = {b};
+          b_elements<1>(rows, k, R, bv);
+          const u32x4 w = bv[0];
           f32x4 v[kLowSplits][2];
 #pragma unroll
           for (int s = 0; s < kLowSplits; ++s)
@@ -153,10 +185,11 @@ __global__ void __launch_bounds__(WAVES * 64) adapter_few_kernel(AdapterKArgs a)
   f32x4 acc[1][NT] = {};
   few.run(wave, WAVES, acc);
   if (left && steps % WAVES == wave) few.tail(left, acc);
+  __syncthreads();                                        // the waves' pieces of lds become the sums
 #pragma unroll
   for (int t = 0; t < NT; ++t) sums[wave][t][i][lane >> 4] = acc[0][t];
   __syncthreads();
-  const float* sum = reinterpret_cast<const float*>(sums);
+  const float* sum = reinterpret_cast<const float*>(lds);
 #pragma unroll
   for (int m = 0; m < kMine; ++m) {
     const int o = m * WAVES * 64 + threadIdx.x, r = o >> 4, c = c0 + (o & 15);
@@ -181,49 +214,76 @@ __global__ void __launch_bounds__(G::kThreads, G::kThreads / 256) adapter_kernel
   typename G::SideQ sq;
   sp.aim(a.w, pt * G::TP);
   sq.aim(a.x, qt * G::TQ);
+  G::begin((MOE_EP_LDS char*)lds, sp, sq, a.k);
   typename G::Acc acc;
-  if (!G::run((MOE_EP_LDS char*)lds, sp, sq, a.k, acc)) return;
+  G::clear(acc);
 
   const int lane = threadIdx.x & 63, quarter = lane >> 4;
   const int N = a.w.rows, R = a.rank;
+  if (G::wave_k() == 0) {
+    int id[G::FQ];
+    const uint16_t* low[G::FQ];
 #pragma unroll
-  for (int j = 0; j < G::FQ; ++j) {
-    const int q = qt * G::TQ + G::wave_q() + j * 16 + (lane & 15);
-    const bool here = q < a.x.rows;
-    int id = here ? a.ids[q] : -1;
-    if (id < 0 || id >= a.adapters) id = -1;
-    uint64_t pending = __ballot(id >= 0);
-    while (pending) {
-      const int ad = __builtin_amdgcn_readlane(id, __builtin_ctzll(pending));
-      pending &= ~__ballot(id == ad);
-      const uint16_t* low = static_cast<const uint16_t*>(a.low) + (int64_t)(here ? q : 0) * a.low_stride + quarter * 8;
-      const int64_t plane = (int64_t)a.x.rows * a.low_stride;
+    for (int j = 0; j < G::FQ; ++j) {
+      const int q = qt * G::TQ + G::wave_q() + j * 16 + (lane & 15);
+      id[j] = q < a.x.rows ? a.ids[q] : -1;
+      low[j] = static_cast<const uint16_t*>(a.low) + (int64_t)min(q, a.x.rows - 1) * a.low_stride + quarter * 8;
+    }
+    const int64_t plane = (int64_t)a.x.rows * a.low_stride;
+    uint64_t pending[G::FQ];
+#pragma unroll
+    for (int j = 0; j < G::FQ; ++j) pending[j] = __ballot(id[j] >= 0 && id[j] < a.adapters);
+    while (true) {
+      int ad = -1;
+#pragma unroll
+      for (int j = 0; j < G::FQ; ++j)
+        if (ad < 0 && pending[j]) ad = __builtin_amdgcn_readlane(id[j], __builtin_ctzll(pending[j]));
+      if (ad < 0) break;
+      uint64_t mine[G::FQ];
+#pragma unroll
+      for (int j = 0; j < G::FQ; ++j) {
+        mine[j] = __ballot(id[j] == ad);
+        pending[j] &= ~mine[j];
+      }
       for (int k = 0; k < R; k += 32) {
-        u32x4 part[kParts];
+        u32x4 part[G::FQ][kParts], b[G::FP];
+        const uint16_t* rows[G::FP];
 #pragma unroll
-        for (int pl = 0; pl < kParts; ++pl) part[pl] = *reinterpret_cast<const u32x4*>(low + pl * plane + k);
-        u32x4 b[G::FP];
+        for (int j = 0; j < G::FQ; ++j)
+#pragma unroll
+          for (int pl = 0; pl < kParts; ++pl) part[j][pl] = *reinterpret_cast<const u32x4*>(low[j] + pl * plane + k);
 #pragma unroll
         for (int i = 0; i < G::FP; ++i) {
           const int p = min(pt * G::TP + G::wave_p() + i * 16 + (lane & 15), N - 1);
-          b[i] = b_elements(a.b + ((int64_t)ad * N + p) * R, k + quarter * 8, R);
+          rows[i] = a.b + ((int64_t)ad * N + p) * R;
         }
+        b_elements<G::FP>(rows, k + quarter * 8, R, b);
 #pragma unroll
-        for (int i = 0; i < G::FP; ++i) {
-          f32x4 sum = {0, 0, 0, 0};
-          u32x4 v[2] = {b[i], {}};
-          if constexpr (std::is_same<T, F16>::value) split_f16(b[i], &v[0], &v[1]);
+        for (int j = 0; j < G::FQ; ++j) {
+          if (!mine[j]) continue;
 #pragma unroll
-          for (int pl = 0; pl < kParts; ++pl) {
-            sum = BF16::mfma(v[0], part[pl], sum);
-            if constexpr (std::is_same<T, F16>::value) sum = BF16::mfma(v[1], part[pl], sum);
+          for (int i = 0; i < G::FP; ++i) {
+            f32x4 sum = {0, 0, 0, 0};
+            u32x4 v[2] = {b[i], {}};
+            if constexpr (std::is_same<T, F16>::value) split_f16(b[i], &v[0], &v[1]);
+#pragma unroll
+            for (int pl = 0; pl < kParts; ++pl) {
+              sum = BF16::mfma(v[0], part[j][pl], sum);
+              if constexpr (std::is_same<T, F16>::value) sum = BF16::mfma(v[1], part[j][pl], sum);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][j][e] = id[j] == ad ? acc[i][j][e] + sum[e] : acc[i][j][e];
           }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][j][e] = id == ad ? acc[i][j][e] + sum[e] : acc[i][j][e];
         }
       }
     }
-    if (!here) continue;
+  }
+
+  if (!G::run((MOE_EP_LDS char*)lds, sp, sq, a.k, acc)) return;
+#pragma unroll
+  for (int j = 0; j < G::FQ; ++j) {
+    const int q = qt * G::TQ + G::wave_q() + j * 16 + (lane & 15);
+    if (q >= a.x.rows) continue;
 #pragma unroll
     for (int i = 0; i < G::FP; ++i) {
       const int c = pt * G::TP + G::wave_p() + i * 16 + quarter * 4;
@@ -252,9 +312,8 @@ hipError_t adapter_few(const AdapterKArgs& a, hipStream_t stream) {
 template <class T, int BLOCK, bool FEW>
 hipError_t low(const AdapterKArgs& a, hipStream_t stream) {
   const dim3 grid(tiles(a.x.rows, BLOCK), a.rank <= 16 ? 1 : tiles(a.rank, 64), FEW ? kLowSplits : 1);
-  const dim3 block(kLowWaves * 64);
-  if (a.rank <= 16) low_kernel<T, BLOCK, 1, FEW><<<grid, block, 0, stream>>>(a);
-  else low_kernel<T, BLOCK, 4, FEW><<<grid, block, 0, stream>>>(a);
+  if (a.rank <= 16) low_kernel<T, BLOCK, 1, FEW><<<grid, dim3(low_waves(1) * 64), 0, stream>>>(a);
+  else low_kernel<T, BLOCK, 4, FEW><<<grid, dim3(low_waves(4) * 64), 0, stream>>>(a);
   return hipGetLastError();
 }
 template <class T>
@@ -263,7 +322,7 @@ hipError_t adapter(const AdapterKArgs& a, hipStream_t stream) {
   const int n = a.x.rows;
   const hipError_t e = n <= kLowFew      ? low<T, 1, true>(a, stream)
                        : n <= kLowSingle ? low<T, 1, false>(a, stream)
-                                         : low<T, 16, false>(a, stream);
+                                         : low<T, 8, false>(a, stream);
   if (e != hipSuccess) return e;
   if (n <= 16) return adapter_few<T, 1>(a, stream);
   if (n <= 32) return adapter_few<T, 2>(a, stream);

@@ -6,12 +6,16 @@
 // the A operand of v_mfma_f32_16x16x32, and rows of x are the columns of B;
 // its waves share k, 64 k (128 bytes of a row) a step in turn, each with
 // kDepth steps' loads under way, and their sums are added through LDS in a
-// fixed order.  Nothing goes through LDS on the way in: a weight is used by
-// one wave only, and x comes from L2.
+// fixed order.
 //
-// Workgroups begin at different k and go around: rows of 4096 elements start
-// in the same channel of L2, and all workgroups at one k would ask the same
-// few channels.
+// As operands, 16 lanes side by side hold 16 rows; loaded like that, each
+// would touch a cache line of its own, and the first cache's look-ups would
+// be the limit.  So 8 lanes load a row's 128 bytes, and at its use a step goes
+// through the wave's own piece of LDS, which hands it out as operands: unit u
+// of row r is at u ^ (r & 7) there.
+//
+// Workgroups begin at different k and go around, so that rows that start in
+// the same channel of L2 are not all asked for at once.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -27,68 +31,78 @@ namespace {
 // x.
 template <class T, int MT, int NT, int WAVES>
 struct Few {
-  static constexpr int kRegs = 8 * (MT + NT);             // of a step
-  static constexpr int kMost = (WAVES > 8 ? 72 : 104) / kRegs;    // 16 waves have 128 registers each
+  static constexpr int kSets = MT + NT;
+  static constexpr int kMost = (WAVES > 8 ? 72 : 104) / (8 * kSets);    // 16 waves have 128 registers each
   static constexpr int kDepth = kMost > 4 ? 4 : kMost;
+  static constexpr int kLds = kSets * 2048;               // bytes of a wave's piece
   static_assert(kDepth >= 2, "a step's loads go out while another's are used");
   struct Stage {
-    u32x4 a[MT][2], b[NT][2];
+    u32x4 v[kSets][2];
   };
 
-  const uint16_t* a[MT];      // the lane's rows, at its first k of a step
-  const uint16_t* b[NT];
-
+  const uint16_t* p[kSets][2];   // the lane's unit of rows lane / 8 and 8 + lane / 8, in step 0
   int steps;                  // whole steps of 64 k that the waves share
   int turn;                   // step 0's place among them
+  MOE_EP_LDS char* lds;
 
-  // The rows of the lane (lane & 15), their steps' number, and who begins where.
-  __device__ __forceinline__ void aim(const uint16_t* const (&ra)[MT], const uint16_t* const (&rb)[NT], int64_t first,
-                                      int count, int workgroup) {
-    const int64_t k = first * 64 + (threadIdx.x & 63) / 16 * 8;
+  static __device__ __forceinline__ int lane() { return threadIdx.x & 63; }
+  static __device__ __forceinline__ int unit() { return (lane() & 7) ^ (lane() >> 3); }
+
+  // a(m, i) and b(t, i) are row i of each set; the steps begin at step `first`
+  // of the rows; `piece` is the wave's LDS.
+  template <class A, class B>
+  __device__ __forceinline__ void aim(A a, B b, int64_t first, int count, int workgroup, void* piece) {
+    lds = (MOE_EP_LDS char*)piece;
+#pragma unroll
+    for (int s = 0; s < kSets; ++s)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = h * 8 + (lane() >> 3);
+        p[s][h] = (s < MT ? a(s, row) : b(s - MT, row)) + first * 64 + unit() * 8;
+      }
     steps = count;
     // 19 steps are 2432 bytes: neighbours are in channels of their own
     turn = count > 0 ? workgroup * 19 % count : 0;
-#pragma unroll
-    for (int m = 0; m < MT; ++m) a[m] = ra[m] + k;
-#pragma unroll
-    for (int t = 0; t < NT; ++t) b[t] = rb[t] + k;
   }
 
-  __device__ __forceinline__ void load(Stage& s, int step) const {
+  __device__ __forceinline__ void load(Stage& st, int step) const {
     const int place = step + turn, at = (place >= steps ? place - steps : place) * 64;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int s = 0; s < kSets; ++s)
 #pragma unroll
-      for (int m = 0; m < MT; ++m) s.a[m][h] = load_any8(a[m] + at + h * 32);
-#pragma unroll
-      for (int t = 0; t < NT; ++t) s.b[t][h] = load_any8(b[t] + at + h * 32);
-    }
+      for (int h = 0; h < 2; ++h) st.v[s][h] = load_any8(p[s][h] + at);
   }
   // The step after the whole ones, of which only `left` (1..63) k exist.
-  __device__ __forceinline__ void load_cut(Stage& s, int left) const {
-    const int at = steps * 64;
-    const int k = (threadIdx.x & 63) / 16 * 8;
+  __device__ __forceinline__ void load_cut(Stage& st, int left) const {
+    const int at = steps * 64, have = left - unit() * 8;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int have = left - k - h * 32;
+    for (int s = 0; s < kSets; ++s)
 #pragma unroll
-      for (int i = 0; i < MT + NT; ++i) {
-        const uint16_t* p = (i < MT ? a[i < MT ? i : 0] : b[i < MT ? 0 : i - MT]) + at + h * 32;
-        u32x4 v = {0, 0, 0, 0};
-        if (have >= 8) v = load_any8(p);
-        else if (have > 0) v = keep_last(load_any8(p + (have - 8)), have);
-        if (i < MT) s.a[i < MT ? i : 0][h] = v;
-        else s.b[i < MT ? 0 : i - MT][h] = v;
+      for (int h = 0; h < 2; ++h) {
+        if (have >= 8) st.v[s][h] = load_any8(p[s][h] + at);
+        else if (have > 0) st.v[s][h] = keep_last(load_any8(p[s][h] + at + (have - 8)), have);
+        else st.v[s][h] = u32x4{0, 0, 0, 0};
       }
-    }
   }
-  static __device__ __forceinline__ void add(const Stage& s, f32x4 (&acc)[MT][NT]) {
+  // (A wave's LDS accesses take their turn, so the next step's writes come
+  // after this one's reads.)
+  __device__ __forceinline__ void add(const Stage& st, f32x4 (&acc)[MT][NT]) const {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int s = 0; s < kSets; ++s)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) *(MOE_EP_LDS u32x4*)(lds + s * 2048 + h * 1024 + lane() * 16) = st.v[s][h];
+    const int row = lane() & 15;
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      u32x4 f[kSets];
+#pragma unroll
+      for (int s = 0; s < kSets; ++s)
+        f[s] = *(const MOE_EP_LDS u32x4*)(lds + s * 2048 + row * 128 + ((ks * 4 + (lane() >> 4)) ^ (row & 7)) * 16);
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) acc[m][t] = T::mfma(s.a[m][h], s.b[t][h], acc[m][t]);
+        for (int t = 0; t < NT; ++t) acc[m][t] = T::mfma(f[m], f[MT + t], acc[m][t]);
+    }
   }
 
   Stage stage[kDepth];
@@ -117,9 +131,9 @@ struct Few {
       if (s + d * stride < steps) add(stage[d], acc);
   }
   __device__ __forceinline__ void tail(int left, f32x4 (&acc)[MT][NT]) {
-    Stage s;
-    load_cut(s, left);
-    add(s, acc);
+    Stage st;
+    load_cut(st, left);
+    add(st, acc);
   }
 };
 

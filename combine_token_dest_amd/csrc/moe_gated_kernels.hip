@@ -40,7 +40,9 @@ __global__ void __launch_bounds__(G::kThreads, G::kThreads / 256) gated_kernel(G
   typename G::SideQ sq;
   sp.aim(a.w, pt * (G::TP / 2));
   sq.aim(a.x, qt * G::TQ);
+  G::begin((MOE_EP_LDS char*)lds, sp, sq, a.hidden);
   typename G::Acc acc;
+  G::clear(acc);
   if (!G::run((MOE_EP_LDS char*)lds, sp, sq, a.hidden, acc)) return;
   const int lane = threadIdx.x & 63;
 #pragma unroll
@@ -70,24 +72,26 @@ __global__ void __launch_bounds__(G::kThreads, G::kThreads / 256) gated_kernel(G
 // same eight up rows to a workgroup.
 template <class T, int NT, int WAVES>
 __global__ void __launch_bounds__(WAVES * 64) gated_few_kernel(GatedKArgs a) {
-  __shared__ f32x4 sums[WAVES][NT][16][4];
+  typedef Few<T, 1, NT, WAVES> F;
+  constexpr int kSums = WAVES * NT * 1024;
+  __shared__ __attribute__((aligned(1024))) char lds[kSums > WAVES * F::kLds ? kSums : WAVES * F::kLds];
+  f32x4 (*sums)[NT][16][4] = reinterpret_cast<f32x4 (*)[NT][16][4]>(lds);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, i = lane & 15;
   const int c0 = blockIdx.x * 8;
-  const uint16_t* ra[1] = {a.w.p + ((int64_t)min(c0 + (i & 7), a.inter - 1) + (i & 8 ? a.inter : 0)) * a.w.stride};
-  const uint16_t* rb[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) rb[t] = a.x.p + (int64_t)min(t * 16 + i, a.x.rows - 1) * a.x.stride;
-  Few<T, 1, NT, WAVES> few;
+  F few;
   const int steps = a.hidden / 64, left = a.hidden % 64;
-  few.aim(ra, rb, 0, steps, blockIdx.x);
+  few.aim([&](int, int r) { return a.w.p + ((int64_t)min(c0 + (r & 7), a.inter - 1) + (r & 8 ? a.inter : 0)) * a.w.stride; },
+          [&](int t, int r) { return a.x.p + (int64_t)min(t * 16 + r, a.x.rows - 1) * a.x.stride; }, 0, steps,
+          blockIdx.x, lds + wave * F::kLds);
   few.prime(wave, WAVES);
   f32x4 acc[1][NT] = {};
   few.run(wave, WAVES, acc);
   if (left && steps % WAVES == wave) few.tail(left, acc);
+  __syncthreads();                                        // the waves' pieces of lds become the sums
 #pragma unroll
   for (int t = 0; t < NT; ++t) sums[wave][t][i][lane >> 4] = acc[0][t];
   __syncthreads();
-  const float* sum = reinterpret_cast<const float*>(sums);
+  const float* sum = reinterpret_cast<const float*>(lds);
   for (int o = threadIdx.x; o < a.x.rows * 8; o += WAVES * 64) {
     const int r = o >> 3, c = o & 7;
     if (c0 + c >= a.inter) continue;
@@ -118,7 +122,9 @@ __global__ void __launch_bounds__(G::kThreads, G::kThreads / 256) product_kernel
   typename G::SideQ sq;
   sp.aim(a.p, pt * G::TP);
   sq.aim(a.q, qt * G::TQ);
+  G::begin((MOE_EP_LDS char*)lds, sp, sq, a.k);
   typename G::Acc acc;
+  G::clear(acc);
   if (!G::run((MOE_EP_LDS char*)lds, sp, sq, a.k, acc)) return;
   const float factor = a.factor ? *a.factor : 1.0f;
   const int lane = threadIdx.x & 63;

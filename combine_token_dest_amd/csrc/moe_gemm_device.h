@@ -37,6 +37,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <cmath>
+
 #include "moe_dense_internal.h"
 #include "moe_experts_device.h"
 
@@ -296,20 +298,26 @@ struct Gemm {
     __builtin_amdgcn_sched_barrier(0);
   }
 
-  // The tile's sums over all K, in the waves with wave_k() 0; the others
-  // return false.
-  static __device__ __forceinline__ bool run(MOE_EP_LDS char* lds, SideP& sp, SideQ& sq, int K, Acc& acc) {
+  static __device__ __forceinline__ void clear(Acc& acc) {
 #pragma unroll
     for (int i = 0; i < FP; ++i)
 #pragma unroll
       for (int j = 0; j < FQ; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-    if (K <= 0) return wave_k() == 0;
+  }
+
+  // Sends out the first two tiles of k.
+  static __device__ __forceinline__ void begin(MOE_EP_LDS char* lds, SideP& sp, SideQ& sq, int K) {
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       const int left = K - b * kK;
       if (DIRECT && left >= kK) load(lds + b * kBuffer, sp, sq);
       else if (left > 0) fill(lds + b * kBuffer, sp, sq, left);
     }
+  }
+  // After begin(): adds the products over all K to acc.  The sums are in the
+  // waves with wave_k() 0; the others return false.
+  static __device__ __forceinline__ bool run(MOE_EP_LDS char* lds, SideP& sp, SideQ& sq, int K, Acc& acc) {
+    if (K <= 0) return wave_k() == 0;
     meet();
     FragsP p;
     FragsQ q;
@@ -395,13 +403,37 @@ __device__ __forceinline__ void store4(void* out, int64_t at, bool f32, int have
 
 constexpr int tiles(int64_t rows, int tile) { return (int)((rows + tile - 1) / tile); }
 
-// The tiles for P x Q results: the largest of which there are enough for the
-// card's 256 CUs.
+// The tiles for P x Q results.  Larger ones move less for each product, but
+// the card's 256 CUs, one tile each at a time, go through them in rounds.  A
+// round takes, for 64 k: 1.6 us with tiles of 256 x 256, 1.0 of 256 x 128 (1.15
+// where several rounds crowd the caches), 0.57 of 128 x 128, 0.28 of 64 x 64; a
+// last round that is not full leaves power to those that work.  Measured,
+// gated products of rows x 4096 (k 7168), us with each:
+//   rows        128   256   512  1024  2048  4096  8192
+//   256 x 256   149   154   153   153   154   189   385
+//   256 x 128    99    99    98    98   113   276   518
+//   128 x 128    58    58    58    64   127   309   576
+//    64 x 64     30    31    61   121   240   515  1056
 enum TileSize { k256x256, k256x128, k128x128, k64x64 };
 inline TileSize tile_size(int64_t P, int64_t Q, bool direct) {
-  if (direct && (int64_t)tiles(P, 256) * tiles(Q, 256) >= 192) return k256x256;
-  if (direct && (int64_t)tiles(P, 256) * tiles(Q, 128) >= 192) return k256x128;
-  return (int64_t)tiles(P, 128) * tiles(Q, 128) >= 160 ? k128x128 : k64x64;
+  constexpr struct {
+    TileSize size;
+    int p, q;
+    double one, more;         // us of a round for 64 k: the only one, or one of several
+  } kinds[] = {{k256x256, 256, 256, 1.6, 1.6}, {k256x128, 256, 128, 1.0, 1.15}, {k128x128, 128, 128, 0.57, 0.57},
+               {k64x64, 64, 64, 0.28, 0.28}};
+  TileSize best = k64x64;
+  double least = 1e300;
+  for (const auto& k : kinds) {
+    if (!direct && k.p > 128) continue;                   // through registers there are the two smaller ones
+    const double r = (double)((P + k.p - 1) / k.p) * (double)((Q + k.q - 1) / k.q) / 256;
+    const double time = r <= 1 ? k.one : k.more * (r + std::ceil(r)) / 2;
+    if (time < least) {
+      least = time;
+      best = k.size;
+    }
+  }
+  return best;
 }
 
 }  // namespace
