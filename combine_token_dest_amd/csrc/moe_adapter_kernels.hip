@@ -6,13 +6,13 @@
 // after another.  Up to kLowFew rows share k between workgroups, whose float32
 // sums the second kernel adds in turn.
 //
-// The shared product is that of moe_gemm_device.h.  Its sums begin with the
-// adapters', made while the first tiles are on their way (behind the product
-// the same took 22 us of 136, most of it waiting for ids, low values and B, for
-// 2048 rows, 4096 x 7168 and one adapter): a wave goes through the adapters
-// that its rows name, one after another, B_a's rows times the low values by
-// matrix instructions, added to the rows that have this adapter and to no
-// others (a row's result never meets another adapter's B, whatever is in it).
+// The shared product is that of moe_gemm_device.h.  Behind it, while the sums
+// are still in registers, a wave goes through the adapters that its rows name,
+// one after another: B_a's rows times the low values by matrix instructions,
+// added to the rows that have this adapter and to no others (a row's result
+// never meets another adapter's B, whatever is in it).  (Before the product it
+// would wait no longer than the first tiles do, but the compiler then finds no
+// registers for the product's loop.)
 // The low values go in as three bfloat16 each, float32's 24 bits.  Few rows take the
 // kernel that streams the weights (moe_few_device.h), where each result adds
 // its own adapter's sum over the rank in float32, made while the first weights
@@ -30,31 +30,27 @@
 namespace moe_ep_detail {
 namespace {
 
-// Eight elements from k on of COUNT rows of `rank`; zeros past it.  All loads
-// go out at once: with a branch for each row's end every load would wait for
-// the one before (prompts of 2048 rows, 4096 x 7168: 143 us, and 123 so).
+// Eight elements from k on of COUNT rows of `rank`, which start `row` bytes
+// after base; zeros past the rank.  All loads go out at once: with a branch
+// for each row's end every load would wait for the one before.
 template <int COUNT>
-__device__ __forceinline__ void b_elements(const uint16_t* const (&row)[COUNT], int k, int rank, u32x4 (&v)[COUNT]) {
+__device__ __forceinline__ void b_elements(const uint16_t* base, const uint32_t (&row)[COUNT], int k, int rank,
+                                           u32x4 (&v)[COUNT]) {
+  const uint8_t* p = reinterpret_cast<const uint8_t*>(base);
   if (rank >= 8) {
     // the last eight of the row where fewer are left, moved to the front
-    const int have = rank - k, at = min(k, rank - 8), gone = 16 * (8 - max(min(have, 8), 0));
+    const int have = rank - k, at = min(k, rank - 8) * 2;
 #pragma unroll
-    for (int i = 0; i < COUNT; ++i) v[i] = load_any8(row[i] + at);
+    for (int i = 0; i < COUNT; ++i) v[i] = load_any8(p + (row[i] + at));
 #pragma unroll
-    for (int i = 0; i < COUNT; ++i) {
-      typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
-      const u64x2 w = __builtin_bit_cast(u64x2, v[i]);
-      u64x2 r;
-      r[0] = gone == 0 ? w[0] : gone < 64 ? w[0] >> gone | w[1] << (64 - gone) : gone < 128 ? w[1] >> (gone - 64) : 0;
-      r[1] = gone < 64 ? w[1] >> gone : 0;
-      v[i] = __builtin_bit_cast(u32x4, r);
-    }
+    for (int i = 0; i < COUNT; ++i) v[i] = keep_last(v[i], have);
   } else {
 #pragma unroll
     for (int i = 0; i < COUNT; ++i) {
+      const uint16_t* r = reinterpret_cast<const uint16_t*>(p + row[i]);
       uint32_t e[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) e[j] = row[i][min(k + j, rank - 1)];
+      for (int j = 0; j < 8; ++j) e[j] = r[min(k + j, rank - 1)];
 #pragma unroll
       for (int j = 0; j < 8; ++j) e[j] = k + j < rank ? e[j] : 0u;
       v[i] = u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
@@ -62,16 +58,14 @@ __device__ __forceinline__ void b_elements(const uint16_t* const (&row)[COUNT], 
   }
 }
 
-// Waves of a workgroup of low_kernel: more where registers allow it.
-constexpr int low_waves(int rt) { return rt == 1 ? 16 : 8; }
+constexpr int kLowWaves = 8;
 // Calls of up to this many rows, which may be one request's each, take them
 // one by one; more are prompts, whose rows share adapters.
 constexpr int kLowSingle = 512;
 
 // The low values of BLOCK rows of x and 16 RT of the rank.
 template <class T, int BLOCK, int RT, bool FEW>
-__global__ void __launch_bounds__(low_waves(RT) * 64) low_kernel(AdapterKArgs a) {
-  constexpr int kLowWaves = low_waves(RT);
+__global__ void __launch_bounds__(kLowWaves * 64) low_kernel(AdapterKArgs a) {
   typedef Few<T, RT, 1, kLowWaves> F;
   static_assert(F::kLds >= RT * 1024, "the sums fit a wave's piece");
   __shared__ __attribute__((aligned(1024))) char lds[kLowWaves * F::kLds];
@@ -105,8 +99,9 @@ __global__ void __launch_bounds__(low_waves(RT) * 64) low_kernel(AdapterKArgs a)
     __syncthreads();
     const float* sum = reinterpret_cast<const float*>(lds);
     const float scale = a.scales ? a.scales[ad] : 1.0f;
-    // a rank up to 16 is followed by zeros up to 32 where the stride has them
+    // the last of the rank is followed by zeros up to the stride
     constexpr int kWide = RT == 1 && !FEW ? 32 : 16 * RT;
+    const bool last_of_rank = k0 + 16 * RT >= R;
     for (int o = threadIdx.x; o < BLOCK * kWide; o += kLowWaves * 64) {
       const int r = o / kWide, c = o % kWide, k = k0 + c;
       float v = 0;
@@ -115,7 +110,7 @@ __global__ void __launch_bounds__(low_waves(RT) * 64) low_kernel(AdapterKArgs a)
         for (int w = 0; w < kLowWaves; ++w) v += sum[((w * RT + c / 16) * 16 + r) * 16 + c % 16];
       }
       v = k < R ? v * scale : 0.0f;
-      if (__shfl(id, r) != ad || k >= a.low_stride) continue;
+      if (__shfl(id, r) != ad || k >= a.low_stride || (c >= 16 * RT && !last_of_rank)) continue;
       const int64_t at = (int64_t)(r0 + r) * a.low_stride + k, plane = (int64_t)n * a.low_stride;
       if constexpr (FEW) {
         static_cast<float*>(a.low)[split * plane + at] = v;
@@ -162,8 +157,8 @@ __global__ void __launch_bounds__(WAVES * 64) adapter_few_kernel(AdapterKArgs a)
 #pragma unroll kUnroll
         for (int k = 0; k < R; k += 8) {
           u32x4 bv[1];
-          const uint16_t* const rows[1] = {b};
-          b_elements<1>(rows, k, R, bv);
+          const uint32_t rows[1] = {0};
+          b_elements<1>(b, rows, k, R, bv);
           const u32x4 w = bv[0];
           f32x4 v[kLowSplits][2];
 #pragma unroll
@@ -204,6 +199,112 @@ __global__ void __launch_bounds__(WAVES * 64) adapter_few_kernel(AdapterKArgs a)
   }
 }
 
+// Adds the adapters' sums to a tile's results.
+template <class G>
+__device__ __forceinline__ void add_adapters(const AdapterKArgs& a, int pt, int qt, typename G::Acc& acc) {
+  typedef typename G::T T;
+  const int lane = threadIdx.x & 63, quarter = lane >> 4;
+  const int N = a.w.rows, R = a.rank;
+  // Each of the waves that share k takes its part of the adapters; B of the
+  // next one is loaded while this one's products are made.
+  constexpr int kWaves = G::kThreads / 64, kGroups = G::kK / 64;
+  static_assert(kWaves % kGroups == 0, "waves that share k");
+  constexpr int kPart = G::FP > 4 ? 4 : G::FP;          // columns' fragments at a time, within the registers
+  constexpr bool kKeep = G::FP * G::FQ <= 16;           // the low values of all rows at once
+  // Rows are found from the tile's first by 32-bit offsets (256 rows of 1024).
+  int id[G::FQ];
+  uint32_t low[G::FQ];
+  const uint16_t* low_base = static_cast<const uint16_t*>(a.low) + (int64_t)qt * G::TQ * a.low_stride;
+#pragma unroll
+  for (int j = 0; j < G::FQ; ++j) {
+    const int q = G::wave_q() + j * 16 + (lane & 15), last = a.x.rows - 1 - qt * G::TQ;
+    id[j] = q <= last ? a.ids[qt * G::TQ + q] : -1;
+    low[j] = (uint32_t)(min(q, last) * a.low_stride + quarter * 8) * 2;
+  }
+  const int64_t plane = (int64_t)a.x.rows * a.low_stride;
+  uint64_t pending[G::FQ];
+  // the next adapter that is left, or -1
+  auto next = [&]() {
+    int ad = -1;
+#pragma unroll
+    for (int j = 0; j < G::FQ; ++j)
+      if (ad < 0 && pending[j]) ad = __builtin_amdgcn_readlane(id[j], __builtin_ctzll(pending[j]));
+#pragma unroll
+    for (int j = 0; j < G::FQ; ++j) pending[j] &= ~__ballot(id[j] == ad);
+    return ad;
+  };
+  auto next_mine = [&]() {
+    int mine = -1;
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      const int ad = next();
+      if (g == G::wave_k()) mine = ad;
+    }
+    return mine;
+  };
+  for (int k = 0; k < R; k += 32) {
+    auto load_low = [&](int j, u32x4 (&part)[kParts]) {
+#pragma unroll
+      for (int pl = 0; pl < kParts; ++pl)
+        part[pl] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const uint8_t*>(low_base + pl * plane + k) + low[j]);
+    };
+    auto load_b = [&](int ad, int i0, u32x4 (&b)[kPart]) {
+      uint32_t rows[kPart];
+#pragma unroll
+      for (int i = 0; i < kPart; ++i)
+        rows[i] = (uint32_t)(min(G::wave_p() + (i0 + i) * 16 + (lane & 15), N - 1 - pt * G::TP) * R) * 2;
+      const uint16_t* base = a.b + ((int64_t)ad * N + pt * G::TP) * R;
+      b_elements<kPart>(base, rows, k + quarter * 8, R, b);
+    };
+#pragma unroll
+    for (int i0 = 0; i0 < G::FP; i0 += kPart) {
+      u32x4 kept[kKeep ? G::FQ : 1][kParts];
+#pragma unroll
+      for (int j = 0; j < G::FQ; ++j) {
+        if constexpr (kKeep) load_low(j, kept[j]);
+        pending[j] = __ballot(id[j] >= 0 && id[j] < a.adapters);
+      }
+      int ad = next_mine();
+      u32x4 b[kPart];
+      if (ad >= 0) load_b(ad, i0, b);
+      while (ad >= 0) {
+        __builtin_amdgcn_sched_barrier(0);
+        const int after = next_mine();
+        u32x4 ahead[kPart];
+        load_b(max(after, 0), i0, ahead);
+#pragma unroll
+        for (int j = 0; j < G::FQ; ++j) {
+          if (!__ballot(id[j] == ad)) continue;
+          u32x4 part[kParts];
+          if constexpr (kKeep) {
+#pragma unroll
+            for (int pl = 0; pl < kParts; ++pl) part[pl] = kept[j][pl];
+          } else {
+            load_low(j, part);
+          }
+#pragma unroll
+          for (int i = 0; i < kPart; ++i) {
+            f32x4 sum = {0, 0, 0, 0};
+            u32x4 v[2] = {b[i], {}};
+            if constexpr (std::is_same<T, F16>::value) split_f16(b[i], &v[0], &v[1]);
+#pragma unroll
+            for (int pl = 0; pl < kParts; ++pl) {
+              sum = BF16::mfma(v[0], part[pl], sum);
+              if constexpr (std::is_same<T, F16>::value) sum = BF16::mfma(v[1], part[pl], sum);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              acc[i0 + i][j][e] = id[j] == ad ? acc[i0 + i][j][e] + sum[e] : acc[i0 + i][j][e];
+          }
+        }
+        ad = after;
+#pragma unroll
+        for (int i = 0; i < kPart; ++i) b[i] = ahead[i];
+      }
+    }
+  }
+}
+
 template <class G>
 __global__ void __launch_bounds__(G::kThreads, G::kThreads / 256) adapter_kernel(AdapterKArgs a) {
   typedef typename G::T T;
@@ -217,69 +318,11 @@ __global__ void __launch_bounds__(G::kThreads, G::kThreads / 256) adapter_kernel
   G::begin((MOE_EP_LDS char*)lds, sp, sq, a.k);
   typename G::Acc acc;
   G::clear(acc);
+  G::loop((MOE_EP_LDS char*)lds, sp, sq, a.k, acc);
+  add_adapters<G>(a, pt, qt, acc);
+  if (!G::join((MOE_EP_LDS char*)lds, acc)) return;
 
-  const int lane = threadIdx.x & 63, quarter = lane >> 4;
-  const int N = a.w.rows, R = a.rank;
-  if (G::wave_k() == 0) {
-    int id[G::FQ];
-    const uint16_t* low[G::FQ];
-#pragma unroll
-    for (int j = 0; j < G::FQ; ++j) {
-      const int q = qt * G::TQ + G::wave_q() + j * 16 + (lane & 15);
-      id[j] = q < a.x.rows ? a.ids[q] : -1;
-      low[j] = static_cast<const uint16_t*>(a.low) + (int64_t)min(q, a.x.rows - 1) * a.low_stride + quarter * 8;
-    }
-    const int64_t plane = (int64_t)a.x.rows * a.low_stride;
-    uint64_t pending[G::FQ];
-#pragma unroll
-    for (int j = 0; j < G::FQ; ++j) pending[j] = __ballot(id[j] >= 0 && id[j] < a.adapters);
-    while (true) {
-      int ad = -1;
-#pragma unroll
-      for (int j = 0; j < G::FQ; ++j)
-        if (ad < 0 && pending[j]) ad = __builtin_amdgcn_readlane(id[j], __builtin_ctzll(pending[j]));
-      if (ad < 0) break;
-      uint64_t mine[G::FQ];
-#pragma unroll
-      for (int j = 0; j < G::FQ; ++j) {
-        mine[j] = __ballot(id[j] == ad);
-        pending[j] &= ~mine[j];
-      }
-      for (int k = 0; k < R; k += 32) {
-        u32x4 part[G::FQ][kParts], b[G::FP];
-        const uint16_t* rows[G::FP];
-#pragma unroll
-        for (int j = 0; j < G::FQ; ++j)
-#pragma unroll
-          for (int pl = 0; pl < kParts; ++pl) part[j][pl] = *reinterpret_cast<const u32x4*>(low[j] + pl * plane + k);
-#pragma unroll
-        for (int i = 0; i < G::FP; ++i) {
-          const int p = min(pt * G::TP + G::wave_p() + i * 16 + (lane & 15), N - 1);
-          rows[i] = a.b + ((int64_t)ad * N + p) * R;
-        }
-        b_elements<G::FP>(rows, k + quarter * 8, R, b);
-#pragma unroll
-        for (int j = 0; j < G::FQ; ++j) {
-          if (!mine[j]) continue;
-#pragma unroll
-          for (int i = 0; i < G::FP; ++i) {
-            f32x4 sum = {0, 0, 0, 0};
-            u32x4 v[2] = {b[i], {}};
-            if constexpr (std::is_same<T, F16>::value) split_f16(b[i], &v[0], &v[1]);
-#pragma unroll
-            for (int pl = 0; pl < kParts; ++pl) {
-              sum = BF16::mfma(v[0], part[j][pl], sum);
-              if constexpr (std::is_same<T, F16>::value) sum = BF16::mfma(v[1], part[j][pl], sum);
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][j][e] = id[j] == ad ? acc[i][j][e] + sum[e] : acc[i][j][e];
-          }
-        }
-      }
-    }
-  }
-
-  if (!G::run((MOE_EP_LDS char*)lds, sp, sq, a.k, acc)) return;
+  const int lane = threadIdx.x & 63, quarter = lane >> 4, N = a.w.rows;
 #pragma unroll
   for (int j = 0; j < G::FQ; ++j) {
     const int q = qt * G::TQ + G::wave_q() + j * 16 + (lane & 15);
@@ -311,9 +354,13 @@ hipError_t adapter_few(const AdapterKArgs& a, hipStream_t stream) {
 }
 template <class T, int BLOCK, bool FEW>
 hipError_t low(const AdapterKArgs& a, hipStream_t stream) {
-  const dim3 grid(tiles(a.x.rows, BLOCK), a.rank <= 16 ? 1 : tiles(a.rank, 64), FEW ? kLowSplits : 1);
-  if (a.rank <= 16) low_kernel<T, BLOCK, 1, FEW><<<grid, dim3(low_waves(1) * 64), 0, stream>>>(a);
-  else low_kernel<T, BLOCK, 4, FEW><<<grid, dim3(low_waves(4) * 64), 0, stream>>>(a);
+  // 64 of the rank to a workgroup read x once for four times 16, where there
+  // are workgroups enough all the same
+  const int blocks = tiles(a.x.rows, BLOCK), parts = FEW ? kLowSplits : 1;
+  if (a.rank > 32 && (int64_t)blocks * tiles(a.rank, 64) * parts >= 128)
+    low_kernel<T, BLOCK, 4, FEW><<<dim3(blocks, tiles(a.rank, 64), parts), dim3(kLowWaves * 64), 0, stream>>>(a);
+  else
+    low_kernel<T, BLOCK, 1, FEW><<<dim3(blocks, tiles(a.rank, 16), parts), dim3(kLowWaves * 64), 0, stream>>>(a);
   return hipGetLastError();
 }
 template <class T>
@@ -328,15 +375,18 @@ hipError_t adapter(const AdapterKArgs& a, hipStream_t stream) {
   if (n <= 32) return adapter_few<T, 2>(a, stream);
   if (n <= 64) return adapter_few<T, 4>(a, stream);
   const bool direct = a.w.whole && a.x.whole;
-  switch (tile_size(a.w.rows, a.x.rows, direct)) {
+  switch (tile_size(a.w.rows, a.x.rows, a.k, direct, true)) {
     case k256x256: return adapter_tiles<Gemm<T, true, true, false, 256, 256, 2, 4, 1, true>>(a, stream);
     case k256x128: return adapter_tiles<Gemm<T, true, true, false, 256, 128, 2, 4, 1, true>>(a, stream);
     case k128x128:
       return direct ? adapter_tiles<Gemm<T, true, true, false, 128, 128, 2, 2, 2, true>>(a, stream)
                     : adapter_tiles<Gemm<T, true, true, false, 128, 128, 2, 2, 2, false>>(a, stream);
-    default:
+    case k64x64:
       return direct ? adapter_tiles<Gemm<T, true, true, false, 64, 64, 2, 2, 4, true>>(a, stream)
                     : adapter_tiles<Gemm<T, true, true, false, 64, 64, 2, 2, 4, false>>(a, stream);
+    default:
+      return direct ? adapter_tiles<Gemm<T, true, true, false, 32, 32, 1, 1, 4, true>>(a, stream)
+                    : adapter_tiles<Gemm<T, true, true, false, 32, 32, 1, 1, 4, false>>(a, stream);
   }
 }
 

@@ -81,9 +81,9 @@ MatK operand(const void* p, int64_t stride, int32_t rows, int64_t side) {
   return m;
 }
 
-// Workspace of the gated product's gradients: [d][tops][factor].
+// Workspace of the gated product's gradients: [d][tops][factor][partial sums].
 struct GradSpace {
-  int64_t d_stride, tops, factor, total;
+  int64_t d_stride, tops, factor, partial, total;
 };
 
 int make_space(const moe_ep_gated_grad_args* a, GradSpace* s) {
@@ -96,7 +96,8 @@ int make_space(const moe_ep_gated_grad_args* a, GradSpace* s) {
   s->d_stride = up(2 * (int64_t)a->intermediate_size, 8);
   s->tops = up(a->num_rows * s->d_stride * 2, 256);
   s->factor = s->tops + (a->dtype == MOE_EP_F16 ? kTops * 4 : 0);
-  s->total = s->factor + 256;
+  s->partial = s->factor + 256;
+  s->total = s->partial + kPartialFloats * 4;
   return MOE_EP_OK;
 }
 
@@ -273,6 +274,7 @@ int moe_ep_gated_grad(const moe_ep_gated_grad_args* a, void* stream) {
   uint16_t* d = reinterpret_cast<uint16_t*>(ws);
   hipError_t e = hipSuccess;
   ProductKArgs k = {};
+  k.partial = reinterpret_cast<float*>(ws + s.partial);
   if (n > 0) {
     GatedGradKArgs g = {};
     g.dout = a->dout;

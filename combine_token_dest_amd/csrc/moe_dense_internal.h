@@ -56,8 +56,11 @@ struct ProductKArgs {
   uint16_t* out;
   int64_t out_stride;
   const float* factor;        // or NULL: 1
+  float* partial;             // kPartialFloats: sums over parts of k, where there are few results
   int32_t ptiles, qtiles;     // (set by the launcher)
+  int32_t parts;              // (set by the launcher)
 };
+constexpr int64_t kPartialFloats = 512 * 64 * 64;
 
 // d = [dgate, dup] of a gated product, times a power of two for float16.
 struct GatedGradKArgs {

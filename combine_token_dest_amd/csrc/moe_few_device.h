@@ -78,11 +78,11 @@ struct Few {
 #pragma unroll
     for (int s = 0; s < kSets; ++s)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (have >= 8) st.v[s][h] = load_any8(p[s][h] + at);
-        else if (have > 0) st.v[s][h] = keep_last(load_any8(p[s][h] + at + (have - 8)), have);
-        else st.v[s][h] = u32x4{0, 0, 0, 0};
-      }
+      for (int h = 0; h < 2; ++h) st.v[s][h] = load_any8(p[s][h] + at + (min(have, 8) - 8));
+#pragma unroll
+    for (int s = 0; s < kSets; ++s)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) st.v[s][h] = keep_last(st.v[s][h], have);
   }
   // (A wave's LDS accesses take their turn, so the next step's writes come
   // after this one's reads.)

@@ -43,7 +43,8 @@ __global__ void __launch_bounds__(G::kThreads, G::kThreads / 256) gated_kernel(G
   G::begin((MOE_EP_LDS char*)lds, sp, sq, a.hidden);
   typename G::Acc acc;
   G::clear(acc);
-  if (!G::run((MOE_EP_LDS char*)lds, sp, sq, a.hidden, acc)) return;
+  G::loop((MOE_EP_LDS char*)lds, sp, sq, a.hidden, acc);
+  if (!G::join((MOE_EP_LDS char*)lds, acc)) return;
   const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int j = 0; j < G::FQ; ++j) {
@@ -112,7 +113,9 @@ __global__ void __launch_bounds__(WAVES * 64) gated_few_kernel(GatedKArgs a) {
   }
 }
 
-template <class G>
+// PARTS: a workgroup of a few results' tiles takes one of a.parts parts of k
+// (blockIdx.y, in whole tiles of k) and leaves float32 sums for sum_kernel.
+template <class G, bool PARTS>
 __global__ void __launch_bounds__(G::kThreads, G::kThreads / 256) product_kernel(ProductKArgs a) {
   typedef typename G::T T;
   __shared__ __attribute__((aligned(1024))) char lds[G::kLds];
@@ -122,11 +125,20 @@ __global__ void __launch_bounds__(G::kThreads, G::kThreads / 256) product_kernel
   typename G::SideQ sq;
   sp.aim(a.p, pt * G::TP);
   sq.aim(a.q, qt * G::TQ);
-  G::begin((MOE_EP_LDS char*)lds, sp, sq, a.k);
+  int k = a.k;
+  if constexpr (PARTS) {
+    const int steps = (a.k + G::kK - 1) / G::kK;
+    const int first = (int)((int64_t)steps * blockIdx.y / a.parts), last = (int)((int64_t)steps * (blockIdx.y + 1) / a.parts);
+    sp.skip(first);
+    sq.skip(first);
+    k = min(a.k, last * G::kK) - first * G::kK;
+  }
+  G::begin((MOE_EP_LDS char*)lds, sp, sq, k);
   typename G::Acc acc;
   G::clear(acc);
-  if (!G::run((MOE_EP_LDS char*)lds, sp, sq, a.k, acc)) return;
-  const float factor = a.factor ? *a.factor : 1.0f;
+  G::loop((MOE_EP_LDS char*)lds, sp, sq, k, acc);
+  if (!G::join((MOE_EP_LDS char*)lds, acc)) return;
+  const float factor = !PARTS && a.factor ? *a.factor : 1.0f;
   const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int j = 0; j < G::FQ; ++j) {
@@ -138,8 +150,24 @@ __global__ void __launch_bounds__(G::kThreads, G::kThreads / 256) product_kernel
       float v[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = acc[i][j][e] * factor;
-      store4<T>(a.out, q * a.out_stride + c, false, a.p.rows - c, v);
+      if constexpr (PARTS)
+        store4<T>(a.partial, ((int64_t)blockIdx.y * a.q_rows + q) * a.p.rows + c, true, a.p.rows - c, v);
+      else
+        store4<T>(a.out, q * a.out_stride + c, false, a.p.rows - c, v);
     }
+  }
+}
+
+// out = *factor * the parts' sums, added in turn.
+template <class T>
+__global__ void __launch_bounds__(256) sum_kernel(ProductKArgs a) {
+  const int64_t total = (int64_t)a.q_rows * a.p.rows;
+  const float factor = a.factor ? *a.factor : 1.0f;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    float v = 0;
+    for (int part = 0; part < a.parts; ++part) v += a.partial[part * total + i];
+    const int64_t q = i / a.p.rows;
+    a.out[q * a.out_stride + (i - q * a.p.rows)] = T::from_float(v * factor);
   }
 }
 
@@ -293,15 +321,18 @@ hipError_t gated(const GatedKArgs& a, hipStream_t stream) {
   if (a.x.rows <= 16) return gated_few<T, 1>(a, stream);
   if (a.x.rows <= 32) return gated_few<T, 2>(a, stream);
   const bool direct = a.w.whole && a.x.whole;
-  switch (tile_size(2 * (int64_t)a.inter, a.x.rows, direct)) {
+  switch (tile_size(2 * (int64_t)a.inter, a.x.rows, a.hidden, direct, true)) {
     case k256x256: return gated_tiles<Gemm<T, true, true, true, 256, 256, 2, 4, 1, true>>(a, stream);
     case k256x128: return gated_tiles<Gemm<T, true, true, true, 256, 128, 2, 4, 1, true>>(a, stream);
     case k128x128:
       return direct ? gated_tiles<Gemm<T, true, true, true, 128, 128, 2, 2, 2, true>>(a, stream)
                     : gated_tiles<Gemm<T, true, true, true, 128, 128, 2, 2, 2, false>>(a, stream);
-    default:
+    case k64x64:
       return direct ? gated_tiles<Gemm<T, true, true, true, 64, 64, 2, 2, 4, true>>(a, stream)
                     : gated_tiles<Gemm<T, true, true, true, 64, 64, 2, 2, 4, false>>(a, stream);
+    default:
+      return direct ? gated_tiles<Gemm<T, true, true, true, 32, 32, 1, 1, 4, true>>(a, stream)
+                    : gated_tiles<Gemm<T, true, true, true, 32, 32, 1, 1, 4, false>>(a, stream);
   }
 }
 
@@ -309,13 +340,27 @@ template <class G>
 hipError_t product_tiles(ProductKArgs a, hipStream_t stream) {
   a.ptiles = tiles(a.p.rows, G::TP);
   a.qtiles = tiles(a.q_rows, G::TQ);
-  product_kernel<G><<<dim3(a.ptiles * a.qtiles), dim3(G::kThreads), 0, stream>>>(a);
+  const int count = a.ptiles * a.qtiles;
+  if constexpr (G::TP == 64) {
+    // A few results of many k (weights' gradients of small layers, a few rows'
+    // gradients): parts of k, two tiles of it at least, for all CUs.
+    const int64_t results = (int64_t)a.p.rows * a.q_rows;
+    a.parts = (int)std::min<int64_t>({8, 256 / count, a.k / (2 * G::kK), kPartialFloats / results});
+    if (a.parts > 1) {
+      product_kernel<G, true><<<dim3(count, a.parts), dim3(G::kThreads), 0, stream>>>(a);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      sum_kernel<typename G::T><<<dim3((int)std::min<int64_t>((results + 255) / 256, 2048)), dim3(256), 0, stream>>>(a);
+      return hipGetLastError();
+    }
+  }
+  product_kernel<G, false><<<dim3(count), dim3(G::kThreads), 0, stream>>>(a);
   return hipGetLastError();
 }
 template <class T, bool QKC>
 hipError_t product(const ProductKArgs& a, hipStream_t stream) {
   const bool direct = a.p.whole && a.q.whole;
-  switch (tile_size(a.p.rows, a.q_rows, direct)) {
+  switch (tile_size(a.p.rows, a.q_rows, a.k, direct, false)) {
     case k256x256: return product_tiles<Gemm<T, false, QKC, false, 256, 256, 2, 4, 1, true>>(a, stream);
     case k256x128: return product_tiles<Gemm<T, false, QKC, false, 256, 128, 2, 4, 1, true>>(a, stream);
     case k128x128:

@@ -58,13 +58,14 @@ __device__ __forceinline__ u32x4 load_any8(const void* p) {
   return reinterpret_cast<const MOE_EP_GLOBAL AnyHalf8*>(reinterpret_cast<uintptr_t>(p))->v;
 }
 
-// Eight elements of which only the last `have` (1..7) of v exist: those, then zeros.
+// Eight elements of which only the last `have` (none: <= 0; all: >= 8) of v
+// exist: those, then zeros.
 __device__ __forceinline__ u32x4 keep_last(const u32x4& v, int have) {
   typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
   const u64x2 w = __builtin_bit_cast(u64x2, v);
-  const int gone = 16 * (8 - have);
+  const int gone = 16 * (8 - max(min(have, 8), 0));
   u64x2 r;
-  r[0] = gone < 64 ? w[0] >> gone | w[1] << (64 - gone) : w[1] >> (gone - 64);
+  r[0] = gone == 0 ? w[0] : gone < 64 ? w[0] >> gone | w[1] << (64 - gone) : gone < 128 ? w[1] >> (gone - 64) : 0;
   r[1] = gone < 64 ? w[1] >> gone : 0;
   return __builtin_bit_cast(u32x4, r);
 }
@@ -150,6 +151,16 @@ struct Side {
     }
   }
 
+  // Past the first `count` tiles of k.
+  __device__ __forceinline__ void skip(int count) {
+    if constexpr (DIRECT) {
+      base += count * step;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) src[i] += count * step;
+    }
+  }
+
   __device__ __forceinline__ void load(MOE_EP_LDS char* __restrict__ dst) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 #pragma unroll
@@ -160,18 +171,27 @@ struct Side {
     next();
   }
 
-  // The tile whose first k has `left` after it (and with it), through registers.
+  // The tile whose first k has `left` (at least 1) after it (and with it),
+  // through registers.  At an edge a unit that ends past it is loaded so as to
+  // end there, and moved: with a branch for each unit its load would wait for
+  // the one before.
   __device__ __forceinline__ void fetch(u32x4 (&v)[kLoads], int left) {
+    if (left >= K && (KC || first + T <= rows)) {
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int have = KC ? left - along(i) : (lds_row(i) < left ? rows - (first + along(i)) : 0);
-      if (have >= 8) {
-        v[i] = load_any8(address(i));
-      } else if (!DIRECT && have > 0) {
-        v[i] = keep_last(load_any8(address(i) + (have - 8) * 2), have);
-      } else {
-        v[i] = u32x4{0, 0, 0, 0};
+      for (int i = 0; i < kLoads; ++i) v[i] = load_any8(address(i));
+    } else {
+      int have[kLoads];
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        have[i] = (KC ? left : rows - first) - along(i);
+        int64_t back = (int64_t)(min(have[i], 8) - 8) * 2;
+        // DIRECT: units past the last row's are loaded from it already
+        if (!KC && DIRECT) back = 0;
+        if (!KC) back -= max(lds_row(i) - (left - 1), 0) * (step / K);
+        v[i] = load_any8(address(i) + back);
       }
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) v[i] = keep_last(v[i], KC || lds_row(i) < left ? have[i] : 0);
     }
     next();
   }
@@ -252,6 +272,18 @@ struct Gemm {
     __builtin_amdgcn_sched_barrier(0);
   }
 
+  // The same where nothing is loaded to LDS: loads to registers stay under way.
+  static __device__ __forceinline__ void meet_lds() {
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_waitcnt(0xC07F);                   // lgkmcnt(0)
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
   static __device__ __forceinline__ void load(MOE_EP_LDS char* __restrict__ dst, SideP& sp, SideQ& sq) {
     sp.load(dst);
     sq.load(dst + SideP::kBytes);
@@ -267,30 +299,42 @@ struct Gemm {
     SideQ::put(dst + SideP::kBytes, v);
   }
 
+  // What a wave holds of a tile on its way through registers.
+  struct Held {
+    u32x4 p[DIRECT ? 1 : SideP::kLoads], q[DIRECT ? 1 : SideQ::kLoads];
+  };
+  static __device__ __forceinline__ void fetch(Held& h, SideP& sp, SideQ& sq, int left) {
+    if constexpr (!DIRECT) {
+      if (left > 0) {
+        sp.fetch(h.p, left);
+        sq.fetch(h.q, left);
+      }
+    }
+  }
+
   // One tile of k at `cur`, its first 32 k already in the fragments; leaves
   // the first of the tile at `nxt` there.  `left`: of k from the tile after
   // that one on, which goes to `dst`: cur's place, when all waves have read
-  // it.  Places of their own for the compiler, which would wait for the loads
-  // to LDS before each read otherwise; what orders them is meet().
+  // it (through registers, it was fetched a step ago, and the one behind it is
+  // now).  Places of their own for the compiler, which would wait for the
+  // loads to LDS before each read otherwise; what orders them is meet().
   static __device__ __forceinline__ void step(const MOE_EP_LDS char* __restrict__ cur,
                                               const MOE_EP_LDS char* __restrict__ nxt, MOE_EP_LDS char* __restrict__ dst,
-                                              SideP& sp, SideQ& sq, FragsP& p, FragsQ& q, Acc& acc, int left) {
-    u32x4 vp[DIRECT ? 1 : SideP::kLoads], vq[DIRECT ? 1 : SideQ::kLoads];
-    if constexpr (!DIRECT) {
-      if (left > 0) {
-        sp.fetch(vp, left);
-        sq.fetch(vq, left);
-      }
-    }
+                                              SideP& sp, SideQ& sq, FragsP& p, FragsQ& q, Acc& acc, Held& held,
+                                              int left) {
     frags(cur, p, q, 1);
     products(p, q, 0, acc);
-    meet();
     if constexpr (DIRECT) {
+      meet();
       if (left >= kK) load(dst, sp, sq);
       else if (left > 0) fill(dst, sp, sq, left);
-    } else if (left > 0) {
-      SideP::put(dst, vp);
-      SideQ::put(dst + SideP::kBytes, vq);
+    } else {
+      meet_lds();
+      if (left > 0) {
+        SideP::put(dst, held.p);
+        SideQ::put(dst + SideP::kBytes, held.q);
+        fetch(held, sp, sq, left - kK);
+      }
     }
     __builtin_amdgcn_sched_barrier(0);
     frags(nxt, p, q, 0);
@@ -314,10 +358,11 @@ struct Gemm {
       else if (left > 0) fill(lds + b * kBuffer, sp, sq, left);
     }
   }
-  // After begin(): adds the products over all K to acc.  The sums are in the
-  // waves with wave_k() 0; the others return false.
-  static __device__ __forceinline__ bool run(MOE_EP_LDS char* lds, SideP& sp, SideQ& sq, int K, Acc& acc) {
-    if (K <= 0) return wave_k() == 0;
+  // After begin(): adds the wave's products over its share of K to acc.
+  static __device__ __forceinline__ void loop(MOE_EP_LDS char* lds, SideP& sp, SideQ& sq, int K, Acc& acc) {
+    if (K <= 0) return;
+    Held held;
+    fetch(held, sp, sq, K - 2 * kK);
     meet();
     FragsP p;
     FragsQ q;
@@ -326,9 +371,13 @@ struct Gemm {
 #pragma unroll 1
     for (int left = K; left > 0; left -= kK) {
       // (past the last tile nxt is read for nothing, inside lds)
-      step(lds + cur, lds + (kBuffer - cur), lds + cur, sp, sq, p, q, acc, left - 2 * kK);
+      step(lds + cur, lds + (kBuffer - cur), lds + cur, sp, sq, p, q, acc, held, left - 2 * kK);
       cur = kBuffer - cur;
     }
+  }
+  // Adds the sums of the waves that share k.  They are in the waves with
+  // wave_k() 0; the others return false.
+  static __device__ __forceinline__ bool join(MOE_EP_LDS char* lds, Acc& acc) {
     if constexpr (WK > 1) {
       meet();
       const int lane = threadIdx.x & 63, w = wave() % (WP * WQ);
@@ -403,34 +452,43 @@ __device__ __forceinline__ void store4(void* out, int64_t at, bool f32, int have
 
 constexpr int tiles(int64_t rows, int tile) { return (int)((rows + tile - 1) / tile); }
 
-// The tiles for P x Q results.  Larger ones move less for each product, but
-// the card's 256 CUs, one tile each at a time, go through them in rounds.  A
-// round takes, for 64 k: 1.6 us with tiles of 256 x 256, 1.0 of 256 x 128 (1.15
-// where several rounds crowd the caches), 0.57 of 128 x 128, 0.28 of 64 x 64; a
-// last round that is not full leaves power to those that work.  Measured,
-// gated products of rows x 4096 (k 7168), us with each:
+// The tiles for P x Q results of k products.  Larger ones move less for each
+// product, but the card's 256 CUs, one tile each at a time, go through them in
+// rounds.  A round takes, for 64 k: 1.6 us with tiles of 256 x 256, 1.0 of
+// 256 x 128 (1.15 where several rounds crowd the caches), 0.57 of 128 x 128,
+// 0.28 of 64 x 64, 0.15 of 32 x 32; and some us to begin and to store.  A last
+// round that is not full leaves power to those of the largest tiles that work.
+// Measured, gated products of rows x
+// 4096 (k 7168), us with each:
 //   rows        128   256   512  1024  2048  4096  8192
 //   256 x 256   149   154   153   153   154   189   385
 //   256 x 128    99    99    98    98   113   276   518
 //   128 x 128    58    58    58    64   127   309   576
 //    64 x 64     30    31    61   121   240   515  1056
-enum TileSize { k256x256, k256x128, k128x128, k64x64 };
-inline TileSize tile_size(int64_t P, int64_t Q, bool direct) {
+// k32x32: only where asked for (`narrow`: both operands with k side by side).
+enum TileSize { k256x256, k256x128, k128x128, k64x64, k32x32 };
+inline TileSize tile_size(int64_t P, int64_t Q, int64_t k, bool direct, bool narrow) {
   constexpr struct {
     TileSize size;
     int p, q;
     double one, more;         // us of a round for 64 k: the only one, or one of several
-  } kinds[] = {{k256x256, 256, 256, 1.6, 1.6}, {k256x128, 256, 128, 1.0, 1.15}, {k128x128, 128, 128, 0.57, 0.57},
-               {k64x64, 64, 64, 0.28, 0.28}};
+    double ends;              // us of a round beside
+  } kinds[] = {{k256x256, 256, 256, 1.6, 1.6, 8},
+               {k256x128, 256, 128, 1.0, 1.15, 6},
+               {k128x128, 128, 128, 0.57, 0.57, 4},
+               {k64x64, 64, 64, 0.28, 0.28, 3},
+               {k32x32, 32, 32, 0.15, 0.12, 3}};
   TileSize best = k64x64;
   double least = 1e300;
-  for (const auto& k : kinds) {
-    if (!direct && k.p > 128) continue;                   // through registers there are the two smaller ones
-    const double r = (double)((P + k.p - 1) / k.p) * (double)((Q + k.q - 1) / k.q) / 256;
-    const double time = r <= 1 ? k.one : k.more * (r + std::ceil(r)) / 2;
+  for (const auto& t : kinds) {
+    if (t.p == 256 && !direct) continue;                  // through registers there are only smaller ones
+    if (t.p == 32 && !narrow) continue;
+    const double r = (double)((P + t.p - 1) / t.p) * (double)((Q + t.q - 1) / t.q) / 256;
+    const double rounds = t.size == k256x256 ? (r + std::ceil(r)) / 2 : std::ceil(r);
+    const double time = r <= 1 ? t.one * k / 64 + t.ends : (t.more * k / 64 + t.ends) * rounds;
     if (time < least) {
       least = time;
-      best = k.size;
+      best = t.size;
     }
   }
   return best;

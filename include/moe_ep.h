@@ -575,7 +575,7 @@ typedef struct moe_ep_gated_grad_args {
 
 /* Bytes of device workspace moe_ep_gated_grad needs for these sizes (the
  * sizes and dtype are read; pointers are not followed): 4 for each element
- * of dout. */
+ * of dout, and 8 MiB. */
 MOE_EP_API int moe_ep_gated_grad_workspace_bytes(const moe_ep_gated_grad_args* args, size_t* out_bytes);
 
 /* The gradients of moe_ep_gated's inputs:
@@ -585,9 +585,9 @@ MOE_EP_API int moe_ep_gated_grad_workspace_bytes(const moe_ep_gated_grad_args* a
  * du are rounded once to dtype, float16 ones after a multiplication with a
  * power of two that brings the largest finite one to 2^14..2^15, so that none
  * overflows.  x is read for dgate_up only and gate_up for dx only; the other
- * may be NULL.  One kernel launch (float16: two) and one for each gradient.
- * Outputs must not overlap inputs or one another.  The workspace holds
- * nothing between calls; calls that may overlap in time need one each. */
+ * may be NULL.  One kernel launch (float16: two) and one or two for each
+ * gradient.  Outputs must not overlap inputs or one another.  The workspace
+ * holds nothing between calls; calls that may overlap in time need one each. */
 MOE_EP_API int moe_ep_gated_grad(const moe_ep_gated_grad_args* args, void* stream);
 
 typedef struct moe_ep_adapter_args {
