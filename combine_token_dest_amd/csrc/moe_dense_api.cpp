@@ -63,10 +63,11 @@ int check_workspace(const void* p, size_t have, size_t need) {
   return MOE_EP_OK;
 }
 
-// Tiles of a product are numbered in 32 bits, the smallest of them 64 x 64.
+// A launch has fewer than 2^32 threads: 512 for each tile of 128 x 128 results
+// (smaller ones are for fewer results).
 int check_tiles(int64_t rows, int64_t cols) {
-  if ((rows + 63) / 64 * ((cols + 63) / 64) > INT32_MAX)
-    return report(MOE_EP_ERR_INVALID_ARG, "%lld x %lld results are more than 2^31 tiles", (long long)rows,
+  if ((rows + 127) / 128 * ((cols + 127) / 128) >= 1 << 23)
+    return report(MOE_EP_ERR_INVALID_ARG, "%lld x %lld results are 2^23 tiles of 128 x 128 or more", (long long)rows,
                   (long long)cols);
   return MOE_EP_OK;
 }
@@ -101,8 +102,12 @@ int make_space(const moe_ep_gated_grad_args* a, GradSpace* s) {
   return MOE_EP_OK;
 }
 
+// Rows of an adapter_linear call: its first kernel has 64 threads for each.
+constexpr int32_t kMaxAdapterRows = 1 << 25;
+
 int check_adapter_sizes(const moe_ep_adapter_args* a) {
-  if (a->num_rows < 0) return report(MOE_EP_ERR_INVALID_ARG, "num_rows %d < 0", a->num_rows);
+  if (a->num_rows < 0 || a->num_rows > kMaxAdapterRows)
+    return report(MOE_EP_ERR_INVALID_ARG, "num_rows %d outside [0, %d]", a->num_rows, kMaxAdapterRows);
   if (a->num_adapters < 1 || a->num_adapters > MOE_EP_MAX_EXPERTS)
     return report(MOE_EP_ERR_INVALID_ARG, "num_adapters %d outside [1, %d]", a->num_adapters, MOE_EP_MAX_EXPERTS);
   if (a->rank < 1 || a->rank > MOE_EP_MAX_RANK)

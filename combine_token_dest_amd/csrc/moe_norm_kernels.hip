@@ -302,23 +302,36 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormKArgs a) {
 }
 
 template <class T, class W, bool EIGHT>
-hipError_t launch(const NormKArgs& a, hipStream_t stream) {
+hipError_t launch(const NormKArgs& all, hipStream_t stream) {
   // Two vectors of a row to a thread where there are rows enough to hide each
   // other's latency (4096 rows of 7168 to 8 bits: 56 us with one, 47 with two,
   // 51 with four; 8192 of 4096 in 16 bits: 49, 51 and 54); one for few rows,
   // and four, or none held, where a workgroup has no more threads.
-  const int vectors = (a.hidden + 7) / 8;
-  int vpt = a.n >= 512 ? 2 : 1;
+  const int vectors = (all.hidden + 7) / 8;
+  int vpt = all.n >= 512 ? 2 : 1;
   while (vpt < 4 && vectors > 1024 * vpt) vpt *= 2;
   int threads = std::min((vectors + vpt - 1) / vpt, 1024);
   threads = (threads + 63) / 64 * 64;
   vpt = (vectors + threads - 1) / threads;
-  const dim3 grid(a.n), block(threads);
-  if (vpt <= 1) norm_kernel<T, W, EIGHT, 1><<<grid, block, 0, stream>>>(a);
-  else if (vpt <= 2) norm_kernel<T, W, EIGHT, 2><<<grid, block, 0, stream>>>(a);
-  else if (vpt <= 4) norm_kernel<T, W, EIGHT, 4><<<grid, block, 0, stream>>>(a);
-  else norm_kernel<T, W, EIGHT, 0><<<grid, block, 0, stream>>>(a);
-  return hipGetLastError();
+  // A launch has fewer than 2^32 threads.
+  const int64_t most = ((int64_t)1 << 31) / threads;
+  for (int64_t r = 0; r < all.n; r += most) {
+    NormKArgs a = all;
+    a.n = (int32_t)std::min<int64_t>(most, all.n - r);
+    a.x += r * a.x_stride;
+    if (a.residual) a.residual += r * a.residual_stride;
+    a.out = static_cast<uint8_t*>(a.out) + r * a.out_stride * (EIGHT ? 1 : 2);
+    if (a.scales) a.scales += r * a.scales_stride;
+    if (a.residual_out) a.residual_out += r * a.residual_out_stride;
+    const dim3 grid(a.n), block(threads);
+    if (vpt <= 1) norm_kernel<T, W, EIGHT, 1><<<grid, block, 0, stream>>>(a);
+    else if (vpt <= 2) norm_kernel<T, W, EIGHT, 2><<<grid, block, 0, stream>>>(a);
+    else if (vpt <= 4) norm_kernel<T, W, EIGHT, 4><<<grid, block, 0, stream>>>(a);
+    else norm_kernel<T, W, EIGHT, 0><<<grid, block, 0, stream>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <class T>

@@ -525,7 +525,8 @@ typedef struct moe_ep_norm_args {
  * rows and scales are what dispatch forwards as hidden and scale rows.  out
  * and residual_out may each be x or residual itself (same address, stride
  * and element size); otherwise no output may overlap an input or another
- * output, each taken from its first element to its last.  One kernel launch. */
+ * output, each taken from its first element to its last.  One kernel launch,
+ * and one more for each 2^21 rows after the first. */
 MOE_EP_API int moe_ep_rms_norm(const moe_ep_norm_args* args, void* stream);
 
 typedef struct moe_ep_gated_args {
@@ -546,7 +547,9 @@ typedef struct moe_ep_gated_args {
 /* The first half of a gated feed-forward, whose weights lie as moe_ep_layer's
  * gate_up of one expert:
  *   g = gate_up[:I] x, u = gate_up[I:] x, out = silu(g) * u = g / (1 + exp(-g)) * u
- * in one kernel launch; g and u stay float32 until out is rounded.  With pre
+ * in one kernel launch; g and u stay float32 until out is rounded.  Results of
+ * 2^23 or more tiles of 128 x 128 (of gate and up) are refused, there and in
+ * the two functions below.  With pre
  * they are kept for moe_ep_gated_grad as they are, g in the first I columns
  * and u in the others.  Outputs must not overlap inputs or one another, each
  * taken from its first element to its last. */
@@ -605,7 +608,7 @@ typedef struct moe_ep_adapter_args {
   size_t workspace_bytes;
   int32_t dtype;                  /* MOE_EP_BF16 or MOE_EP_F16 */
   int32_t out_dtype;              /* dtype, or MOE_EP_F32 */
-  int32_t num_rows;
+  int32_t num_rows;               /* 0..2^25 */
   int32_t in_features;            /* 8..2^22 */
   int32_t out_features;           /* 1..2^22 */
   int32_t num_adapters;           /* 1..MOE_EP_MAX_EXPERTS */

@@ -215,7 +215,9 @@ def test_gated_grad_workspace():
 
 
 @pytest.mark.parametrize("kw", [
-    dict(dtype=0), dict(out_dtype=2), dict(num_rows=-1), dict(in_features=7), dict(in_features=SIDE),
+    dict(dtype=0), dict(out_dtype=2), dict(num_rows=-1), dict(num_rows=(1 << 25) + 1, workspace_bytes=1 << 40),
+    dict(num_rows=1 << 25, out_features=1 << 14, out_stride=1 << 14, workspace_bytes=1 << 40),
+    dict(in_features=7), dict(in_features=SIDE),
     dict(out_features=0), dict(out_features=SIDE), dict(num_adapters=0), dict(num_adapters=1025), dict(rank=0),
     dict(rank=1025), dict(x=None), dict(x_stride=63), dict(weight=None), dict(weight_stride=63), dict(lora_a=None),
     dict(lora_b=None), dict(adapter_ids=None), dict(out=None), dict(out_stride=31), dict(workspace=None),

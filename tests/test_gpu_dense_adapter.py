@@ -160,6 +160,37 @@ def test_streams_and_graph(n):
         torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("n", [40, 300])
+def test_two_streams_at_once(n):
+    sets = [make(n, 264, 136, 5, 16, BF16, seed=40 * i) for i in range(2)]
+    dev = [[t.cuda() for t in s] for s in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        for d, st in zip(dev, streams):
+            with torch.cuda.stream(st):
+                got.append(adapter_linear(*d[:5], scales=d[5]))
+    torch.cuda.synchronize()
+    for i, y in enumerate(got):
+        check(y, *sets[i % 2])
+
+
+@pytest.mark.parametrize("n,N,K", [(300, 264, 1000), (700, 500, 264), (2300, 4096, 64), (2048, 2050, 72)])
+@pytest.mark.parametrize("R", [3, 16, 72])
+def test_an_adapter_of_each_rows_own(n, N, K, R):
+    """As many adapters in a tile as there are, at every size of tiles."""
+    x, w, a, b, ids, scales = make(n, N, K, 40, R, BF16)
+    check(run(x, w, a, b, ids, scales), x, w, a, b, ids, scales)
+
+
+def test_same_bits_each_time():
+    t = [v.cuda() for v in make(200, 264, 1032, 8, 16, BF16)]
+    y = adapter_linear(*t[:5], scales=t[5])
+    for _ in range(3):
+        assert torch.equal(adapter_linear(*t[:5], scales=t[5]), y)
+
+
 @pytest.mark.parametrize("n", [2, 9, 300])
 def test_a_block(n):
     """Norm, gated product and an adapted projection one after another, each

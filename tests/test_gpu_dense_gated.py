@@ -235,6 +235,59 @@ def test_streams_and_graph(n):
         torch.cuda.synchronize()
 
 
+def test_no_second_derivatives():
+    x, w, dh = (t.cuda().requires_grad_() for t in make(8, 64, 16, BF16))
+    dx, = torch.autograd.grad(gated_linear(x, w), x, dh, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        dx.float().sum().backward()
+
+
+def test_weights_changed_before_the_backward_pass_are_noticed():
+    x, w, dh = (t.cuda() for t in make(8, 64, 16, BF16))
+    w.requires_grad_()
+    h = gated_linear(x, w)
+    with torch.no_grad():
+        w.add_(1)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        torch.autograd.grad(h, w, dh)
+
+
+def test_inference_mode_and_leaves_through_a_module():
+    """A down projection by torch behind it, gradients into .grad."""
+    x, w, _ = make(20, 64, 24, BF16)
+    down = rand(9, 64, 24)
+    gx, gw, gd = (t.cuda().requires_grad_() for t in (x, w, down))
+    with torch.inference_mode():
+        check_forward(gated_linear(gx, gw), x, w)
+    (gated_linear(gx, gw).float() @ gd.float().t()).sum().backward()
+    dh = down.double().sum(0, keepdim=True).expand(20, 24)
+    want = ref.gated_grad(x, w, dh, BF16)
+    # the gradient of h arrives as bfloat16 of a float32 sum: one rounding more of each term
+    more = 2.0 ** -8
+    _, _, _, tg, tu, _ = ref.gated(x, w)
+    d = torch.cat((dh.abs(), dh.abs()), 1) * 2 * (ref.gated(x, w)[1].abs().repeat(1, 2) + ref.gated(x, w)[0].abs().repeat(1, 2))
+    close(gx.grad, want[0], want[1] + more * d @ w.double().abs())
+    close(gw.grad, want[2], want[3] + more * d.t() @ x.double().abs())
+
+
+def test_two_streams_at_once():
+    sets = [make(90, 264, 72, BF16, seed=30 * i) for i in range(2)]
+    dev = [[t.cuda() for t in s] for s in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        for (x, w, dh), st in zip(dev, streams):
+            with torch.cuda.stream(st):
+                a, b = x.detach().requires_grad_(), w.detach().requires_grad_()
+                h = gated_linear(a, b)
+                got.append((h.detach(), *torch.autograd.grad(h, (a, b), dh)))
+    torch.cuda.synchronize()
+    for i, (h, dx, dw) in enumerate(got):
+        check_forward(h, *sets[i % 2][:2])
+        check_grads(dx, dw, *sets[i % 2], BF16)
+
+
 def test_same_bits_each_time():
     x, w, dh = (t.cuda() for t in make(300, 520, 264, BF16))
     x.requires_grad_(), w.requires_grad_()

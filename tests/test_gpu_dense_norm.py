@@ -176,6 +176,19 @@ def test_past_32_bits():
     verify(rms_norm(rows, w.cuda(), out=rows), x, w, None)
 
 
+def test_more_rows_than_a_launch():
+    """2^25 rows are a launch's most at 64 threads each."""
+    n, H = (1 << 25) + 1000, 8
+    x = torch.empty(n, H, dtype=BF16, device="cuda").fill_(1.0)
+    w = rand(3, H)
+    at = torch.tensor([0, 1, 12345, (1 << 25) - 1, 1 << 25, (1 << 25) + 1, n - 1])
+    some = rand(4, len(at), H)
+    x[at.cuda()] = some.cuda()
+    r = rms_norm(x, w.cuda(), x, out_dtype=E4M3)
+    picked = type(r)(r.rows.view(torch.uint8)[at.cuda()].view(E4M3), r.scales[at.cuda()], r.residual[at.cuda()])
+    verify(picked, some, w, some, eight=True)
+
+
 def test_streams_and_graph():
     n, H = 64, 7168
     xs = [rand(i, n, H) for i in range(3)]
