@@ -113,13 +113,12 @@ def adapter(x, w, a, b, ids, scales, out_dtype):
     product whole; both products' sums are added in float32."""
     x = x.double()
     y, t = matmul(x, w.double())
-    for r, i in enumerate(ids.tolist()):
-        if not 0 <= i < a.shape[0]:
-            continue
+    for i in set(ids.tolist()) & set(range(a.shape[0])):
+        rows = ids == i
         s = 1.0 if scales is None else float(scales[i])
-        low, tl = matmul(x[r:r + 1], a[i].double())
+        low, tl = matmul(x[rows], a[i].double())
         tl = (tl + 2 * U * low.abs()) * abs(s)
         v, tv = matmul(low * s, b[i].double())
-        y[r] += v[0]
-        t[r] += (3 * tv + tl @ b[i].double().abs().t())[0] + 2 * U * (y[r].abs() + v[0].abs())
+        y[rows] += v
+        t[rows] += 3 * tv + tl @ b[i].double().abs().t() + 2 * U * (y[rows].abs() + v.abs())
     return y, rounded(y, t, out_dtype)

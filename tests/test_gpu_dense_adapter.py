@@ -55,6 +55,15 @@ def test_prompts_one_after_another(dtype):
     check(run(x, w, a, b, ids, None), x, w, a, b, ids, None)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("n,N,K", [(5578, 141, 330), (131, 5492, 328), (1314, 5896, 72), (520, 6573, 136),
+                                   (70, 90, 330), (65, 80, 520), (4226, 35, 333), (4232, 33, 328)])
+def test_every_kind_of_tile(n, N, K, dtype):
+    x, w, a, b, _, scales = make(n, N, K, 4, 20, dtype)
+    ids = (torch.arange(n) // 77 % 5 - 1).to(torch.int32)
+    check(run(x, w, a, b, ids, scales), x, w, a, b, ids, scales)
+
+
 def test_largest_tiles():
     x, w, a, b, _, scales = make(4100, 4096, 72, 4, 16, BF16)
     ids = (torch.arange(4100) // 333 % 5 - 1).to(torch.int32)

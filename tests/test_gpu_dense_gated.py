@@ -69,6 +69,21 @@ def test_largest_tiles(n, H, I):
     check_grads(*torch.autograd.grad(h, (gx, gw), dh.cuda()), x, w, dh, BF16)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("n,H,I", [
+    (5506, 265, 65), (134, 264, 2744), (1081, 136, 3592), (516, 200, 3336), (35, 333, 2234), (35, 328, 2112),
+    (132, 5682, 149), (134, 5456, 152), (5378, 1416, 40), (641, 5408, 72), (34, 68, 1301), (34, 64, 1304),
+    (1058, 70, 16), (300, 139, 2732), (300, 3592, 1090), (170, 6648, 264)])
+def test_every_kind_of_tile(n, H, I, dtype):
+    """Each size of tiles, aligned and not, whole and in parts of k, in each
+    of the three products."""
+    x, w, dh = make(n, H, I, dtype)
+    gx, gw = x.cuda().requires_grad_(), w.cuda().requires_grad_()
+    h = gated_linear(gx, gw)
+    check_forward(h.detach(), x, w)
+    check_grads(*torch.autograd.grad(h, (gx, gw), dh.cuda()), x, w, dh, dtype)
+
+
 @pytest.mark.parametrize("which", ["x", "gate_up"])
 def test_one_gradient_alone(which):
     x, w, dh = make(40, 96, 56, BF16)
