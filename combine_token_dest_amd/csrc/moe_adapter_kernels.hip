@@ -63,54 +63,47 @@ constexpr int kLowWaves = 8;
 // one by one; more are prompts, whose rows share adapters.
 constexpr int kLowSingle = 512;
 
-// The low values of BLOCK rows of x and 16 RT of the rank.
-template <class T, int BLOCK, int RT, bool FEW>
-__global__ void __launch_bounds__(kLowWaves * 64) low_kernel(AdapterKArgs a) {
-  typedef Few<T, RT, 1, kLowWaves> F;
-  static_assert(F::kLds >= RT * 1024, "the sums fit a wave's piece");
-  __shared__ __attribute__((aligned(1024))) char lds[kLowWaves * F::kLds];
-  f32x4 (*sums)[RT][16][4] = reinterpret_cast<f32x4 (*)[RT][16][4]>(lds);
+// One pass of low_kernel: M adapters' rows of A with the workgroup's rows of x.
+template <class T, int BLOCK, int RT, bool FEW, int M>
+__device__ __forceinline__ void low_pass(const AdapterKArgs& a, const int (&ad)[M], int id, char* lds) {
+  typedef Few<T, RT * M, 1, kLowWaves> F;
+  static_assert(F::kLds >= RT * M * 1024, "the sums fit a wave's piece");
+  f32x4 (*sums)[RT * M][16][4] = reinterpret_cast<f32x4 (*)[RT * M][16][4]>(lds);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, i = lane & 15;
   const int r0 = blockIdx.x * BLOCK, k0 = blockIdx.y * (16 * RT), split = blockIdx.z;
   const int R = a.rank, n = a.x.rows;
-  const int row = min(r0 + min(i, BLOCK - 1), n - 1);
-  // lanes of the same row name the same adapter; rows past the last none
-  int id = r0 + min(i, BLOCK - 1) < n ? a.ids[row] : -1;
-  if (id < 0 || id >= a.adapters) id = -1;
   // this part's steps of 64 k
   constexpr int splits = FEW ? kLowSplits : 1;
   const int steps = a.k / 64, left = a.k % 64;
   const int first = (int)((int64_t)steps * split / splits), last = (int)((int64_t)steps * (split + 1) / splits);
-  uint64_t pending = __ballot(id >= 0);
-  while (pending) {
-    const int ad = __builtin_amdgcn_readlane(id, __builtin_ctzll(pending));
-    pending &= ~__ballot(id == ad);
-    F few;
-    few.aim([&](int m, int r) { return a.a + ((int64_t)ad * R + min(k0 + m * 16 + r, R - 1)) * a.k; },
-            [&](int, int r) { return a.x.p + (int64_t)min(r0 + min(r, BLOCK - 1), n - 1) * a.x.stride; }, first,
-            last - first, blockIdx.x, lds + wave * F::kLds);
-    few.prime(wave, kLowWaves);
-    f32x4 acc[RT][1] = {};
-    few.run(wave, kLowWaves, acc);
-    if (left && split == splits - 1 && wave == kLowWaves - 1) few.tail(left, acc);
-    __syncthreads();                                      // the waves' pieces of lds become the sums
+  F few;
+  few.aim([&](int m, int r) { return a.a + ((int64_t)ad[m / RT] * R + min(k0 + m % RT * 16 + r, R - 1)) * a.k; },
+          [&](int, int r) { return a.x.p + (int64_t)min(r0 + min(r, BLOCK - 1), n - 1) * a.x.stride; }, first,
+          last - first, blockIdx.x, lds + wave * F::kLds);
+  few.prime(wave, kLowWaves);
+  f32x4 acc[RT * M][1] = {};
+  few.run(wave, kLowWaves, acc);
+  if (left && split == splits - 1 && wave == kLowWaves - 1) few.tail(left, acc);
+  __syncthreads();                                        // the waves' pieces of lds become the sums
 #pragma unroll
-    for (int m = 0; m < RT; ++m) sums[wave][m][i][lane >> 4] = acc[m][0];
-    __syncthreads();
-    const float* sum = reinterpret_cast<const float*>(lds);
-    const float scale = a.scales ? a.scales[ad] : 1.0f;
-    // the last of the rank is followed by zeros up to the stride
-    constexpr int kWide = RT == 1 && !FEW ? 32 : 16 * RT;
-    const bool last_of_rank = k0 + 16 * RT >= R;
+  for (int m = 0; m < RT * M; ++m) sums[wave][m][i][lane >> 4] = acc[m][0];
+  __syncthreads();
+  const float* sum = reinterpret_cast<const float*>(lds);
+  // the last of the rank is followed by zeros up to the stride
+  constexpr int kWide = RT == 1 && !FEW ? 32 : 16 * RT;
+  const bool last_of_rank = k0 + 16 * RT >= R;
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    const float scale = a.scales ? a.scales[ad[m]] : 1.0f;
     for (int o = threadIdx.x; o < BLOCK * kWide; o += kLowWaves * 64) {
       const int r = o / kWide, c = o % kWide, k = k0 + c;
       float v = 0;
       if (c < 16 * RT) {
 #pragma unroll
-        for (int w = 0; w < kLowWaves; ++w) v += sum[((w * RT + c / 16) * 16 + r) * 16 + c % 16];
+        for (int w = 0; w < kLowWaves; ++w) v += sum[((w * RT * M + m * RT + c / 16) * 16 + r) * 16 + c % 16];
       }
       v = k < R ? v * scale : 0.0f;
-      if (__shfl(id, r) != ad || k >= a.low_stride || (c >= 16 * RT && !last_of_rank)) continue;
+      if (__shfl(id, r) != ad[m] || k >= a.low_stride || (c >= 16 * RT && !last_of_rank)) continue;
       const int64_t at = (int64_t)(r0 + r) * a.low_stride + k, plane = (int64_t)n * a.low_stride;
       if constexpr (FEW) {
         static_cast<float*>(a.low)[split * plane + at] = v;
@@ -121,7 +114,36 @@ __global__ void __launch_bounds__(kLowWaves * 64) low_kernel(AdapterKArgs a) {
         for (int pl = 0; pl < kParts; ++pl) static_cast<uint16_t*>(a.low)[pl * plane + at] = part[pl];
       }
     }
-    __syncthreads();
+  }
+  __syncthreads();
+}
+
+// The low values of BLOCK rows of x and 16 RT of the rank.
+template <class T, int BLOCK, int RT, bool FEW>
+__global__ void __launch_bounds__(kLowWaves * 64) low_kernel(AdapterKArgs a) {
+  // two adapters a pass, where rows of two prompts meet
+  constexpr bool kPairs = BLOCK > 1 && RT == 1;
+  __shared__ __attribute__((aligned(1024))) char lds[kLowWaves * Few<T, kPairs ? 2 : RT, 1, kLowWaves>::kLds];
+  const int row = blockIdx.x * BLOCK + min((int)threadIdx.x & 15, BLOCK - 1);
+  // lanes of the same row name the same adapter; rows past the last none
+  int id = row < a.x.rows ? a.ids[row] : -1;
+  if (id < 0 || id >= a.adapters) id = -1;
+  uint64_t pending = __ballot(id >= 0);
+  auto next = [&]() {
+    const int ad = __builtin_amdgcn_readlane(id, __builtin_ctzll(pending));
+    pending &= ~__ballot(id == ad);
+    return ad;
+  };
+  while (pending) {
+    const int one[1] = {next()};
+    if constexpr (kPairs) {
+      if (pending) {
+        const int two[2] = {one[0], next()};
+        low_pass<T, BLOCK, RT, FEW, 2>(a, two, id, lds);
+        continue;
+      }
+    }
+    low_pass<T, BLOCK, RT, FEW, 1>(a, one, id, lds);
   }
 }
 
@@ -201,7 +223,8 @@ __global__ void __launch_bounds__(WAVES * 64) adapter_few_kernel(AdapterKArgs a)
 
 // Adds the adapters' sums to a tile's results.
 template <class G>
-__device__ __forceinline__ void add_adapters(const AdapterKArgs& a, int pt, int qt, typename G::Acc& acc) {
+__device__ __forceinline__ void add_adapters(const AdapterKArgs& a, int pt, int qt, const int (&id)[G::FQ],
+                                             typename G::Acc& acc) {
   typedef typename G::T T;
   const int lane = threadIdx.x & 63, quarter = lane >> 4;
   const int N = a.w.rows, R = a.rank;
@@ -209,16 +232,16 @@ __device__ __forceinline__ void add_adapters(const AdapterKArgs& a, int pt, int 
   // next one is loaded while this one's products are made.
   constexpr int kWaves = G::kThreads / 64, kGroups = G::kK / 64;
   static_assert(kWaves % kGroups == 0, "waves that share k");
-  constexpr int kPart = G::FP > 4 ? 4 : G::FP;          // columns' fragments at a time, within the registers
-  constexpr bool kKeep = G::FP * G::FQ <= 16;           // the low values of all rows at once
+  // Columns' fragments at a time, and whether the low values of all rows are
+  // held at once, within the registers.
+  constexpr bool kKeep = G::FP * G::FQ <= 16;
+  constexpr int kPart = kKeep ? G::FP : 4;
   // Rows are found from the tile's first by 32-bit offsets (256 rows of 1024).
-  int id[G::FQ];
   uint32_t low[G::FQ];
   const uint16_t* low_base = static_cast<const uint16_t*>(a.low) + (int64_t)qt * G::TQ * a.low_stride;
 #pragma unroll
   for (int j = 0; j < G::FQ; ++j) {
     const int q = G::wave_q() + j * 16 + (lane & 15), last = a.x.rows - 1 - qt * G::TQ;
-    id[j] = q <= last ? a.ids[qt * G::TQ + q] : -1;
     low[j] = (uint32_t)(min(q, last) * a.low_stride + quarter * 8) * 2;
   }
   const int64_t plane = (int64_t)a.x.rows * a.low_stride;
@@ -271,7 +294,7 @@ __device__ __forceinline__ void add_adapters(const AdapterKArgs& a, int pt, int 
         __builtin_amdgcn_sched_barrier(0);
         const int after = next_mine();
         u32x4 ahead[kPart];
-        load_b(max(after, 0), i0, ahead);
+        if (after >= 0) load_b(after, i0, ahead);
 #pragma unroll
         for (int j = 0; j < G::FQ; ++j) {
           if (!__ballot(id[j] == ad)) continue;
@@ -318,8 +341,14 @@ __global__ void __launch_bounds__(G::kThreads, G::kThreads / 256) adapter_kernel
   G::begin((MOE_EP_LDS char*)lds, sp, sq, a.k);
   typename G::Acc acc;
   G::clear(acc);
+  int id[G::FQ];                                          // of the wave's rows
+#pragma unroll
+  for (int j = 0; j < G::FQ; ++j) {
+    const int q = qt * G::TQ + G::wave_q() + j * 16 + (threadIdx.x & 15);
+    id[j] = q < a.x.rows ? a.ids[q] : -1;
+  }
   G::loop((MOE_EP_LDS char*)lds, sp, sq, a.k, acc);
-  add_adapters<G>(a, pt, qt, acc);
+  add_adapters<G>(a, pt, qt, id, acc);
   if (!G::join((MOE_EP_LDS char*)lds, acc)) return;
 
   const int lane = threadIdx.x & 63, quarter = lane >> 4, N = a.w.rows;
