@@ -35,13 +35,15 @@ class NormResult:
     residual: Optional[torch.Tensor]        # [n, hidden], x + residual; None without a residual
 
 
-def _like(out: Optional[torch.Tensor], shape, dtype: torch.dtype, x: torch.Tensor, what: str) -> torch.Tensor:
-    """``out``, checked, or a new tensor."""
+def _result(out: Optional[torch.Tensor], shape, dtype: torch.dtype, x: torch.Tensor, dev: int, what: str):
+    """(tensor, address, row stride) of ``out``, checked, or of a new tensor
+    (one of x's shape is made in half the time of any other)."""
     if out is None:
-        return x.new_empty(shape, dtype=dtype)
+        out = torch.empty_like(x, dtype=dtype) if shape == x.shape else x.new_empty(shape, dtype=dtype)
+        return out, out.data_ptr(), out.stride(0)
     if out.dtype != dtype or tuple(out.shape) != tuple(shape):
         raise ValueError(f"{what} must be {dtype} {list(shape)}")
-    return out
+    return (out, *_rows(out, dev, what))
 
 
 def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, *, eps: float = 1e-6,
@@ -73,23 +75,22 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Ten
     if not eight and out_dtype is not None and out_dtype != x.dtype:
         raise TypeError(f"out_dtype must be {x.dtype} or torch.float8_e4m3fn, got {out_dtype}")
     odt = torch.float8_e4m3fn if eight else x.dtype
-    out = _like(out, (n, H), odt, x, "out")
     a.x, a.x_stride = _rows(x, dev, "x")
-    a.out, a.out_stride = _rows(out, dev, "out")
+    out, a.out, a.out_stride = _result(out, (n, H), odt, x, dev, "out")
     a.weight = _on(weight, dev, "weight")
     if eight:
         if group_size not in (0, 32, 64, 128):
             raise ValueError(f"group_size {group_size} is not 0, 32, 64 or 128")
-        scales = _like(scales, (n, -(-H // group_size) if group_size else 1), torch.float32, x, "scales")
-        a.scales, a.scales_stride = _rows(scales, dev, "scales")
+        shape = (n, -(-H // group_size) if group_size else 1)
+        scales, a.scales, a.scales_stride = _result(scales, shape, torch.float32, x, dev, "scales")
     elif scales is not None or group_size:
         raise ValueError("scales and group_size go with out_dtype=torch.float8_e4m3fn")
     if residual is not None:
         if residual.dtype != x.dtype or residual.shape != x.shape:
             raise ValueError(f"residual must be {x.dtype} {list(x.shape)}")
         a.residual, a.residual_stride = _rows(residual, dev, "residual")
-        residual_out = _like(residual_out, (n, H), x.dtype, x, "residual_out")
-        a.residual_out, a.residual_out_stride = _rows(residual_out, dev, "residual_out")
+        residual_out, a.residual_out, a.residual_out_stride = _result(residual_out, (n, H), x.dtype, x, dev,
+                                                                      "residual_out")
     elif residual_out is not None:
         raise ValueError("residual_out goes with residual")
     a.dtype, a.weight_dtype = _DTYPES[x.dtype], _DTYPES[weight.dtype]
