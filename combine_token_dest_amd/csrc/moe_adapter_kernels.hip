@@ -378,7 +378,7 @@ template <class T, int NT>
 hipError_t adapter_few(const AdapterKArgs& a, hipStream_t stream) {
   const int blocks = tiles(a.w.rows, 16);
   if (NT > 2 || blocks >= 256) adapter_few_kernel<T, NT, 8><<<dim3(blocks), dim3(512), 0, stream>>>(a);
-  else adapter_few_kernel<T, NT < 4 ? NT : 2, 16><<<dim3(blocks), dim3(1024), 0, stream>>>(a);
+  else adapter_few_kernel<T, NT <= 2 ? NT : 2, 16><<<dim3(blocks), dim3(1024), 0, stream>>>(a);
   return hipGetLastError();
 }
 template <class T, int BLOCK, bool FEW>
@@ -402,6 +402,7 @@ hipError_t adapter(const AdapterKArgs& a, hipStream_t stream) {
   if (e != hipSuccess) return e;
   if (n <= 16) return adapter_few<T, 1>(a, stream);
   if (n <= 32) return adapter_few<T, 2>(a, stream);
+  if (n <= 48) return adapter_few<T, 3>(a, stream);
   if (n <= 64) return adapter_few<T, 4>(a, stream);
   const bool direct = a.w.whole && a.x.whole;
   switch (tile_size(a.w.rows, a.x.rows, a.k, direct, true)) {

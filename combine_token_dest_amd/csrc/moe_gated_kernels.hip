@@ -312,14 +312,22 @@ hipError_t gated_tiles(GatedKArgs a, hipStream_t stream) {
 template <class T, int NT>
 hipError_t gated_few(const GatedKArgs& a, hipStream_t stream) {
   const int blocks = tiles(a.inter, 8);
-  if (blocks >= 256) gated_few_kernel<T, NT, 8><<<dim3(blocks), dim3(512), 0, stream>>>(a);
-  else gated_few_kernel<T, NT, 16><<<dim3(blocks), dim3(1024), 0, stream>>>(a);
+  if (NT > 2 || blocks >= 256) gated_few_kernel<T, NT, 8><<<dim3(blocks), dim3(512), 0, stream>>>(a);
+  else gated_few_kernel<T, NT <= 2 ? NT : 2, 16><<<dim3(blocks), dim3(1024), 0, stream>>>(a);
   return hipGetLastError();
 }
 template <class T>
 hipError_t gated(const GatedKArgs& a, hipStream_t stream) {
   if (a.x.rows <= 16) return gated_few<T, 1>(a, stream);
   if (a.x.rows <= 32) return gated_few<T, 2>(a, stream);
+  // Up to 64 rows the weights' stream still wins, while its workgroups, each
+  // reading all of x, go through the card twice at most (48 rows, us, this and
+  // tiles: 7168 x 2048 14.6 and 21.6, 4096 x 1024 8.9 and 12.4, 2048 x 5632 17.2
+  // and 12.7).
+  if (tiles(a.inter, 8) <= 512) {
+    if (a.x.rows <= 48) return gated_few<T, 3>(a, stream);
+    if (a.x.rows <= 64) return gated_few<T, 4>(a, stream);
+  }
   const bool direct = a.w.whole && a.x.whole;
   switch (tile_size(2 * (int64_t)a.inter, a.x.rows, a.hidden, direct, true)) {
     case k256x256: return gated_tiles<Gemm<T, true, true, true, 256, 256, 2, 4, 1, true>>(a, stream);

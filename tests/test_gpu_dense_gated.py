@@ -35,7 +35,7 @@ def check_grads(dx, dw, x, w, dh, dtype):
 
 
 SIZES = [(1, 8, 8), (1, 7168, 64), (2, 64, 1000), (3, 100, 37), (5, 1030, 9), (16, 256, 24), (17, 64, 64),
-         (33, 129, 40), (64, 512, 128), (65, 200, 264), (127, 4100, 64), (129, 264, 136), (257, 520, 300),
+         (33, 129, 40), (64, 512, 128), (48, 1000, 72), (49, 264, 4200), (40, 72, 4104), (65, 200, 264), (127, 4100, 64), (129, 264, 136), (257, 520, 300),
          (300, 64, 8), (1000, 72, 200)]
 
 
