@@ -134,7 +134,7 @@ def gated(**kw):
 def grad_args(**kw):
     base = dict(dout=FAKE, dout_stride=32, x=2 * FAKE, x_stride=64, gate_up=3 * FAKE, gate_up_stride=64, pre=4 * FAKE,
                 dx=5 * FAKE, dx_stride=64, dgate_up=6 * FAKE, dgate_up_stride=64, workspace=7 * FAKE,
-                workspace_bytes=1 << 20, dtype=_lib.MOE_EP_F16, dout_dtype=_lib.MOE_EP_F16, num_rows=4, hidden_size=64,
+                workspace_bytes=1 << 24, dtype=_lib.MOE_EP_F16, dout_dtype=_lib.MOE_EP_F16, num_rows=4, hidden_size=64,
                 intermediate_size=32)
     base.update(kw)
     return _lib.moe_ep_gated_grad_args(**base)
