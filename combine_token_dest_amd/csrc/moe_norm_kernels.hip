@@ -98,19 +98,22 @@ __device__ __forceinline__ void store_e4m3(uint8_t* p, int have, const float (&q
   }
 }
 
-// v / scale, where the scale is max / 448 of the group: v * (1 / scale).  A
-// scale whose inverse would leave float32 is brought up by 2^100 first, and v
-// with it; such a scale may be subnormal, far enough below max / 448 that the
-// quotient needs an end.
-__device__ __forceinline__ void divide(float (&v)[8], float scale) {
+// 448 v / top of a group with the largest magnitude top, whose scale is
+// m top / 448.  The factor 448 / top has two parts, so beside v's own roundings
+// only the quotient's is left: every other one would put more quotients on the
+// wrong side of the middle between two e4m3 values.  A scale near float32's end
+// may be rounded by any share, so there it is what is divided by, brought up by
+// 2^100 as v is, and the quotient needs an end.
+__device__ __forceinline__ void divide(float (&v)[8], float top, float scale, float m) {
   if (scale < 0x1p-64f) {
-    const float inv = scale == 0.0f ? 0.0f : 1.0f / (scale * 0x1p100f);
+    const float inv = scale == 0.0f ? 0.0f : m / (scale * 0x1p100f);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = fminf(fmaxf(v[e] * 0x1p100f * inv, -448.0f), 448.0f);
   } else {
-    const float inv = 1.0f / scale;
+    const float high = 448.0f / top;                       // 0 of an infinity, NaN of NaN
+    const float low = high > 0.0f ? __builtin_fmaf(-top, high, 448.0f) / top : 0.0f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= inv;
+    for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(v[e], high, v[e] * low);
   }
 }
 
@@ -187,18 +190,20 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormKArgs a) {
     }
   }
   const double rstd = 1.0 / sqrt(block_sum(q, sums, waves) / H + (double)a.eps);
-  // Where the factor is outside the middle of float32's range a power of two
-  // of it goes apart.
-  const bool far = rstd > 0 && rstd < 1e300 && (rstd < 0x1p-96 || rstd > 0x1p96);
-  const int ex = far ? min(max(ilogb(rstd), -126), 126) : 0;
-  const float r1 = ldexpf(1.0f, ex), r2 = (float)ldexp(rstd, -ex);
+  // For 16 bits a power of two of the factor goes apart where it is outside the
+  // middle of float32's range.  For 8 bits it always does, and the rest stays
+  // out of the values, whose quotients do not need it.
+  const bool usual = rstd > 0 && rstd < 1e300, far = usual && (rstd < 0x1p-96 || rstd > 0x1p96);
+  const int ex = (EIGHT ? usual : far) ? min(max(ilogb(rstd), -126), 126) : 0;
+  const double rest = ldexp(rstd, -ex);
+  const float r1 = EIGHT && !usual ? (float)rstd : ldexpf(1.0f, ex), r2 = (float)rest;
 
-  auto scaled = [&](int c, int have, float (&v)[8]) {     // s to y
+  auto scaled = [&](int c, int have, float (&v)[8]) {     // s to y; for 8 bits to y / rest
     float w[8];
     if constexpr (sizeof(W) == 4) load_row8(reinterpret_cast<const float*>(weight) + c, have, w);
     else load_row8<T>(reinterpret_cast<const uint16_t*>(weight) + c, have, w);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = (far ? v[e] * r1 : v[e]) * r2 * w[e];
+    for (int e = 0; e < 8; ++e) v[e] = EIGHT ? v[e] * r1 * w[e] : (far ? v[e] * r1 : v[e]) * r2 * w[e];
   };
   auto keep = [&](int c, int have, const float (&v)[8]) {
     if (a.residual_out) store_row8<T>(a.residual_out + r * a.residual_out_stride + c, have, v);
@@ -236,17 +241,19 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormKArgs a) {
       for (int e = 0; e < 8; ++e) t = max(t, magnitude(y[e]));
       return t;
     };
-    auto put = [&](int c, int have, float (&y)[8], float scale) {
-      divide(y, scale);
+    const double share = usual ? rest / 448 : 1.0 / 448;
+    const float m = usual ? r2 : 1.0f;
+    auto scale_of = [&](uint32_t t) { return (float)(__uint_as_float(t) * share); };
+    auto put = [&](int c, int have, float (&y)[8], uint32_t t) {
+      divide(y, __uint_as_float(t), scale_of(t), m);
       store_e4m3(out + c, have, y);
     };
     // The lanes of a group of columns are neighbours: the maximum of theirs.
     const int lanes = a.group / 8;
-    auto group_scale = [&](uint32_t t, int c) {
+    auto group_top = [&](uint32_t t, int c) {
       for (int d = 1; d < lanes; d *= 2) t = max(t, (uint32_t)__shfl_xor((int)t, d));
-      const float scale = __uint_as_float(t) / 448.0f;
-      if (c < H && c % a.group == 0) scales[c / a.group] = scale;
-      return scale;
+      if (c < H && c % a.group == 0) scales[c / a.group] = scale_of(t);
+      return t;
     };
     if constexpr (VPT > 0) {
       uint32_t top = 0;
@@ -257,20 +264,20 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormKArgs a) {
           keep(c, H - c, s[i]);
           scaled(c, H - c, s[i]);
         }
-        const uint32_t t = top8(s[i]);
+        uint32_t t = top8(s[i]);
         top = max(top, t);
         if (a.group) {
-          const float scale = group_scale(t, c);
-          if (c < H) put(c, H - c, s[i], scale);
+          t = group_top(t, c);
+          if (c < H) put(c, H - c, s[i], t);
         }
       }
       if (!a.group) {
-        const float scale = __uint_as_float(block_max(top, tops, waves)) / 448.0f;
-        if (tid == 0) scales[0] = scale;
+        top = block_max(top, tops, waves);
+        if (tid == 0) scales[0] = scale_of(top);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
           const int c = (i * threads + tid) * 8;
-          if (c < H) put(c, H - c, s[i], scale);
+          if (c < H) put(c, H - c, s[i], top);
         }
       }
     } else {
@@ -282,7 +289,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormKArgs a) {
           top = max(top, top8(s[0]));
         }
         top = block_max(top, tops, waves);
-        if (tid == 0) scales[0] = __uint_as_float(top) / 448.0f;
+        if (tid == 0) scales[0] = scale_of(top);
       }
       for (int v = tid; v < (vectors + threads - 1) / threads * threads; v += threads) {   // all lanes take part
         const int c = v * 8;
@@ -294,8 +301,8 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormKArgs a) {
           scaled(c, H - c, y);
           keep(c, H - c, s[0]);
         }
-        const float scale = a.group ? group_scale(top8(y), c) : __uint_as_float(top) / 448.0f;
-        if (c < H) put(c, H - c, y, scale);
+        const uint32_t t = a.group ? group_top(top8(y), c) : top;
+        if (c < H) put(c, H - c, y, t);
       }
     }
   }

@@ -126,6 +126,21 @@ def test_small_and_large_values(std, eps):
     check(x, w, eps=eps, eight=True)
 
 
+@pytest.mark.parametrize("group", [0, 32, 64])
+@pytest.mark.parametrize("k", [1, 3, 5, 7])
+def test_middles_round_to_even(k, group):
+    """Rows of a largest value 448 k with values k t, t in the middle of two
+    e4m3 values: the quotients are t whatever the norm is, and t k has at most
+    8 bits, so the whole path but for its roundings is exact."""
+    H = 192
+    t = torch.tensor([17.0, 19, 21, 23, 25, 27, 29, 31])
+    t = torch.cat([t * 2.0 ** e for e in (-8, -4, 0, 3)] + [-t, -t / 2])[torch.arange(H) % 48]
+    t[::32] = 448.0
+    x = (t * k * torch.tensor([[1.0], [2.0 ** -20], [2.0 ** 30], [0.125]])).to(BF16)
+    r = rms_norm(x.cuda(), torch.ones(H, dtype=BF16, device="cuda"), out_dtype=E4M3, group_size=group, eps=1e-6)
+    assert (r.rows.cpu().float() == t.to(E4M3).float()).all()
+
+
 def test_scales_below_the_smallest_normal():
     """Groups whose weight is tiny: the scale is subnormal or 0."""
     x = rand(1, 4, 256)
