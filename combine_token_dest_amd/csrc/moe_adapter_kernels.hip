@@ -165,40 +165,51 @@ __global__ void __launch_bounds__(WAVES * 64) adapter_few_kernel(AdapterKArgs a)
           [&](int t, int r) { return a.x.p + (int64_t)min(t * 16 + r, a.x.rows - 1) * a.x.stride; }, 0, steps,
           blockIdx.x, lds + wave * F::kLds);
   few.prime(wave, WAVES);
-  // The adapters' sums of this thread's results, while the first weights are on their way.
-  constexpr int kMine = (NT * 256 + WAVES * 64 - 1) / (WAVES * 64);
-  constexpr int kUnroll = WAVES > 8 ? 1 : 2;
-  float own[kMine];
+  // The adapters' sums of this thread's results, while the first weights are on
+  // their way: kRank of the rank at a time, whose low values, which 16 columns
+  // share, are added up in LDS once.
+  constexpr int kRank = 64, kThreads = WAVES * 64;
+  constexpr int kMine = (NT * 256 + kThreads - 1) / kThreads;
+  constexpr int kUnroll = WAVES > 8 ? 2 : 4;
+  __shared__ __attribute__((aligned(16))) float lows[NT * 16][kRank + 4];
+  float own[kMine] = {};
+  int id[kMine];
 #pragma unroll
   for (int m = 0; m < kMine; ++m) {
-    const int o = m * WAVES * 64 + threadIdx.x, r = o >> 4, c = c0 + (o & 15);
-    own[m] = 0;
-    if (r < a.x.rows && c < N) {
-      const int id = a.ids[r];
-      if (id >= 0 && id < a.adapters) {
-        const uint16_t* b = a.b + ((int64_t)id * N + c) * R;
-        const float* low = static_cast<const float*>(a.low) + (int64_t)r * a.low_stride;
-        const int64_t plane = (int64_t)a.x.rows * a.low_stride;
+    const int o = m * kThreads + threadIdx.x, r = o >> 4;
+    id[m] = r < a.x.rows && c0 + (o & 15) < N ? a.ids[r] : -1;
+    if (id[m] >= a.adapters) id[m] = -1;
+  }
+  const int64_t plane = (int64_t)a.x.rows * a.low_stride;
+  for (int k0 = 0; k0 < R; k0 += kRank) {
+    if (k0) __syncthreads();
+    for (int o = threadIdx.x; o < NT * kRank * 4; o += kThreads) {
+      const int r = o / (kRank / 4), k = o % (kRank / 4) * 4;
+      const float* low =
+          static_cast<const float*>(a.low) + (int64_t)min(r, a.x.rows - 1) * a.low_stride + min(k0 + k, a.low_stride - 4);
+      f32x4 v[kLowSplits];
+#pragma unroll
+      for (int s = 0; s < kLowSplits; ++s) v[s] = *reinterpret_cast<const f32x4*>(low + s * plane);
+      f32x4 sum = v[0];
+#pragma unroll
+      for (int s = 1; s < kLowSplits; ++s) sum += v[s];
+      *reinterpret_cast<f32x4*>(&lows[r][k]) = sum;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < kMine; ++m) {
+      if (id[m] < 0) continue;
+      const int o = m * kThreads + threadIdx.x;
+      const uint16_t* b = a.b + ((int64_t)id[m] * N + c0 + (o & 15)) * R;
 #pragma unroll kUnroll
-        for (int k = 0; k < R; k += 8) {
-          u32x4 bv[1];
-          const uint32_t rows[1] = {0};
-          b_elements<1>(b, rows, k, R, bv);
-          const u32x4 w = bv[0];
-          f32x4 v[kLowSplits][2];
+      for (int k = k0; k < min(k0 + kRank, R); k += 8) {
+        u32x4 w[1];
+        const uint32_t rows[1] = {0};
+        b_elements<1>(b, rows, k, R, w);
+        // (what is past the rank is 0 in both)
 #pragma unroll
-          for (int s = 0; s < kLowSplits; ++s)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) v[s][h] = *reinterpret_cast<const f32x4*>(low + s * plane + k + h * 4);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            float l = 0;
-#pragma unroll
-            for (int s = 0; s < kLowSplits; ++s) l += v[s][e >> 2][e & 3];
-            // (what is past the rank is 0 in both)
-            own[m] += l * T::to_float((uint16_t)(w[e >> 1] >> (e & 1) * 16));
-          }
-        }
+        for (int e = 0; e < 8; ++e)
+          own[m] += lows[o >> 4][k - k0 + e] * T::to_float((uint16_t)(w[0][e >> 1] >> (e & 1) * 16));
       }
     }
   }
