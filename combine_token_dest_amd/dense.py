@@ -182,7 +182,10 @@ def gated_linear(x: torch.Tensor, gate_up: torch.Tensor, *, out: Optional[torch.
 
     Where autograd records (x or gate_up requires gradients), both get theirs,
     in x's type and from float32 sums; gate and up are kept for it as float32
-    [rows, 2 * intermediate], and ``out`` is refused.  See include/moe_ep.h,
+    [rows, 2 * intermediate], and ``out`` is refused.  As for torch's own
+    operators, a ``backward()`` may be captured into a graph only while no
+    result that was recorded outside the capture from the same leaves is
+    alive: torch would accumulate on the other stream.  See include/moe_ep.h,
     moe_ep_gated and moe_ep_gated_grad."""
     if torch.is_grad_enabled() and (x.requires_grad or gate_up.requires_grad or
                                     (out is not None and out.requires_grad)):

@@ -48,6 +48,14 @@ def test_sizes(n, N, K, L, R, dtype, out_dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("n,N,K,L,R", [(30, 70, 136, 3, 77), (3, 20, 64, 2, 1000), (50, 33, 72, 7, 65), (10, 40, 80, 4, 1024),
+                                       (64, 16, 64, 5, 127), (9, 4100, 64, 3, 129)])
+def test_ranks_of_several_parts(n, N, K, L, R, dtype):
+    t = make(n, N, K, L, R, dtype)
+    check(run(*t), *t)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
 def test_prompts_one_after_another(dtype):
     """Runs of rows with one adapter, whose ends fall inside tiles; no scales; int64 ids."""
     x, w, a, b, _, _ = make(700, 264, 192, 4, 16, dtype)
