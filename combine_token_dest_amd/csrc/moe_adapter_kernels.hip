@@ -13,10 +13,12 @@
 // never meets another adapter's B, whatever is in it).  (Before the product it
 // would wait no longer than the first tiles do, but the compiler then finds no
 // registers for the product's loop.)
-// The low values go in as three bfloat16 each, float32's 24 bits.  Few rows take the
-// kernel that streams the weights (moe_few_device.h), where each result adds
-// its own adapter's sum over the rank in float32, made while the first weights
-// are on their way.
+// The low values go in as three bfloat16 each, float32's 24 bits.  An infinity
+// on either side meets all of the other's parts, of which none may be 0 or of
+// the other sign then: low_parts() and the float16 path see to it.  Few rows
+// take the kernel that streams the weights (moe_few_device.h), where each
+// result adds its own adapter's sum over the rank in float32, made while the
+// first weights are on their way.
 //
 // 2048 rows of 4096 x 7168 with five adapters of rank 16 take 144 us: 15 for the
 // low values and the rest for the product, which alone takes 113; one row 4 and 11.
@@ -59,6 +61,51 @@ __device__ __forceinline__ void b_elements(const uint16_t* base, const uint32_t 
       v[i] = u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
     }
   }
+}
+
+// A low value's parts (split_parts), where a part that would be 0 beside a
+// number is 2^-40 of it instead: less than float32's 24 bits tell, and an
+// infinity in B times each part has the number's sign.  (Numbers below 2^-100,
+// beside which bfloat16 has no room for that, keep the zeros.)
+__device__ __forceinline__ void low_parts(float v, uint16_t (&part)[kParts]) {
+  split_parts(v, part);
+  const int first = part[0], exponent = first >> 7 & 0xFF;
+  const uint16_t least = (uint16_t)((first & 0x8000) | max(exponent - 40, 1) << 7);
+#pragma unroll
+  for (int pl = 1; pl < kParts; ++pl)
+    if (exponent >= 27 && exponent < 255 && !(part[pl] & 0x7FFF)) part[pl] = least;
+}
+
+// split_f16 with a second part of 0 beside an infinity or NaN.
+__device__ __forceinline__ void split_f16_finite(const u32x4& v, u32x4* hi, u32x4* lo) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = F16::to_float((uint16_t)v[i]), b = F16::to_float((uint16_t)(v[i] >> 16));
+    const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b) & 0xFFFF0000u;
+    float ra = a - __uint_as_float(ua & 0xFFFF0000u), rb = b - __uint_as_float(ub);
+    ra = ra == ra ? ra : 0.0f;
+    rb = rb == rb ? rb : 0.0f;
+    (*hi)[i] = ua >> 16 | ub;
+    (*lo)[i] = __float_as_uint(ra) >> 16 | (__float_as_uint(rb) & 0xFFFF0000u);
+  }
+}
+
+// Eight bfloat16 with zeros for infinities and NaN.
+__device__ __forceinline__ u32x4 finite_ones(const u32x4& v) {
+  u32x4 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // an exponent of ones carries into its half's top bit, which then fills the half
+    const uint32_t bad = ((v[i] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+    r[i] = v[i] & ~((bad << 1) - (bad >> 15));
+  }
+  return r;
+}
+__device__ __forceinline__ bool all_finite(const u32x4& v) {
+  uint32_t bad = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) bad |= (v[i] & 0x7F807F80u) + 0x00800080u;
+  return !(bad & 0x80008000u);
 }
 
 constexpr int kLowWaves = 8;
@@ -112,7 +159,7 @@ __device__ __forceinline__ void low_pass(const AdapterKArgs& a, const int (&ad)[
         static_cast<float*>(a.low)[split * plane + at] = v;
       } else {
         uint16_t part[kParts];
-        split_parts(v, part);
+        low_parts(v, part);
 #pragma unroll
         for (int pl = 0; pl < kParts; ++pl) static_cast<uint16_t*>(a.low)[pl * plane + at] = part[pl];
       }
@@ -247,7 +294,9 @@ __device__ __forceinline__ void add_adapters(const AdapterKArgs& a, int pt, int 
   constexpr int kWaves = G::kThreads / 64, kGroups = G::kK / 64;
   static_assert(kWaves % kGroups == 0, "waves that share k");
   // Columns' fragments at a time, and whether the low values of all rows are
-  // held at once, within the registers.
+  // held at once, within the registers.  (float16 tiles of 256 x 256 still keep
+  // 12 of them in scratch memory; with two fragments at a time none, but 4096
+  // rows of 8192 x 1024 with 300 prompts take 152 us for 142.)
   constexpr bool kKeep = G::FP * G::FQ <= 16;
   constexpr int kPart = kKeep ? G::FP : 4;
   // Rows are found from the tile's first by 32-bit offsets (256 rows of 1024).
@@ -319,15 +368,21 @@ __device__ __forceinline__ void add_adapters(const AdapterKArgs& a, int pt, int 
           } else {
             load_low(j, part);
           }
+          // float16: B's second part, which may be 0, and an infinite low value
+          // do not meet.
+          u32x4 finite = part[0];
+          if constexpr (std::is_same<T, F16>::value) {
+            if (__ballot(!all_finite(part[0]))) finite = finite_ones(part[0]);
+          }
 #pragma unroll
           for (int i = 0; i < kPart; ++i) {
             f32x4 sum = {0, 0, 0, 0};
             u32x4 v[2] = {b[i], {}};
-            if constexpr (std::is_same<T, F16>::value) split_f16(b[i], &v[0], &v[1]);
+            if constexpr (std::is_same<T, F16>::value) split_f16_finite(b[i], &v[0], &v[1]);
 #pragma unroll
             for (int pl = 0; pl < kParts; ++pl) {
               sum = BF16::mfma(v[0], part[pl], sum);
-              if constexpr (std::is_same<T, F16>::value) sum = BF16::mfma(v[1], part[pl], sum);
+              if constexpr (std::is_same<T, F16>::value) sum = BF16::mfma(v[1], pl ? part[pl] : finite, sum);
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e)

@@ -628,10 +628,12 @@ MOE_EP_API int moe_ep_adapter_workspace_bytes(const moe_ep_adapter_args* args, s
  *   out[r] = weight x[r] + scales[a] * lora_b[a] (lora_a[a] x[r]), a = adapter_ids[r];
  * rows whose id is outside [0, num_adapters) have no adapter.  lora_a[a] x is
  * kept as float32, whole, and the sum of both products is rounded once.  What
- * is in an adapter that a row does not name does not reach the row.  out must
- * not overlap an input, each taken from its first element to its last.  The
- * workspace holds nothing between calls; calls that may overlap in time need
- * one each.  Two kernel launches. */
+ * is in an adapter that a row does not name does not reach the row; infinities
+ * and NaN in its own give what the formula gives (but an infinity in lora_b
+ * times a low value below 2^-100 may give NaN).  out must not overlap an input,
+ * each taken from its first element to its last.  The workspace holds nothing
+ * between calls; calls that may overlap in time need one each.  Two kernel
+ * launches. */
 MOE_EP_API int moe_ep_adapter_linear(const moe_ep_adapter_args* args, void* stream);
 
 /* Static text for a status code. */

@@ -224,3 +224,43 @@ def test_a_block(n):
     close(h, want, ref.rounded(want, th, BF16))
     out = adapter_linear(h, w.cuda(), a.cuda(), b.cuda(), ids.cuda(), scales=scales.cuda())
     check(out, h.cpu(), w, a, b, ids, scales)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("n,N,K,R", [(4, 136, 64, 16), (64, 40, 72, 5), (65, 136, 64, 16), (150, 264, 64, 33), (700, 500, 72, 3),
+                                     (2300, 4096, 64, 16)])
+def test_infinities_and_nan_of_a_rows_own_adapter(n, N, K, R, dtype):
+    """They reach a row's results as the formula says, in few rows and many:
+    against low values of one bfloat16, of three, negative ones, infinite ones
+    and zeros."""
+    x, w, a, b, _, _ = make(n, N, K, 4, R, dtype)
+    # low values of adapter 0: 0.5, 1 + 2^-7 and some more bits, 0; of adapter 2, with its scale: -2, 6
+    a[0], a[2] = 0, 0
+    x[:, :3] = torch.tensor([0.5, 1.0, -3.0], dtype=dtype)
+    x[:, 3:].abs_().clamp_min_(0.25)
+    a[0, 0, 0], a[0, 1, 1], a[0, 1, 0], a[0, 1, 2] = 1, 1, 2.0 ** -7, -(2.0 ** -8) / 3
+    a[2, 0, 1], a[2, 1, 2] = 1, 1
+    a[1, 1, 5] = math.inf                      # an infinite low value, beside finite ones
+    b[0, 0, 0], b[0, 1, 0], b[0, 2, 1], b[0, 3, 1] = math.inf, -math.inf, math.inf, math.nan
+    b[0, 4, 2] = math.inf                      # times 0
+    b[0, 5, 0], b[0, 5, 1] = math.inf, -math.inf
+    b[1, 6, 1], b[1, 7, 1], b[1, 8, 1] = 0.5, -0.5, 0
+    b[2, 9, 1], b[2, 10, 0] = math.inf, -math.inf
+    ids = (torch.arange(n) % 5 - 1).to(torch.int32)
+    scales = torch.tensor([1.0, 0.75, -2.0, 1.0])
+    got = run(x, w, a, b, ids, scales).double().cpu()
+    want = x.double() @ w.double().t()
+    for i in range(4):
+        rows = ids == i
+        low = (x[rows].double() @ a[i].double().t()) * float(scales[i])
+        want[rows] += low @ b[i].double().t()
+    assert want.isinf().any() and want.isnan().any() and want.isfinite().any()
+    assert torch.equal(got.isnan(), want.isnan())
+    special = want.isinf() & ~want.isnan()
+    assert torch.equal(got[special], want[special])
+    assert torch.equal(got.isfinite(), want.isfinite())
+    # the finite ones: of adapters 0, 2 and 3 without the infinities, which are not in their sums
+    fine = [torch.nan_to_num(t.float(), nan=0.0, posinf=0.0, neginf=0.0).to(dtype) for t in (a, b)]
+    y, tol = ref.adapter(x, w, *fine, ids, scales, dtype)
+    keep = want.isfinite()
+    assert ((got - y).abs()[keep] <= tol[keep]).all()
