@@ -12,7 +12,8 @@ Every step runs in the library's gfx950 kernels (include/moe_ep.h); torch is
 used for device memory and the current stream.  Work is enqueued on the
 current stream of the tensors' device; what a call needs beyond its inputs
 comes from torch's allocator for that stream, so calls may be captured into
-graphs and run on several streams at once.
+graphs and run on several streams at once.  Tensors that carry a forward-mode
+derivative are refused.
 """
 
 from __future__ import annotations
@@ -23,7 +24,8 @@ from typing import Optional
 import torch
 
 from . import _lib
-from .experts import _DTYPES, _activations, _call, _forward_only, _ids, _int32, _on, _output, _rows
+from .experts import (_DTYPES, _activations, _call, _forward_only, _ids, _int32, _no_tangents, _on, _output,
+                      _rows)
 
 
 @dataclass
@@ -187,6 +189,7 @@ def gated_linear(x: torch.Tensor, gate_up: torch.Tensor, *, out: Optional[torch.
     result that was recorded outside the capture from the same leaves is
     alive: torch would accumulate on the other stream.  See include/moe_ep.h,
     moe_ep_gated and moe_ep_gated_grad."""
+    _no_tangents("gated_linear", x, gate_up, out)
     if torch.is_grad_enabled() and (x.requires_grad or gate_up.requires_grad or
                                     (out is not None and out.requires_grad)):
         if out is not None:

@@ -10,7 +10,8 @@ used for device memory and the current stream.  Work is enqueued on the
 current stream of the tensors' device; what a call needs beyond its inputs
 comes from torch's allocator for that stream, so calls may be captured into
 graphs and run on several streams at once.  There is no backward pass: tensors
-that require gradients are refused outside ``torch.no_grad()``.
+that require gradients are refused outside ``torch.no_grad()``, and tensors that
+carry a forward-mode derivative everywhere.
 """
 
 from __future__ import annotations
@@ -21,6 +22,7 @@ from dataclasses import dataclass
 from typing import Optional, Tuple, Union
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _lib
 from ._lib import MOE_EP_BF16, MOE_EP_F16, MOE_EP_F32
@@ -155,8 +157,21 @@ class W4Weights:
 Weight = Union[torch.Tensor, W4Weights]
 
 
+def _no_tangents(what: str, *tensors) -> None:
+    """Refuses tensors that carry a forward-mode derivative (the result would
+    have none, which reads as zero)."""
+    if forward_ad._current_level >= 0:
+        for t in tensors:
+            if isinstance(t, W4Weights):
+                t = t.scales
+            if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+                raise RuntimeError(f"{what} has no forward-mode derivative, but a tensor carries a tangent: "
+                                   f"call it with the primal")
+
+
 def _forward_only(what: str, *tensors) -> None:
     """Refuses what autograd would have to record (the result has no graph)."""
+    _no_tangents(what, *tensors)
     if torch.is_grad_enabled():
         for t in tensors:
             if isinstance(t, W4Weights):
