@@ -243,8 +243,9 @@ def adapter_linear(x: torch.Tensor, weight: torch.Tensor, lora_a: torch.Tensor, 
     a.x, a.x_stride = _rows(x, dev, "x")
     a.out, a.out_stride = _rows(out, dev, "out")
     a.dtype, a.out_dtype = _DTYPES[x.dtype], _DTYPES[out.dtype]
-    a.num_rows, a.in_features, a.out_features = _int32(n, "row count"), _int32(K, "in_features"), N
-    a.num_adapters, a.rank = L, R
+    a.num_rows = _int32(n, "row count")
+    a.in_features, a.out_features = _int32(K, "in_features"), _int32(N, "out_features")
+    a.num_adapters, a.rank = _int32(L, "adapter count"), _int32(R, "rank")
     if workspace is None:
         nbytes = _lib.moe_ep_adapter_workspace_bytes(a)
         workspace = x.new_empty((nbytes,), dtype=torch.uint8)
@@ -259,5 +260,6 @@ def adapter_linear(x: torch.Tensor, weight: torch.Tensor, lora_a: torch.Tensor, 
 
 def adapter_linear_workspace_bytes(rows: int, rank: int) -> int:
     """Bytes of workspace ``adapter_linear`` takes for these sizes."""
-    a = _lib.moe_ep_adapter_args(num_rows=rows, rank=rank, num_adapters=1, in_features=8, out_features=1)
+    a = _lib.moe_ep_adapter_args(num_rows=_int32(rows, "row count"), rank=_int32(rank, "rank"), num_adapters=1,
+                                 in_features=8, out_features=1)
     return _lib.moe_ep_adapter_workspace_bytes(a)

@@ -360,9 +360,9 @@ def expert_linear(x: torch.Tensor, weight: Weight, expert_ids: Optional[torch.Te
         expert_ids = _ids(expert_ids, (n,), dev, "expert_ids")
         a.expert_ids = expert_ids.data_ptr()
     a.dtype, a.out_dtype = _DTYPES[x.dtype], _DTYPES[out.dtype]
-    a.num_rows, a.num_experts = _int32(n, "row count"), E
+    a.num_rows, a.num_experts = _int32(n, "row count"), _int32(E, "expert count")
     a.expert_offset = _int32(expert_offset, "expert_offset")
-    a.in_features, a.out_features = K, N
+    a.in_features, a.out_features = _int32(K, "in_features"), _int32(N, "out_features")
     _call(_lib.moe_ep_expert_linear, dev, a)
     return out
 
@@ -423,9 +423,9 @@ def moe_layer(hidden: torch.Tensor, gate_up: Weight, down: Weight, topk_ids: Opt
     a.hidden, a.hidden_stride = _rows(hidden, dev, "hidden")
     a.out, a.out_stride = _rows(out, dev, "out")
     a.dtype, a.out_dtype = _DTYPES[dtype], _DTYPES[out.dtype]
-    a.num_tokens, a.top_k, a.num_experts = _int32(n, "token count"), top_k, E
+    a.num_tokens, a.top_k, a.num_experts = _int32(n, "token count"), _int32(top_k, "top_k"), _int32(E, "expert count")
     a.expert_offset = _int32(expert_offset, "expert_offset")
-    a.hidden_size, a.intermediate_size = H, inter
+    a.hidden_size, a.intermediate_size = _int32(H, "hidden size"), _int32(inter, "intermediate size")
     if workspace is None:
         nbytes = _lib.moe_ep_layer_workspace_bytes(a)
         workspace = hidden.new_empty((nbytes,), dtype=torch.uint8)
@@ -444,8 +444,9 @@ def moe_layer_workspace_bytes(tokens: int, top_k: int, num_experts: int, hidden:
     is that of a 4-bit ``gate_up`` (0: dense), ``routed`` when it is given
     router logits."""
     a = _lib.moe_ep_layer_args()
-    a.num_tokens, a.top_k, a.num_experts = tokens, top_k, num_experts
-    a.hidden_size, a.intermediate_size, a.gate_up.group_size = hidden, intermediate, group_size
+    a.num_tokens, a.top_k = _int32(tokens, "token count"), _int32(top_k, "top_k")
+    a.num_experts, a.gate_up.group_size = _int32(num_experts, "expert count"), group_size
+    a.hidden_size, a.intermediate_size = _int32(hidden, "hidden size"), _int32(intermediate, "intermediate size")
     if routed:
         a.router = ctypes.pointer(_lib.moe_ep_router())
     return _lib.moe_ep_layer_workspace_bytes(a)
