@@ -25,7 +25,7 @@ import torch
 
 from . import _lib
 from .experts import (_DTYPES, _activations, _call, _forward_only, _ids, _int32, _no_tangents, _on, _output,
-                      _rows)
+                      _rows, _written)
 
 
 @dataclass
@@ -69,6 +69,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Ten
     dev = _activations(x, "x")
     n, H = x.shape
     a = _lib.moe_ep_norm_args()
+    given = (out, scales, residual_out)
     if weight.dtype != x.dtype and weight.dtype != torch.float32:
         raise TypeError(f"weight is {weight.dtype}, x {x.dtype}: it must be of x's type or float32")
     if tuple(weight.shape) != (H,) or not weight.is_contiguous():
@@ -99,6 +100,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Ten
     a.out_dtype = _lib.MOE_EP_E4M3 if eight else a.dtype
     a.group_size, a.num_rows, a.hidden_size, a.eps = group_size, _int32(n, "row count"), _int32(H, "hidden size"), eps
     _call(_lib.moe_ep_rms_norm, dev, a)
+    _written(*given)
     return NormResult(out, scales, residual_out)
 
 
@@ -121,7 +123,7 @@ def _gated(x: torch.Tensor, gate_up: torch.Tensor, out, out_dtype, keep: bool):
     if gate_up.shape[0] % 2:
         raise ValueError(f"gate_up has {gate_up.shape[0]} rows, not twice as many as the result has columns")
     inter = gate_up.shape[0] // 2
-    out = _output(out, (n, inter), x.dtype, out_dtype, x)
+    given, out = out, _output(out, (n, inter), x.dtype, out_dtype, x)
     a.x, a.x_stride = _rows(x, dev, "x")
     a.out, a.out_stride = _rows(out, dev, "out")
     pre = None
@@ -132,6 +134,7 @@ def _gated(x: torch.Tensor, gate_up: torch.Tensor, out, out_dtype, keep: bool):
     a.num_rows, a.hidden_size = _int32(n, "row count"), _int32(H, "hidden size")
     a.intermediate_size = _int32(inter, "intermediate size")
     _call(_lib.moe_ep_gated, dev, a)
+    _written(given)
     return out, pre
 
 
@@ -239,7 +242,7 @@ def adapter_linear(x: torch.Tensor, weight: torch.Tensor, lora_a: torch.Tensor, 
         if scales.dtype != torch.float32 or tuple(scales.shape) != (L,) or not scales.is_contiguous():
             raise ValueError(f"scales must be a contiguous float32 [{L}]")
         a.scales = _on(scales, dev, "scales")
-    out = _output(out, (n, N), x.dtype, out_dtype, x)
+    given, out = out, _output(out, (n, N), x.dtype, out_dtype, x)
     a.x, a.x_stride = _rows(x, dev, "x")
     a.out, a.out_stride = _rows(out, dev, "out")
     a.dtype, a.out_dtype = _DTYPES[x.dtype], _DTYPES[out.dtype]
@@ -255,6 +258,7 @@ def adapter_linear(x: torch.Tensor, weight: torch.Tensor, lora_a: torch.Tensor, 
         nbytes = workspace.numel()
     a.workspace, a.workspace_bytes = _on(workspace, dev, "workspace"), nbytes
     _call(_lib.moe_ep_adapter_linear, dev, a)
+    _written(given)
     return out
 
 

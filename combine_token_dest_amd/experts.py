@@ -307,6 +307,14 @@ def _call(entry, dev: int, *args) -> None:
             entry(*args, torch._C._cuda_getCurrentRawStream(dev))
 
 
+def _written(*outputs: Optional[torch.Tensor]) -> None:
+    """Counts a new version of the caller's outputs, as torch's own operators
+    do: a backward pass that saved one refuses what is there now."""
+    for t in outputs:
+        if t is not None and not t.is_inference():
+            torch.autograd.graph.increment_version(t)
+
+
 def route(logits: torch.Tensor, router: Router, *, topk_ids: Optional[torch.Tensor] = None,
           topk_weights: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Each token's ``top_k`` expert ids (int32) and weights (float32), both
@@ -320,7 +328,7 @@ def route(logits: torch.Tensor, router: Router, *, topk_ids: Optional[torch.Tens
     n, E = logits.shape
     _int32(n, "token count")
     r = _router(router, E, dev)
-    shape = (n, router.top_k)
+    shape, given = (n, router.top_k), (topk_ids, topk_weights)
     if topk_ids is None:
         topk_ids = logits.new_empty(shape, dtype=torch.int32)
     elif topk_ids.dtype != torch.int32 or tuple(topk_ids.shape) != shape or not topk_ids.is_contiguous():
@@ -332,6 +340,7 @@ def route(logits: torch.Tensor, router: Router, *, topk_ids: Optional[torch.Tens
         raise ValueError(f"topk_weights must be a contiguous float32 {list(shape)}")
     _call(_lib.moe_ep_route, dev, r, logits.data_ptr(), dtype, stride, n, _on(topk_ids, dev, "topk_ids"),
           _on(topk_weights, dev, "topk_weights"))
+    _written(*given)
     return topk_ids, topk_weights
 
 
@@ -353,7 +362,7 @@ def expert_linear(x: torch.Tensor, weight: Weight, expert_ids: Optional[torch.Te
     n = x.shape[0]
     if x.shape[1] != K:
         raise ValueError(f"x has {x.shape[1]} features, weight {K}")
-    out = _output(out, (n, N), x.dtype, out_dtype, x)
+    given, out = out, _output(out, (n, N), x.dtype, out_dtype, x)
     a.x, a.x_stride = _rows(x, dev, "x")
     a.out, a.out_stride = _rows(out, dev, "out")
     if expert_ids is not None:
@@ -364,6 +373,7 @@ def expert_linear(x: torch.Tensor, weight: Weight, expert_ids: Optional[torch.Te
     a.expert_offset = _int32(expert_offset, "expert_offset")
     a.in_features, a.out_features = _int32(K, "in_features"), _int32(N, "out_features")
     _call(_lib.moe_ep_expert_linear, dev, a)
+    _written(given)
     return out
 
 
@@ -419,7 +429,7 @@ def moe_layer(hidden: torch.Tensor, gate_up: Weight, down: Weight, topk_ids: Opt
             if w.dtype != torch.float32 or tuple(w.shape) != (n, top_k) or not w.is_contiguous():
                 raise ValueError(f"topk_weights must be a contiguous float32 [{n}, {top_k}]")
             a.topk_weights = _on(w, dev, "topk_weights")
-    out = _output(out, (n, H), dtype, out_dtype, hidden)
+    given, out = out, _output(out, (n, H), dtype, out_dtype, hidden)
     a.hidden, a.hidden_stride = _rows(hidden, dev, "hidden")
     a.out, a.out_stride = _rows(out, dev, "out")
     a.dtype, a.out_dtype = _DTYPES[dtype], _DTYPES[out.dtype]
@@ -435,6 +445,7 @@ def moe_layer(hidden: torch.Tensor, gate_up: Weight, down: Weight, topk_ids: Opt
         nbytes = workspace.numel()
     a.workspace, a.workspace_bytes = _on(workspace, dev, "workspace"), nbytes
     _call(_lib.moe_ep_layer, dev, a)
+    _written(given)
     return out
 
 
