@@ -152,7 +152,7 @@ class moe_ep_gated_grad_args(Structure):
         ("gate_up", c_void_p), ("gate_up_stride", c_int64), ("pre", c_void_p), ("dx", c_void_p),
         ("dx_stride", c_int64), ("dgate_up", c_void_p), ("dgate_up_stride", c_int64), ("workspace", c_void_p),
         ("workspace_bytes", c_size_t), ("dtype", c_int32), ("dout_dtype", c_int32), ("num_rows", c_int32),
-        ("hidden_size", c_int32), ("intermediate_size", c_int32),
+        ("hidden_size", c_int32), ("intermediate_size", c_int32), ("d_parts", c_int32),
     ]
 
 

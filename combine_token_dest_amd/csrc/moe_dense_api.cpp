@@ -82,9 +82,10 @@ MatK operand(const void* p, int64_t stride, int32_t rows, int64_t side) {
   return m;
 }
 
-// Workspace of the gated product's gradients: [d][tops][factor][partial sums].
+// Workspace of the gated product's gradients: [d][rest of d, with two
+// parts][tops][factor][partial sums].
 struct GradSpace {
-  int64_t d_stride, tops, factor, partial, total;
+  int64_t d_stride, rest, tops, factor, partial, total;
 };
 
 int make_space(const moe_ep_gated_grad_args* a, GradSpace* s) {
@@ -94,8 +95,11 @@ int make_space(const moe_ep_gated_grad_args* a, GradSpace* s) {
   int st = check_side("hidden_size", a->hidden_size, kMinRow);
   if (st == MOE_EP_OK) st = check_side("intermediate_size", a->intermediate_size, kMinRow);
   if (st != MOE_EP_OK) return st;
+  if (a->d_parts < 0 || a->d_parts > 2)
+    return report(MOE_EP_ERR_INVALID_ARG, "d_parts %d is not 0, 1 or 2", a->d_parts);
   s->d_stride = up(2 * (int64_t)a->intermediate_size, 8);
-  s->tops = up(a->num_rows * s->d_stride * 2, 256);
+  s->rest = up(a->num_rows * s->d_stride * 2, 256);
+  s->tops = a->d_parts == 2 ? 2 * s->rest : s->rest;
   s->factor = s->tops + (a->dtype == MOE_EP_F16 ? kTops * 4 : 0);
   s->partial = s->factor + 256;
   s->total = s->partial + kPartialFloats * 4;
@@ -277,14 +281,17 @@ int moe_ep_gated_grad(const moe_ep_gated_grad_args* a, void* stream) {
   hipStream_t hs = static_cast<hipStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(a->workspace);
   uint16_t* d = reinterpret_cast<uint16_t*>(ws);
+  uint16_t* rest = a->d_parts == 2 && n > 0 ? reinterpret_cast<uint16_t*>(ws + s.rest) : nullptr;
   hipError_t e = hipSuccess;
   ProductKArgs k = {};
   k.partial = reinterpret_cast<float*>(ws + s.partial);
+  k.q_rest = rest ? rest - d : 0;
   if (n > 0) {
     GatedGradKArgs g = {};
     g.dout = a->dout;
     g.pre = a->pre;
     g.d = d;
+    g.rest = rest;
     g.dout_stride = a->dout_stride;
     g.d_stride = s.d_stride;
     g.dout_f32 = a->dout_dtype == MOE_EP_F32;

@@ -48,7 +48,7 @@ struct GatedKArgs {
   int32_t ptiles, qtiles;     // (set by the launcher)
 };
 
-// out[q][p] = *factor * sum over k
+// out[q][p] = *factor * sum over k of (q + q_rest) p
 struct ProductKArgs {
   MatK p, q;
   int32_t k;
@@ -56,6 +56,9 @@ struct ProductKArgs {
   uint16_t* out;
   int64_t out_stride;
   const float* factor;        // or NULL: 1
+  // Elements from q to what q lacks (float16: times kRestUpF16), which lies as
+  // q does; or 0.
+  int64_t q_rest;
   float* partial;             // kPartialFloats: sums over parts of k, where there are few results
   int32_t ptiles, qtiles;     // (set by the launcher)
   int32_t parts;              // (set by the launcher)
@@ -67,6 +70,7 @@ struct GatedGradKArgs {
   const void* dout;           // [n, inter]
   const float* pre;           // [n, 2 * inter]
   uint16_t* d;                // [n, d_stride], columns from 2 * inter on are not written
+  uint16_t* rest;             // or NULL: what d's rounding leaves (float16: times kRestUpF16), as d lies
   int64_t dout_stride, d_stride;
   int32_t dout_f32;
   int32_t n, inter;
@@ -74,6 +78,9 @@ struct GatedGradKArgs {
   float* factor;              // float16: what the products are multiplied with
 };
 constexpr int kTops = 1024;
+// float16 keeps what a rounding leaves (2^-11 of the number at most) times
+// 2^11, so that its smallest values are not lost.
+constexpr float kRestUpF16 = 2048.0f;
 
 struct AdapterKArgs {
   MatK w, x;

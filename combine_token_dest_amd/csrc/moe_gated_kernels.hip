@@ -11,9 +11,13 @@
 // g and u are kept as float32: rounded to bfloat16 they would add as much to
 // the gradients' error as their own rounding does (8192 rows of 7168 x 2048,
 // off by 0.0030 of the norm where float32 leaves 0.0024), for 2% of the time.
-// d is rounded once to the inputs' type, which the matrix instructions take:
-// half a step of an element beside the same half step that dx and dW are
-// rounded by.  float16 would lose what is small and turn what is large into
+// d goes into the products in the inputs' type, which the matrix instructions
+// take.  Rounded once it adds half a step of an element to the same half step
+// that dx and dW are rounded by (8192 rows of 7168 x 2048: off by 0.0023 of the
+// norm, where a float32 d leaves 0.0017; float16 0.00029 and 0.00021).  With the
+// rest of each rounding as a second part, whose products are added first, that
+// part of the error is gone, for twice the products (forward and backward 1297 -> 2110 us).
+// float16 would lose what is small and turn what is large into
 // infinities, so there d is multiplied with a power of two that puts its
 // largest element at 2^14 .. 2^15, and the products with its inverse.
 
@@ -116,7 +120,8 @@ __global__ void __launch_bounds__(WAVES * 64) gated_few_kernel(GatedKArgs a) {
 
 // PARTS: a workgroup of a few results' tiles takes one of a.parts parts of k
 // (blockIdx.y, in whole tiles of k) and leaves float32 sums for sum_kernel.
-template <class G, bool PARTS>
+// REST: q's second part is gone through first, with the same p.
+template <class G, bool PARTS, bool REST>
 __global__ void __launch_bounds__(G::kThreads, G::kThreads / 256) product_kernel(ProductKArgs a) {
   typedef typename G::T T;
   __shared__ __attribute__((aligned(1024))) char lds[G::kLds];
@@ -134,10 +139,29 @@ __global__ void __launch_bounds__(G::kThreads, G::kThreads / 256) product_kernel
     sq.skip(first);
     k = min(a.k, last * G::kK) - first * G::kK;
   }
-  G::begin((MOE_EP_LDS char*)lds, sp, sq, k);
   typename G::Acc acc;
-  G::clear(acc);
-  G::loop((MOE_EP_LDS char*)lds, sp, sq, k, acc);
+  if constexpr (REST) {
+    G::clear(acc);
+    sq.move(a.q_rest);
+    auto back = [&](int count) {
+      sp.skip(-count);
+      sq.skip(-count);
+      sq.move(-a.q_rest);
+    };
+    auto between = [&]() {
+      if constexpr (std::is_same<T, F16>::value) {
+#pragma unroll
+        for (int i = 0; i < G::FP; ++i)
+#pragma unroll
+          for (int j = 0; j < G::FQ; ++j) acc[i][j] *= 1.0f / kRestUpF16;
+      }
+    };
+    G::loop_twice((MOE_EP_LDS char*)lds, sp, sq, k, acc, back, between);
+  } else {
+    G::begin((MOE_EP_LDS char*)lds, sp, sq, k);
+    G::clear(acc);
+    G::loop((MOE_EP_LDS char*)lds, sp, sq, k, acc);
+  }
   if (!G::join((MOE_EP_LDS char*)lds, acc)) return;
   const float factor = !PARTS && a.factor ? *a.factor : 1.0f;
   const int lane = threadIdx.x & 63;
@@ -222,6 +246,17 @@ __device__ __forceinline__ void write8(uint16_t* p, int have, const float (&v)[8
   }
 }
 
+// What rounding to T leaves of each number (nothing of one that it makes
+// infinite), in the scale that T keeps it in.
+template <class T>
+__device__ __forceinline__ void rests(float (&v)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float near = T::to_float(T::from_float(v[e])), rest = v[e] - near;
+    v[e] = __builtin_isfinite(near) ? rest * (std::is_same<T, F16>::value ? kRestUpF16 : 1.0f) : 0.0f;
+  }
+}
+
 // Eight columns of dgate and dup.
 template <class T>
 __device__ __forceinline__ void gate_grads(const GatedGradKArgs& a, int64_t row, int c, float (&dg)[8], float (&du)[8]) {
@@ -300,6 +335,13 @@ __global__ void __launch_bounds__(256) gated_grad_kernel(GatedGradKArgs a, int t
     uint16_t* d = a.d + row * a.d_stride + c;
     write8<T>(d, a.inter - c, dg);
     write8<T>(d + a.inter, a.inter - c, du);
+    if (a.rest) {
+      uint16_t* r = a.rest + row * a.d_stride + c;
+      rests<T>(dg);
+      rests<T>(du);
+      write8<T>(r, a.inter - c, dg);
+      write8<T>(r + a.inter, a.inter - c, du);
+    }
   }
 }
 
@@ -356,20 +398,23 @@ hipError_t product_tiles(ProductKArgs a, hipStream_t stream) {
     const int64_t results = (int64_t)a.p.rows * a.q_rows;
     a.parts = (int)std::min<int64_t>({8, 256 / count, a.k / (2 * G::kK), kPartialFloats / results});
     if (a.parts > 1) {
-      product_kernel<G, true><<<dim3(count, a.parts), dim3(G::kThreads), 0, stream>>>(a);
+      const dim3 grid(count, a.parts), block(G::kThreads);
+      if (a.q_rest) product_kernel<G, true, true><<<grid, block, 0, stream>>>(a);
+      else product_kernel<G, true, false><<<grid, block, 0, stream>>>(a);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
       sum_kernel<typename G::T><<<dim3((int)std::min<int64_t>((results + 255) / 256, 2048)), dim3(256), 0, stream>>>(a);
       return hipGetLastError();
     }
   }
-  product_kernel<G, false><<<dim3(count), dim3(G::kThreads), 0, stream>>>(a);
+  if (a.q_rest) product_kernel<G, false, true><<<dim3(count), dim3(G::kThreads), 0, stream>>>(a);
+  else product_kernel<G, false, false><<<dim3(count), dim3(G::kThreads), 0, stream>>>(a);
   return hipGetLastError();
 }
 template <class T, bool QKC>
 hipError_t product(const ProductKArgs& a, hipStream_t stream) {
   const bool direct = a.p.whole && a.q.whole;
-  switch (tile_size(a.p.rows, a.q_rows, a.k, direct, false)) {
+  switch (tile_size(a.p.rows, a.q_rows, a.q_rest ? 2 * (int64_t)a.k : a.k, direct, false)) {
     case k256x256: return product_tiles<Gemm<T, false, QKC, false, 256, 256, 2, 4, 1, true>>(a, stream);
     case k256x128: return product_tiles<Gemm<T, false, QKC, false, 256, 128, 2, 4, 1, true>>(a, stream);
     case k128x128:

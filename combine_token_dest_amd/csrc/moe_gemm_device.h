@@ -151,7 +151,17 @@ struct Side {
     }
   }
 
-  // Past the first `count` tiles of k.
+  // By so many elements.
+  __device__ __forceinline__ void move(int64_t elements) {
+    if constexpr (DIRECT) {
+      base += elements * 2;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) src[i] += elements * 2;
+    }
+  }
+
+  // Past the next `count` tiles of k (below 0: back over the last).
   __device__ __forceinline__ void skip(int count) {
     if constexpr (DIRECT) {
       base += count * step;
@@ -315,13 +325,13 @@ struct Gemm {
   // One tile of k at `cur`, its first 32 k already in the fragments; leaves
   // the first of the tile at `nxt` there.  `left`: of k from the tile after
   // that one on, which goes to `dst`: cur's place, when all waves have read
-  // it (through registers, it was fetched a step ago, and the one behind it is
-  // now).  Places of their own for the compiler, which would wait for the
+  // it (through registers, it was fetched a step ago, and the one behind it,
+  // with `behind`, is now).  Places of their own for the compiler, which would wait for the
   // loads to LDS before each read otherwise; what orders them is meet().
   static __device__ __forceinline__ void step(const MOE_EP_LDS char* __restrict__ cur,
                                               const MOE_EP_LDS char* __restrict__ nxt, MOE_EP_LDS char* __restrict__ dst,
                                               SideP& sp, SideQ& sq, FragsP& p, FragsQ& q, Acc& acc, Held& held,
-                                              int left) {
+                                              int left, int behind) {
     frags(cur, p, q, 1);
     products(p, q, 0, acc);
     if constexpr (DIRECT) {
@@ -333,7 +343,7 @@ struct Gemm {
       if (left > 0) {
         SideP::put(dst, held.p);
         SideQ::put(dst + SideP::kBytes, held.q);
-        fetch(held, sp, sq, left - kK);
+        fetch(held, sp, sq, behind);
       }
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -371,7 +381,41 @@ struct Gemm {
 #pragma unroll 1
     for (int left = K; left > 0; left -= kK) {
       // (past the last tile nxt is read for nothing, inside lds)
-      step(lds + cur, lds + (kBuffer - cur), lds + cur, sp, sq, p, q, acc, held, left - 2 * kK);
+      step(lds + cur, lds + (kBuffer - cur), lds + cur, sp, sq, p, q, acc, held, left - 2 * kK,
+           left - 3 * kK);
+      cur = kBuffer - cur;
+    }
+  }
+  // begin() and loop() over the same K (at least 1) twice: back(count) is called
+  // when the last of the first time's `count` tiles has been sent for, between()
+  // when its products are made.
+  template <class Back, class Between>
+  static __device__ __forceinline__ void loop_twice(MOE_EP_LDS char* lds, SideP& sp, SideQ& sq, int K, Acc& acc,
+                                                    const Back& back, const Between& between) {
+    const int count = (K + kK - 1) / kK;
+    auto left = [&](int t) { return t < 2 * count ? K - (t < count ? t : t - count) * kK : 0; };
+    auto sent = [&](int t) {
+      if (t == count - 1) back(count);
+    };
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      if (DIRECT && left(b) >= kK) load(lds + b * kBuffer, sp, sq);
+      else fill(lds + b * kBuffer, sp, sq, left(b));
+      sent(b);
+    }
+    Held held;
+    fetch(held, sp, sq, left(2));
+    if (!DIRECT) sent(2);
+    meet();
+    FragsP p;
+    FragsQ q;
+    frags(lds, p, q, 0);
+    int cur = 0;
+#pragma unroll 1
+    for (int t = 0; t < 2 * count; ++t) {
+      step(lds + cur, lds + (kBuffer - cur), lds + cur, sp, sq, p, q, acc, held, left(t + 2), left(t + 3));
+      sent(t + (DIRECT ? 2 : 3));
+      if (t == count - 1) between();
       cur = kBuffer - cur;
     }
   }

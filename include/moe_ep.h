@@ -575,20 +575,24 @@ typedef struct moe_ep_gated_grad_args {
   int32_t num_rows;
   int32_t hidden_size;            /* 8..2^22 */
   int32_t intermediate_size;      /* 8..2^22 */
+  int32_t d_parts;                /* numbers of dtype that each of dg and du goes into the products as: 1 (or 0), 2 */
 } moe_ep_gated_grad_args;
 
 /* Bytes of device workspace moe_ep_gated_grad needs for these sizes (the
- * sizes and dtype are read; pointers are not followed): 4 for each element
- * of dout, and 8 MiB. */
+ * sizes, dtype and d_parts are read; pointers are not followed): 4 for each
+ * element of dout (8 with two parts), and 8 MiB. */
 MOE_EP_API int moe_ep_gated_grad_workspace_bytes(const moe_ep_gated_grad_args* args, size_t* out_bytes);
 
 /* The gradients of moe_ep_gated's inputs:
  *   dg = dout * u * s * (1 + g * (1 - s)), s = 1 / (1 + exp(-g));  du = dout * g * s
  *   dx = dg gate_up[:I] + du gate_up[I:],  dgate_up = [dg^T x; du^T x]
  * each written whole, not added to (without rows dgate_up is zeros).  dg and
- * du are rounded once to dtype, float16 ones after a multiplication with a
- * power of two that brings the largest finite one to 2^14..2^15, so that none
- * overflows.  x is read for dgate_up only and gate_up for dx only; the other
+ * du are made in float32.  With one part they are rounded once to dtype before
+ * the products, which adds to the results' error about as much as their own
+ * rounding does; with two they go in as the rounding and the rounding of what it
+ * leaves, 16 bits for bfloat16 and 22 for float16, and the products take twice
+ * as long.  float16 ones are multiplied with a power of two that brings the
+ * largest finite one to 2^14..2^15 first, so that none overflows.  x is read for dgate_up only and gate_up for dx only; the other
  * may be NULL.  One kernel launch (float16: two) and one or two for each
  * gradient.  Outputs must not overlap inputs or one another.  The workspace
  * holds nothing between calls; calls that may overlap in time need one each. */

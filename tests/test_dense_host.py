@@ -277,3 +277,21 @@ def test_gated_gradient_formula_against_differences():
             slope = (at(t + step) - at(t - step)) / 2e-5
             # the third derivative times step^2 / 6, and float64's cancellation
             assert abs(slope - float(d.reshape(-1)[i])) <= 1e-7 * (1 + abs(slope))
+
+
+def test_gated_grad_parts():
+    """Of what d is kept in: 0 and 1 are one; two take as much workspace again."""
+    def size(**kw):
+        return _lib.moe_ep_gated_grad_workspace_bytes(grad_args(num_rows=100, **kw))
+    assert size() == size(d_parts=1) and size(d_parts=2) - size() >= 100 * 64 * 2
+    for bad in (-1, 3):
+        assert grad(d_parts=bad) == INVALID
+        assert status(_lib.moe_ep_gated_grad_workspace_bytes, grad_args(d_parts=bad)) == INVALID
+    assert grad(num_rows=100, d_parts=2, workspace_bytes=size()) == INVALID
+    assert grad(num_rows=0, d_parts=2, dgate_up=None, workspace=None, dout=None, pre=None, dx=None) == OK
+
+
+@pytest.mark.parametrize("parts", [0, 3, None])
+def test_gated_refuses_other_parts(parts):
+    with pytest.raises(ValueError, match="grad_parts"):
+        gated_linear(bf16(2, 64), bf16(16, 64), grad_parts=parts)
