@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include "moe_ep.h"
+#include "moe_tile_rule.h"
 
 namespace moe_ep_detail {
 
@@ -63,7 +64,6 @@ struct ProductKArgs {
   int32_t ptiles, qtiles;     // (set by the launcher)
   int32_t parts;              // (set by the launcher)
 };
-constexpr int64_t kPartialFloats = 512 * 64 * 64;
 
 // d = [dgate, dup] of a gated product, times a power of two for float16.
 struct GatedGradKArgs {

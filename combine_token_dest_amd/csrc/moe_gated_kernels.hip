@@ -363,14 +363,8 @@ template <class T>
 hipError_t gated(const GatedKArgs& a, hipStream_t stream) {
   if (a.x.rows <= 16) return gated_few<T, 1>(a, stream);
   if (a.x.rows <= 32) return gated_few<T, 2>(a, stream);
-  // Up to 64 rows the weights' stream still wins, while its workgroups, each
-  // reading all of x, go through the card twice at most (48 rows, us, this and
-  // tiles: 7168 x 2048 14.6 and 21.6, 4096 x 1024 8.9 and 12.4, 2048 x 5632 17.2
-  // and 12.7).
-  if (tiles(a.inter, 8) <= 512) {
-    if (a.x.rows <= 48) return gated_few<T, 3>(a, stream);
-    if (a.x.rows <= 64) return gated_few<T, 4>(a, stream);
-  }
+  if (a.x.rows <= gated_few_rows(a.inter))
+    return a.x.rows <= 48 ? gated_few<T, 3>(a, stream) : gated_few<T, 4>(a, stream);
   const bool direct = a.w.whole && a.x.whole;
   switch (tile_size(2 * (int64_t)a.inter, a.x.rows, a.hidden, direct, true)) {
     case k256x256: return gated_tiles<Gemm<T, true, true, true, 256, 256, 2, 4, 1, true>>(a, stream);
@@ -393,10 +387,9 @@ hipError_t product_tiles(ProductKArgs a, hipStream_t stream) {
   a.qtiles = tiles(a.q_rows, G::TQ);
   const int count = a.ptiles * a.qtiles;
   if constexpr (G::TP == 64) {
-    // A few results of many k (weights' gradients of small layers, a few rows'
-    // gradients): parts of k, two tiles of it at least, for all CUs.
+    static_assert(G::TQ == 64 && G::kK == 256, "product_parts()");
     const int64_t results = (int64_t)a.p.rows * a.q_rows;
-    a.parts = (int)std::min<int64_t>({8, 256 / count, a.k / (2 * G::kK), kPartialFloats / results});
+    a.parts = product_parts(a.p.rows, a.q_rows, a.k);
     if (a.parts > 1) {
       const dim3 grid(count, a.parts), block(G::kThreads);
       if (a.q_rest) product_kernel<G, true, true><<<grid, block, 0, stream>>>(a);
