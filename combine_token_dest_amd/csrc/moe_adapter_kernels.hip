@@ -110,7 +110,14 @@ __device__ __forceinline__ bool all_finite(const u32x4& v) {
 
 constexpr int kLowWaves = 8;
 // Calls of up to this many rows, which may be one request's each, take them
-// one by one; more are prompts, whose rows share adapters.
+// one by one; more are prompts, whose rows share adapters.  (The host does not
+// see the ids.)  Calls of 2048 columns, us, row by row and 8 rows at a time:
+//                        an adapter a row           four prompts
+//   k, rank     rows  128      512      1024     128      512      1024
+//   2048, 16        18 28    25 35    49 56     18 18    19 18    33 29
+//   7168, 16        34 61    52 73    98 115    30 30    44 41    79 68
+//   4096, 64        36 48    70 72   130 147    27 22    44 33    77 54
+//   7168, 128       72 82   172 190  343 352    49 35    96 60   172 95
 constexpr int kLowSingle = 512;
 
 // One pass of low_kernel: M adapters' rows of A with the workgroup's rows of x.
