@@ -517,8 +517,9 @@ typedef struct moe_ep_norm_args {
  *   scales       = max|y| / 448 over a group of columns (the last may be short)
  *   out          = y / scale, rounded to e4m3, ties to even
  * y is made from the float32 sum, not from its rounding, and m is summed in
- * float64, so no square overflows.  The quotient y / scale is made without the
- * roundings of both.  A group whose scale is 0 holds zeros.  An
+ * float64, so no square overflows.  The 8-bit values are the nearest ones to
+ * 448 s w / max|s w| of the group, without the roundings of y and scale (groups
+ * with a scale below 2^-64 apart).  A group whose scale is 0 holds zeros.  An
  * infinity or NaN in a row makes NaN of the row's y that it reaches by the
  * formula, and a group with NaN has the scale NaN and NaN throughout.
  *
