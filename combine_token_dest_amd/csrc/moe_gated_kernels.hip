@@ -6,7 +6,7 @@
 // (moe_gemm_device.h); for a backward pass it also writes both as they are.
 // Backward, from these: d = [dh u silu'(g), dh silu(g)] by a pass over the
 // elements, then dx = d W and dW = d^T x as two products.  8192 rows of 7168 x
-// 2048: 390 us forward (1.23 PFLOP/s), then 38 + 459 + 435.
+// 2048: 397 us forward (1.21 PFLOP/s), then 38 + 457 + 442.
 //
 // g and u are kept as float32: rounded to bfloat16 they would add as much to
 // the gradients' error as their own rounding does (8192 rows of 7168 x 2048,

@@ -15,9 +15,11 @@
 //
 // A large product is bound by the card's power: 8192 x 4096 x 7168 takes 300 us
 // on zeros and 380 to 400 on random numbers (1.20 to 1.26 PFLOP/s; a training
-// step's products with rows side by side 450 and 430).  The same tiles in
-// v_mfma_f32_32x32x16 take 13% more.  A swizzle that leaves no bank conflict
-// (they are 14 to 22% of the time where rows lie side by side) changes nothing.
+// step's products with rows side by side 457 and 442).  The same tiles in
+// v_mfma_f32_32x32x16 take 13% more.  Bank conflicts are 14 to 22% of the cycles
+// where rows lie side by side, and 12 to 22% where a row of LDS has 128 k and
+// more, which are spread over 8 units only; layouts without any take the same
+// time in both (8192 rows, and 1024 rows of 7168 x 2048 at one tile a CU).
 //
 // LDS layout, in 16-byte units of 8 elements.  KC: a row of kK k, unit u of
 // row r at u ^ (r & 7), so that the 8 lanes that read side by side meet all

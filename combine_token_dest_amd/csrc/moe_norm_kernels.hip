@@ -483,8 +483,8 @@ __global__ void __launch_bounds__(1024, VPT <= 2 ? 8 : 4) norm_kernel(NormKArgs 
 template <class T, class W, Rows ROWS>
 hipError_t launch(const NormKArgs& all, hipStream_t stream) {
   // Two vectors of a row to a thread where there are rows enough to hide each
-  // other's latency (4096 rows of 7168 to 8 bits: 56 us with one, 47 with two,
-  // 51 with four; 8192 of 4096 in 16 bits: 49, 51 and 54); one for few rows,
+  // other's latency (calls of 4096 rows of 7168 to 8 bits: 56 us with one, 47 with
+  // two, 51 with four; 8192 of 4096 in 16 bits: 49, 51 and 54); one for few rows,
   // and four, or none held, where a workgroup has no more threads.
   const int vectors = (all.hidden + 7) / 8;
   int vpt = all.n >= 512 ? 2 : 1;
