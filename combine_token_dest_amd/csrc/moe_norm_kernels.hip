@@ -14,8 +14,9 @@
 // infinity there, so it is not lost, as it would be in a float maximum.
 //
 // The 8-bit values are the nearest ones to 448 s w / max|s w|.  float32 tells for
-// all but one in 2^17; those are settled by float64 products, which are whole.
-// A value on the wrong side of a middle is off by a sixteenth of itself, and
+// all but one in 2^16 (with 16-bit weights, whose quotients often lie in a
+// middle itself, one in 2^13); those are settled by float64 products, which are
+// whole.  A value on the wrong side of a middle is off by a sixteenth of itself, and
 // some few of a million were (of 8 million with float32 weights 21): 1 to 2 us
 // of the 44 above with a scale a group, and of 42 with a scale a row.
 
@@ -112,7 +113,7 @@ __device__ __forceinline__ void store_e4m3(uint8_t* p, int have, const u32x2& w)
 // m top / 448.  Each v and top is off by one rounding; with those of the
 // quotient that is at most 5 x 2^-24 of it, so where 2^-21 more and less round to
 // the same value, that is the quotient's, whatever the roundings were.
-// Elsewhere (one value of 2^17) the two differ, for settle().  A scale near
+// Elsewhere the two differ, for settle().  A scale near
 // float32's end may be rounded by any share, so there it is what is divided by,
 // brought up by 2^100 as v is, and the quotient needs an end.
 __device__ __forceinline__ void quotients(const float (&v)[8], float top, float scale, float m, u32x2* more, u32x2* less) {
